@@ -1,6 +1,6 @@
 /*
- * moe.h -- C ABI of the MI355X (gfx950) sparse Mixture-of-Experts FFN layer
- * forward.
+ * moe.h -- C ABI of the MI355X (gfx950) sparse Mixture-of-Experts FFN layer:
+ * forward, gradient, and what a training step needs around them.
  *
  * The layer (sources are the pages' titles and sections):
  *   1. router logits  l[t,e] = x[t,:] . Wr[e,:] + add[e] - b[e], softmax
@@ -69,8 +69,9 @@
  *     check returns a negative moe_status and enqueues nothing.  A failed
  *     kernel launch returns MOE_ERR_HIP.  T == 0 is valid: once the
  *     descriptor passes its checks the call returns MOE_OK, enqueues
- *     nothing and does not look at the pointers.  Non-finite inputs are not
- *     checked.
+ *     nothing and does not look at the pointers (but see moe_router_grad
+ *     and moe_backward, which then zero weight gradients).  Non-finite
+ *     inputs are not checked.
  *   - Calls on distinct streams with distinct workspaces may run
  *     concurrently.
  *   - The residual is not applied: a token whose every assignment
@@ -341,6 +342,117 @@ int moe_forward_noalloc(const moe_desc *desc, const void *x,
  * fp32 add.  Apply after a forward; it affects the next call. */
 int moe_bias_update(int32_t E, const int32_t *counts, float target,
                     float gamma, float *expert_bias, void *stream);
+
+/* ------------------------------------------------------------------
+ * Training.  Rows of an "expert-sorted" tensor are laid out as the expert
+ * outputs of moe_grouped_ffn: R routed rows (T*k, or E*C for expert
+ * choice) in the order of slot_token, then, with a shared expert, one row
+ * per token (row R + t).  Routed rows at and beyond offsets[E] (capacity
+ * drops) belong to no token: they are neither read nor written.  A row
+ * tensor may be NULL when it has no rows.  Everything here is written
+ * without atomics: the same inputs give the same bits.
+ * ------------------------------------------------------------------ */
+
+/* Tokens into expert-sorted rows: xs[slot_of[t,j]] = x[t] for every kept
+ * assignment, and xs[R + t] = x[t] with a shared expert.  Needs r->slot_of;
+ * x [T][d], xs [R + n_shared*T][d], dtype. */
+int moe_dispatch_rows(const moe_desc *desc, const moe_routing *r,
+                      const void *x, void *xs, void *stream);
+
+/* Gradient of moe_dispatch_rows: dx[t] = sum over kept j of
+ * dxs[slot_of[t,j]], plus dxs[R + t] with a shared expert; summed in that
+ * order in fp32, rounded once. */
+int moe_dispatch_rows_grad(const moe_desc *desc, const moe_routing *r,
+                           const void *dxs, void *dx, void *stream);
+
+/* Expert-sorted rows back into token order with the routing weights
+ * applied: y[t] = sum over kept j of topk_w[t,j] * ys[slot_of[t,j]], plus
+ * ys[R + t] with a shared expert (moe_combine, of the caller's own rows).
+ * Needs r->slot_of and r->topk_w. */
+int moe_combine_rows(const moe_desc *desc, const moe_routing *r,
+                     const void *ys, void *y, void *stream);
+
+/* Gradient of moe_combine_rows, for dy [T][d]:
+ *   dys[slot_of[t,j]] = topk_w[t,j] * dy[t],   dys[R + t] = dy[t],
+ *   dw[t,j] = <dy[t], ys[slot_of[t,j]]>, 0 for a dropped assignment.
+ * dw is [T][k] fp32; dys may be ys (in place). */
+int moe_combine_rows_grad(const moe_desc *desc, const moe_routing *r,
+                          const void *dy, const void *ys, void *dys,
+                          float *dw, void *stream);
+
+/* Gradients of a layer: caller-owned device buffers, each of its weight's
+ * shape and type (b_router fp32; x [T][d]), written whole, not added to.
+ * NULL = not wanted.  There is no gradient of expert_bias (balancing state,
+ * stepped by moe_bias_update).  Groups without rows get zeros. */
+typedef struct moe_grads {
+    void *x;
+    void *w_router;
+    float *b_router;
+    void *w1, *b1, *w2, *b2;
+    void *ws1, *bs1, *ws2, *bs2;
+    void *w3, *b3, *ws3, *bs3;
+} moe_grads;
+
+/* Host.  Bytes of workspace of moe_router_grad and moe_backward, functions
+ * of the descriptor alone (0 if it is invalid, and for moe_backward if
+ * expert_fp8: FP8 experts have no gradient).  The workspace holds nothing
+ * between calls; it is not the forward's. */
+size_t moe_router_grad_workspace_size(const moe_desc *desc);
+size_t moe_grad_workspace_size(const moe_desc *desc);
+
+/* Gradient of the router: of
+ *   sum dw * topk_w + aux_scale * l_aux + z_scale * z-loss
+ * (monitor[0]), with dw [T][k] fp32 the gradient of the routing weights (as
+ * moe_combine_rows_grad leaves it) and the selection and the counts behind
+ * f constant.  Top-k: through the renormalised weights; expert choice:
+ * through the probabilities.  Reads x, w->w_router, b_router, expert_bias
+ * (logits, where the losses need them) and of r topk_idx, topk_w, slot_of
+ * and, for aux_scale != 0, f.  Writes g->x = dx_add + the router's part
+ * (dx_add [T][d] dtype, NULL = 0, may be g->x), g->w_router, g->b_router.
+ * T == 0: the weights' gradients are zeroed. */
+int moe_router_grad(const moe_desc *desc, const void *x,
+                    const moe_weights *w, const moe_routing *r,
+                    const float *dw, const void *dx_add, float aux_scale,
+                    float z_scale, const moe_grads *g, void *ws,
+                    size_t ws_bytes, void *stream);
+
+/* Gradient of the whole layer (moe_forward) for dy [T][d]: of
+ *   sum dy * y + aux_scale * l_aux + z_scale * z-loss,
+ * through the experts, the shared expert, the combine and the router.  x, w
+ * and r are the forward's (r needs topk_idx, topk_w, offsets, slot_of and,
+ * for aux_scale != 0, f); nothing else of the forward is kept: hidden
+ * activations are computed again.  Matrix products accumulate in fp32; the
+ * hidden activations and their gradients are rounded to dtype between two
+ * products.  Refuses expert_fp8 (MOE_ERR_UNSUPPORTED).  T == 0: the
+ * weights' gradients are zeroed. */
+int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
+                 const moe_routing *r, const void *dy, float aux_scale,
+                 float z_scale, const moe_grads *g, void *ws,
+                 size_t ws_bytes, void *stream);
+
+/* One tensor of a clipping call: numel elements of dtype (a moe_dtype) at
+ * src, aligned to their size; the result goes to dst (src for in place,
+ * else not overlapping any other tensor; NULL = only counted). */
+typedef struct moe_tensor {
+    const void *src;
+    void *dst;
+    int64_t numel;
+    int32_t dtype;
+} moe_tensor;
+
+/* Host.  Bytes of workspace moe_clip_grads needs for n tensors. */
+size_t moe_clip_workspace_size(int32_t n);
+
+/* Global gradient norm over n tensors and clipping:
+ *   *norm = sqrt(sum over all tensors of src^2)      (device, fp32)
+ *   dst = src * min(1, max_norm / (norm + 1e-6)),
+ * rounded once to the tensor's type.  `tensors` is a HOST array, read during
+ * the call; max_norm is finite and >= 0.  Squares are summed in double.  A
+ * norm that is not a number reaches every dst; an infinite one gives zeros
+ * (and not-a-number where src is infinite).  Tensors of any mix of sizes
+ * and types, n == 0 included (norm 0). */
+int moe_clip_grads(int32_t n, const moe_tensor *tensors, float max_norm,
+                   float *norm, void *ws, size_t ws_bytes, void *stream);
 
 /* Host.  Static English text of a moe_status value. */
 const char *moe_status_string(int status);

@@ -57,6 +57,18 @@ class MoeRouting(ctypes.Structure):
                 ("l_aux", c_vp), ("monitor", c_vp)]
 
 
+class MoeGrads(ctypes.Structure):
+    _fields_ = [("x", c_vp), ("w_router", c_vp), ("b_router", c_vp),
+                ("w1", c_vp), ("b1", c_vp), ("w2", c_vp), ("b2", c_vp),
+                ("ws1", c_vp), ("bs1", c_vp), ("ws2", c_vp), ("bs2", c_vp),
+                ("w3", c_vp), ("b3", c_vp), ("ws3", c_vp), ("bs3", c_vp)]
+
+
+class MoeTensor(ctypes.Structure):
+    _fields_ = [("src", c_vp), ("dst", c_vp), ("numel", ctypes.c_int64),
+                ("dtype", c_i32)]
+
+
 # (name, restype, argtypes) of every entry point of include/moe.h
 SIGNATURES = {
     "moe_capacity": (c_i32, [c_i32, c_i32, ctypes.c_double]),
@@ -100,6 +112,37 @@ SIGNATURES = {
                                            c_vp]),
     "moe_bias_update": (ctypes.c_int, [c_i32, c_vp, ctypes.c_float,
                                        ctypes.c_float, c_vp, c_vp]),
+    "moe_dispatch_rows": (ctypes.c_int, [ctypes.POINTER(MoeDesc),
+                                         ctypes.POINTER(MoeRouting), c_vp,
+                                         c_vp, c_vp]),
+    "moe_dispatch_rows_grad": (ctypes.c_int, [ctypes.POINTER(MoeDesc),
+                                              ctypes.POINTER(MoeRouting),
+                                              c_vp, c_vp, c_vp]),
+    "moe_combine_rows": (ctypes.c_int, [ctypes.POINTER(MoeDesc),
+                                        ctypes.POINTER(MoeRouting), c_vp,
+                                        c_vp, c_vp]),
+    "moe_combine_rows_grad": (ctypes.c_int, [ctypes.POINTER(MoeDesc),
+                                             ctypes.POINTER(MoeRouting),
+                                             c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "moe_router_grad_workspace_size": (ctypes.c_size_t,
+                                       [ctypes.POINTER(MoeDesc)]),
+    "moe_grad_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(MoeDesc)]),
+    "moe_router_grad": (ctypes.c_int, [ctypes.POINTER(MoeDesc), c_vp,
+                                       ctypes.POINTER(MoeWeights),
+                                       ctypes.POINTER(MoeRouting), c_vp,
+                                       c_vp, ctypes.c_float, ctypes.c_float,
+                                       ctypes.POINTER(MoeGrads), c_vp,
+                                       ctypes.c_size_t, c_vp]),
+    "moe_backward": (ctypes.c_int, [ctypes.POINTER(MoeDesc), c_vp,
+                                    ctypes.POINTER(MoeWeights),
+                                    ctypes.POINTER(MoeRouting), c_vp,
+                                    ctypes.c_float, ctypes.c_float,
+                                    ctypes.POINTER(MoeGrads), c_vp,
+                                    ctypes.c_size_t, c_vp]),
+    "moe_clip_workspace_size": (ctypes.c_size_t, [c_i32]),
+    "moe_clip_grads": (ctypes.c_int, [c_i32, ctypes.POINTER(MoeTensor),
+                                      ctypes.c_float, c_vp, c_vp,
+                                      ctypes.c_size_t, c_vp]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_version": (ctypes.c_char_p, []),
 }

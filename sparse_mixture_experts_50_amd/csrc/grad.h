@@ -1,0 +1,117 @@
+// Launch interfaces of the training kernels: expert-sorted rows, the
+// layer's gradient, gradient clipping (internal to the library).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "common.h"
+
+// ------------------------------------------------ expert-sorted rows
+// Row space: routed rows 0 .. shared_base - 1 in expert order, then (with a
+// shared expert) one row per token.
+struct RowsParams {
+    const void *tok;          // [T][d] token-order input (dispatch: x; combine_grad: dy)
+    const void *tok2;         // second token-order input, or null
+    const void *rows_in;      // [rows][d] (dispatch_grad, combine, combine_grad)
+    void *rows_out;           // [rows][d] (dispatch, combine_grad)
+    void *rows_out2;          // rows of tok2, or null
+    void *tok_out;            // [T][d] (dispatch_grad, combine)
+    const int32_t *slot_of;   // [T][k]
+    const float *topk_w;      // [T][k]
+    float *row_w;             // dispatch: [rows] routing weight of each row
+                              // (1 for shared rows), or null
+    float *dw;                // combine_grad: [T][k]
+    int T, d, k, n_shared, shared_base;
+};
+hipError_t launch_dispatch_rows(const RowsParams &p, int dtype, hipStream_t s);
+// tok_out[t] = sum over kept j of rows_in[slot] (times topk_w if weighted)
+// + the shared row.
+hipError_t launch_sum_rows(const RowsParams &p, int dtype, bool weighted,
+                           hipStream_t s);
+hipError_t launch_combine_rows_grad(const RowsParams &p, int dtype,
+                                    hipStream_t s);
+
+// ------------------------------------------------ the layer's gradient
+// Weight matrices and gradients by group: routed experts stacked, the
+// shared expert apart.
+struct FfnGradParams {
+    const int32_t *offsets;   // [E+1]
+    const void *xs, *dys;     // [rows][d] dispatched x and dy
+    const float *row_w;       // [rows]
+    const void *w1, *w2, *w3, *ws1, *ws2, *ws3;
+    const void *b1, *b2, *b3, *bs1, *bs2, *bs3;
+    // h times the row weight, and the gradients of the pre-activations,
+    // [rows][d_ff] each (du: SwiGLU)
+    void *h, *dz, *du;
+    float *dw_part;           // [rows][dw_tiles]: <dy W2, h> by column tile
+    int dw_tiles;
+    float *dxs;               // [rows][d] fp32
+    void *g_w1, *g_w2, *g_w3, *g_ws1, *g_ws2, *g_ws3;
+    void *g_b1, *g_b2, *g_b3, *g_bs1, *g_bs2, *g_bs3;
+    int E, n_shared, T, shared_base, d, d_ff, act;
+    int rows;                 // shared_base + n_shared * T
+};
+// Column tiles that launch_ffn_act_grad writes to dw_part.
+int ffn_grad_dw_tiles(int dtype, int d_ff);
+hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype, hipStream_t s);
+hipError_t launch_ffn_row_grad(const FfnGradParams &p, int dtype, hipStream_t s);
+hipError_t launch_ffn_weight_grad(const FfnGradParams &p, int dtype, hipStream_t s);
+hipError_t launch_ffn_bias_grad(const FfnGradParams &p, int dtype, hipStream_t s);
+
+struct RouterGradParams {
+    const void *x;            // [T][d]
+    const void *wr;           // [E][d]
+    const float *add, *sub;   // [E] or null
+    const int32_t *topk_idx;  // [T][k]
+    const float *topk_w;      // [T][k]
+    const int32_t *slot_of;   // [T][k]
+    const float *f;           // [E] (aux != 0)
+    const float *dw;          // [T][k], or null: from the row partials
+    const float *dw_part;     // [rows][dw_tiles]
+    int dw_tiles;
+    float *logits;            // [T][ep] (where the losses need them)
+    float *dl;                // [T][ep], columns E.. zero
+    float *db_part;           // [ceil(T / MOE_ROUTER_GRAD_TOKENS)][E]
+    float *wr_part;           // [splits][E][d]
+    int splits;
+    const void *dx_add;       // [T][d] in the layer's type, or null
+    const float *dxs;         // [rows][d] expert row gradients, or null
+    void *dx, *dwr;           // [T][d], [E][d]; null = not wanted
+    float *db;                // [E] or null
+    float aux, z;             // d L / d (sum_t f p) and d L / d (sum lse^2)
+    int T, d, E, k, choice, n_shared, shared_base;
+    int ep;                   // E rounded up to 64
+};
+// Tokens of one partial sum of the bias gradient.
+#define MOE_ROUTER_GRAD_TOKENS 32
+// Token ranges that the router weight gradient is split into.
+int router_grad_splits(int T, int d, int E);
+hipError_t launch_router_grad(const RouterGradParams &p, int dtype, hipStream_t s);
+
+// Zero bytes [0, n) (n a multiple of 2) with a kernel.
+hipError_t launch_zero(void *dst, size_t n, hipStream_t s);
+
+// ------------------------------------------------------------- clipping
+// Tensors of one launch; more take several launches.
+#define MOE_CLIP_TENSORS 96
+struct ClipTensor {
+    const void *src;
+    void *dst;
+    long long n;
+};
+struct ClipTable {
+    ClipTensor t[MOE_CLIP_TENSORS];
+    int32_t first[MOE_CLIP_TENSORS + 1];   // first block of each tensor
+    uint32_t f32[(MOE_CLIP_TENSORS + 31) / 32];
+    int32_t count;
+};
+// 32 KB chunks of a tensor (0 for an empty one), the unit of first[].
+long long clip_chunks(long long n, int f32);
+// One partial sum of squares per block.
+hipError_t launch_clip_norm(const ClipTable &tab, double *part, int grid,
+                            hipStream_t s);
+hipError_t launch_clip_scale(const ClipTable &tab, const double *part,
+                             int parts, float max_norm, float *norm, int grid,
+                             hipStream_t s);

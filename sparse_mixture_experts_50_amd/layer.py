@@ -11,6 +11,8 @@ holding OCP E4M3 codes, with float32 per-output-channel scales
 w1_scale [E][d_ff], w2_scale [E][d], ws1_scale [d_ff], ws2_scale [d].
 SwiGLU experts add the up projection w3 [E][d_ff][d], b3 [E][d_ff] (ws3,
 bs3 for the shared expert; w3_scale, ws3_scale for FP8); W1 is the gate.
+Expert-sorted rows are [R + n_shared * T][d]: R = T * k routed rows (E * C
+for expert choice) in slot order, then the shared expert's, one per token.
 """
 from __future__ import annotations
 
@@ -20,7 +22,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import MoeDesc, MoeRouting, MoeWeights, check
+from ._lib import MoeDesc, MoeGrads, MoeRouting, MoeWeights, check
 
 _DT = {torch.float32: _lib.MOE_F32, torch.bfloat16: _lib.MOE_BF16}
 _ROUTING = {"topk": _lib.MOE_ROUTE_TOPK,
@@ -328,6 +330,267 @@ def moe_bias_update(counts, target: float, gamma: float,
         expert_bias.data_ptr(), _stream(expert_bias)))
 
 
+# ------------------------------------------------------------- training
+
+class RouterWeights:
+    """The router's weights alone, for moe_router_grad beside experts that
+    are not this package's: w_router [E][d], b_router / expert_bias [E]
+    float32 or None."""
+
+    def __init__(self, w_router, b_router=None, expert_bias=None):
+        E, d = w_router.shape
+        self.E, self.d = E, d
+        self.dtype, self.device = w_router.dtype, w_router.device
+        self.w_router, self.b_router = w_router, b_router
+        self.expert_bias = expert_bias
+        f32 = torch.float32
+        _need(w_router, "w_router", (E, d), self.dtype, self.device)
+        _opt(b_router, "b_router", (E,), f32, self.device)
+        _opt(expert_bias, "expert_bias", (E,), f32, self.device)
+
+    def struct(self) -> MoeWeights:
+        return MoeWeights(w_router=_ptr(self.w_router),
+                          b_router=_ptr(self.b_router),
+                          expert_bias=_ptr(self.expert_bias))
+
+
+_TORCH = {v: k for k, v in _DT.items()}
+
+
+def _grad_shapes(desc: MoeDesc) -> dict:
+    T, d, E, F = desc.T, desc.d, desc.E, desc.d_ff
+    return {"x": (T, d), "w_router": (E, d), "b_router": (E,),
+            "w1": (E, F, d), "b1": (E, F), "w2": (E, d, F), "b2": (E, d),
+            "ws1": (F, d), "bs1": (F,), "ws2": (d, F), "bs2": (d,),
+            "w3": (E, F, d), "b3": (E, F), "ws3": (F, d), "bs3": (F,)}
+
+
+class Grads:
+    """Gradient buffers of a layer, of the shapes and types of what they
+    are the gradients of (b_router float32).  ``names``: the wanted ones
+    ("x", "w_router", "b_router", "w1", "b1", ... "bs3"); the others are
+    None.  Buffers given by name (``w1=...``) are used as they are."""
+
+    def __init__(self, desc: MoeDesc, device, names=(), **given):
+        shapes = _grad_shapes(desc)
+        dt = _TORCH[desc.dtype]
+        for name in (*names, *given):
+            if name not in shapes:
+                raise ValueError(f"unknown gradient {name!r}")
+        for name, shape in shapes.items():
+            t = given.get(name)
+            want = torch.float32 if name == "b_router" else dt
+            if t is not None:
+                _need(t, name, shape, want, t.device)
+            elif name in names:
+                t = torch.empty(shape, dtype=want, device=device)
+            setattr(self, name, t)
+
+    def as_dict(self) -> dict:
+        """The wanted gradients by name."""
+        return {n: getattr(self, n) for n, _ in MoeGrads._fields_
+                if getattr(self, n) is not None}
+
+    def struct(self) -> MoeGrads:
+        return MoeGrads(*[_ptr(getattr(self, n))
+                          for n, _ in MoeGrads._fields_])
+
+
+def _routed(desc: MoeDesc) -> int:
+    if desc.routing == _lib.MOE_ROUTE_EXPERT_CHOICE:
+        return desc.E * desc.capacity
+    return desc.T * desc.k
+
+
+def _tokens(desc, t, name, device):
+    _need(t, name, (desc.T, desc.d), _TORCH[desc.dtype], device)
+
+
+def _rows(desc, t, name, device):
+    _need(t, name, (_routed(desc) + desc.n_shared * desc.T, desc.d),
+          _TORCH[desc.dtype], device)
+
+
+def _routing(desc, r: Routing, device):
+    """The routing buffers of this descriptor's calls."""
+    if r.slot_of.device != device:
+        raise ValueError(f"routing on {r.slot_of.device}, expected {device}")
+    if (tuple(r.slot_of.shape) != (desc.T, desc.k) or
+            r.slot_token.numel() != _routed(desc) or
+            r.offsets.numel() != desc.E + 1):
+        raise ValueError("routing buffers of another shape")
+
+
+def _run(name: str, t: torch.Tensor, *args) -> None:
+    """Call an entry point on the current stream of t's device, with that
+    device current (a stream handle of 0 means the current device's)."""
+    fn = getattr(_lib.lib(), name)
+    if t.device.index == torch.cuda.current_device():
+        check(name, fn(*args, _stream(t)))
+    else:
+        with torch.cuda.device(t.device):
+            check(name, fn(*args, _stream(t)))
+
+
+def moe_dispatch_rows(desc, r: Routing, x, xs) -> None:
+    """x [T][d] into expert-sorted rows xs; rows of dropped assignments are
+    left as they were."""
+    _tokens(desc, x, "x", x.device)
+    _rows(desc, xs, "xs", x.device)
+    _routing(desc, r, x.device)
+    rs = r.struct()
+    _run("moe_dispatch_rows", x, ctypes.byref(desc), ctypes.byref(rs),
+         x.data_ptr(), xs.data_ptr())
+
+
+def moe_dispatch_rows_grad(desc, r: Routing, dxs, dx) -> None:
+    """dx [T][d]: the gradient of moe_dispatch_rows for row gradients dxs."""
+    _tokens(desc, dx, "dx", dx.device)
+    _rows(desc, dxs, "dxs", dx.device)
+    _routing(desc, r, dx.device)
+    rs = r.struct()
+    _run("moe_dispatch_rows_grad", dx, ctypes.byref(desc), ctypes.byref(rs),
+         dxs.data_ptr(), dx.data_ptr())
+
+
+def moe_combine_rows(desc, r: Routing, ys, y) -> None:
+    """Expert-sorted rows ys back into token order, weighted: y [T][d]."""
+    _tokens(desc, y, "y", y.device)
+    _rows(desc, ys, "ys", y.device)
+    _routing(desc, r, y.device)
+    rs = r.struct()
+    _run("moe_combine_rows", y, ctypes.byref(desc), ctypes.byref(rs),
+         ys.data_ptr(), y.data_ptr())
+
+
+def moe_combine_rows_grad(desc, r: Routing, dy, ys, dys, dw) -> None:
+    """Gradients of moe_combine_rows for dy [T][d]: of the rows into dys
+    (may be ys itself; rows of dropped assignments are left as they were),
+    of the routing weights into dw [T][k] float32."""
+    _tokens(desc, dy, "dy", dy.device)
+    _rows(desc, ys, "ys", dy.device)
+    _rows(desc, dys, "dys", dy.device)
+    _need(dw, "dw", (desc.T, desc.k), torch.float32, dy.device)
+    _routing(desc, r, dy.device)
+    rs = r.struct()
+    _run("moe_combine_rows_grad", dy, ctypes.byref(desc), ctypes.byref(rs),
+         dy.data_ptr(), ys.data_ptr(), dys.data_ptr(), dw.data_ptr())
+
+
+def moe_router_grad_workspace_size(desc: MoeDesc) -> int:
+    n = _lib.lib().moe_router_grad_workspace_size(ctypes.byref(desc))
+    if n == 0:
+        raise _lib.MoeError("moe_router_grad_workspace_size",
+                            _lib.MOE_ERR_INVALID_ARG)
+    return n
+
+
+def moe_grad_workspace_size(desc: MoeDesc) -> int:
+    n = _lib.lib().moe_grad_workspace_size(ctypes.byref(desc))
+    if n == 0:
+        raise _lib.MoeError(
+            "moe_grad_workspace_size", _lib.MOE_ERR_UNSUPPORTED
+            if desc.expert_fp8 else _lib.MOE_ERR_INVALID_ARG)
+    return n
+
+
+def _grad_ws(need: int, ws: torch.Tensor, device):
+    if ws.device != device:
+        raise ValueError(f"workspace on {ws.device}, expected {device}")
+    n = ws.numel() * ws.element_size()
+    if n < need or not ws.is_contiguous():
+        raise ValueError(f"workspace needs {need} contiguous bytes")
+    return ws.data_ptr(), n
+
+
+def _check_grads(desc, g: Grads, device):
+    shapes = _grad_shapes(desc)
+    for name, t in g.as_dict().items():
+        want = torch.float32 if name == "b_router" else _TORCH[desc.dtype]
+        _need(t, "gradient " + name, shapes[name], want, device)
+
+
+def _check_router(desc, x, w, r, what):
+    _tokens(desc, x, "x", w.device)
+    if (w.E, w.d) != (desc.E, desc.d) or w.dtype != x.dtype:
+        raise ValueError(f"{what}: weights of another layer")
+    _routing(desc, r, w.device)
+
+
+def moe_router_grad(desc, x, w, r: Routing, dw, g: Grads, ws,
+                    aux_scale: float = 0.0, z_scale: float = 0.0,
+                    dx_add=None) -> None:
+    """Gradient of the router for the gradient dw [T][k] of the routing
+    weights and of aux_scale * l_aux + z_scale * z-loss, into g.x (plus
+    ``dx_add``), g.w_router and g.b_router where wanted.  ``w``: Weights or
+    RouterWeights; ``ws`` of moe_router_grad_workspace_size(desc) bytes."""
+    _check_router(desc, x, w, r, "moe_router_grad")
+    _need(dw, "dw", (desc.T, desc.k), torch.float32, w.device)
+    if dx_add is not None:
+        _tokens(desc, dx_add, "dx_add", w.device)
+    _check_grads(desc, g, w.device)
+    p, n = _grad_ws(moe_router_grad_workspace_size(desc), ws, w.device)
+    rs, wsct, gs = r.struct(), w.struct(), g.struct()
+    _run("moe_router_grad", x, ctypes.byref(desc), x.data_ptr(),
+         ctypes.byref(wsct), ctypes.byref(rs), dw.data_ptr(), _ptr(dx_add),
+         float(aux_scale), float(z_scale), ctypes.byref(gs), p, n)
+
+
+def moe_backward(desc, x, w: Weights, r: Routing, dy, g: Grads, ws,
+                 aux_scale: float = 0.0, z_scale: float = 0.0) -> None:
+    """Gradient of the layer (moe_forward) for dy [T][d] and of
+    aux_scale * l_aux + z_scale * z-loss, into the buffers of g.  x, w and r
+    are the forward's; ``ws`` of moe_grad_workspace_size(desc) bytes."""
+    _check_router(desc, x, w, r, "moe_backward")
+    if (w.d_ff, w.n_shared, int(w.expert_fp8)) != (
+            desc.d_ff, desc.n_shared, desc.expert_fp8):
+        raise ValueError("moe_backward: weights of another layer")
+    _tokens(desc, dy, "dy", w.device)
+    _check_grads(desc, g, w.device)
+    p, n = _grad_ws(moe_grad_workspace_size(desc), ws, w.device)
+    rs, wsct, gs = r.struct(), w.struct(), g.struct()
+    _run("moe_backward", x, ctypes.byref(desc), x.data_ptr(),
+         ctypes.byref(wsct), ctypes.byref(rs), dy.data_ptr(),
+         float(aux_scale), float(z_scale), ctypes.byref(gs), p, n)
+
+
+def moe_clip_workspace_size(tensors) -> int:
+    """Workspace bytes of moe_clip_grads for these tensors."""
+    return _lib.lib().moe_clip_workspace_size(len(tensors))
+
+
+def moe_clip_grads(tensors, max_norm: float, norm, ws, out=None) -> None:
+    """Global norm of contiguous float32 / bfloat16 tensors into norm [1]
+    (float32), and the tensors scaled by min(1, max_norm / (norm + 1e-6)),
+    in place or into ``out`` (tensors of the same sizes and types).  ``ws``
+    of moe_clip_workspace_size(tensors) bytes."""
+    device = norm.device
+    _need(norm, "norm", (1,), torch.float32, device)
+    out = tensors if out is None else out
+    if len(out) != len(tensors):
+        raise ValueError("out: as many tensors as there are gradients")
+    arr = (_lib.MoeTensor * len(tensors))()
+    seen = set()
+    for item, t, o in zip(arr, tensors, out):
+        n = t.numel()
+        if t.dtype not in _DT:
+            raise ValueError(f"unsupported dtype {t.dtype}")
+        if (t.device != device or o.device != device or o.dtype != t.dtype
+                or o.numel() != n):
+            raise ValueError("tensors of one device; out of the same sizes "
+                             "and types")
+        if not (t.is_contiguous() and o.is_contiguous()):
+            raise ValueError("tensors must be contiguous")
+        item.src, item.dst = t.data_ptr(), o.data_ptr()
+        item.numel, item.dtype = n, _DT[t.dtype]
+        if n and item.dst in seen:
+            raise ValueError("a tensor is given twice")
+        seen.add(item.dst)
+    p, size = _grad_ws(moe_clip_workspace_size(tensors), ws, device)
+    _run("moe_clip_grads", norm, len(tensors), arr, float(max_norm),
+         norm.data_ptr(), p, size)
+
+
 class MoeLayer:
     """One sparse MoE FFN layer on a GPU: weights plus reusable buffers.
 
@@ -361,6 +624,7 @@ class MoeLayer:
         self.aux_alpha = aux_alpha
         self.routing = routing
         self._bufs = {}
+        self._grad_bufs = {}
 
     def desc(self, T: int) -> MoeDesc:
         w = self.w
@@ -394,6 +658,32 @@ class MoeLayer:
         desc, r, ws, y = self.buffers(x.shape[0])
         moe_forward(desc, x.contiguous(), self.w, r, y, ws)
         return y, r
+
+    def grad_buffers(self, T: int):
+        """(descriptor, Grads of x and every weight of the layer, gradient
+        workspace) for calls of T tokens."""
+        if T not in self._grad_bufs:
+            desc, w = self.desc(T), self.w
+            ws = torch.empty(moe_grad_workspace_size(desc),
+                             dtype=torch.uint8, device=w.device)
+            names = ["x"] + [n for n in _grad_shapes(desc)
+                             if getattr(w, n, None) is not None]
+            self._grad_bufs[T] = (desc, Grads(desc, w.device, names), ws)
+        return self._grad_bufs[T]
+
+    def backward(self, x: torch.Tensor, routing: Routing, dy: torch.Tensor,
+                 aux_scale: float = 1.0, z_scale: float = 0.0) -> Grads:
+        """Gradients of sum(dy * y) + aux_scale * l_aux + z_scale * z-loss
+        for the forward that had this x and left this routing: of x and of
+        every weight (FP8 experts have none).  The buffers are reused by
+        the next backward with the same T; its x is (T, H) also for a
+        (B, S, H) input."""
+        x = x.reshape(-1, x.shape[-1]).contiguous()
+        dy = dy.reshape(-1, dy.shape[-1]).contiguous()
+        desc, g, ws = self.grad_buffers(x.shape[0])
+        moe_backward(desc, x, self.w, routing, dy, g, ws,
+                     aux_scale=aux_scale, z_scale=z_scale)
+        return g
 
     def bias_update(self, routing: Routing, gamma: float) -> None:
         """One aux-loss-free step on weights.expert_bias from the counts of
