@@ -15,7 +15,7 @@
 // the backward reads nothing of the forward but the routing.  z and u are
 // computed again from x (2 or 4 d d_ff operations a row) instead of being
 // kept by the forward (4 or 8 bytes a value, written and read).
-#include "grad.h"
+#include "ffn_grad.h"
 #include "simt.h"
 
 namespace {
@@ -44,20 +44,6 @@ __device__ __forceinline__ void act_grad(float z, float u, float &h, float &hz,
             hu = a;
         }
     }
-}
-
-// Matrix of group g: routed experts stacked, the shared expert apart.
-template <typename T>
-__device__ __forceinline__ T *of_group(void *routed, void *shared, int g,
-                                       int E, size_t per) {
-    return g < E ? (routed ? (T *)routed + g * per : nullptr) : (T *)shared;
-}
-template <typename T>
-__device__ __forceinline__ const T *of_group(const void *routed,
-                                             const void *shared, int g, int E,
-                                             size_t per) {
-    return g < E ? (routed ? (const T *)routed + g * per : nullptr)
-                 : (const T *)shared;
 }
 
 // Row tiles: 64 rows of one group by 64 columns.
@@ -168,18 +154,6 @@ __global__ __launch_bounds__(256) void ffn_row_grad_simt(FfnGradParams p) {
     }
 }
 
-// Rows of group g: [start, start + rows).
-__device__ __forceinline__ void group_rows(const FfnGradParams &p, int g,
-                                           int &start, int &rows) {
-    if (g < p.E) {
-        start = p.offsets[g];
-        rows = p.offsets[g + 1] - start;
-    } else {
-        start = p.shared_base;
-        rows = p.T;
-    }
-}
-
 // dW[m][n] = sum over the group's rows s of L[s][m] R[s][n]; blockIdx.z:
 // dW1 (dz, x), dW2 (dy, r h), dW3 (du, x).  A group without rows gets
 // zeros.
@@ -265,10 +239,8 @@ __global__ __launch_bounds__(256) void ffn_bias_dot(FfnGradParams p) {
     }
 }
 
-// Row tiles of a grid: at most ceil(rows / bm) plus one per group.
 int row_tiles(const FfnGradParams &p, int bm, int ncols) {
-    const long long mt = (p.rows + bm - 1) / bm + p.E + p.n_shared;
-    const long long n = mt * ncols;
+    const long long n = ffn_row_tiles(p, bm) * ncols;
     return (int)(n < 65536 ? n : 65536);
 }
 
@@ -285,7 +257,9 @@ void act_grad_simt(const FfnGradParams &p, hipStream_t s) {
 
 }  // namespace
 
-int ffn_grad_dw_tiles(int dtype, int d_ff) { return d_ff / simt::BN; }
+int ffn_grad_dw_tiles(int dtype, int d_ff) {
+    return dtype == 1 ? mfma_dw_tiles(d_ff) : d_ff / simt::BN;
+}
 
 hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype,
                                hipStream_t s) {
@@ -296,29 +270,25 @@ hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype,
         else
             hipLaunchKernelGGL((ffn_bias_dot<float>), grid, dim3(256), 0, s, p);
     }
-    if (dtype == 1) act_grad_simt<uint16_t>(p, s);
-    else act_grad_simt<float>(p, s);
+    if (dtype == 1) return launch_act_grad_mfma(p, s);
+    act_grad_simt<float>(p, s);
     return hipGetLastError();
 }
 
 hipError_t launch_ffn_row_grad(const FfnGradParams &p, int dtype,
                                hipStream_t s) {
+    if (dtype == 1) return launch_row_grad_mfma(p, s);
     const dim3 grid(row_tiles(p, simt::BM, p.d / simt::BN));
-    if (dtype == 1)
-        hipLaunchKernelGGL((ffn_row_grad_simt<uint16_t>), grid, dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL((ffn_row_grad_simt<float>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((ffn_row_grad_simt<float>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
 hipError_t launch_ffn_weight_grad(const FfnGradParams &p, int dtype,
                                   hipStream_t s) {
+    if (dtype == 1) return launch_weight_grad_mfma(p, s);
     const dim3 grid(p.d / simt::BM * (p.d_ff / simt::BN), p.E + p.n_shared,
                     p.act == ACT_SWIGLU ? 3 : 2);
-    if (dtype == 1)
-        hipLaunchKernelGGL((ffn_weight_grad_simt<uint16_t>), grid, dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL((ffn_weight_grad_simt<float>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((ffn_weight_grad_simt<float>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
