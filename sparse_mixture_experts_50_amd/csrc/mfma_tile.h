@@ -62,8 +62,9 @@ struct Operand {
 };
 
 // W rows (columns) of one operand in a slot, PANELS of them: the addresses
-// of its loads and fragments.  ZK: K is ragged (kvalid holds).
-template <bool KF, int W, int PANELS, bool ZK>
+// of its loads and of a wave's NQ fragments (of one panel).  ZK: K is ragged
+// (kvalid holds).
+template <bool KF, int W, int PANELS, int NQ, bool ZK>
 struct Side {
     static constexpr int UNITS = W * 8 * PANELS;     // 16-byte units a stage
     static constexpr int LOADS = UNITS / 256;        // per wave and stage
@@ -112,39 +113,53 @@ struct Side {
         }
     }
 
-    // load q of stage s into the slot's part of this operand
-    __device__ __forceinline__ void load(int s, int q, u32x4 *st, int wave) const {
+    // load q of stage s into the slot's part of this operand (at unit u0)
+    __device__ __forceinline__ void load(int s, int q, u32x4 *st, int u0, int wave) const {
         if (KF) {
             const int k0 = s * SK + q * KSTEP;
             const char *p = base + (size_t)k0 * ld + off[q & 1];
             if (ZK && k0 + kl >= kvalid) p = zero_line + (threadIdx.x & 63) * 16;
-            dma16(p, st + (q * 4 + wave) * 64);
+            dma16(p, st + (u0 + (q * 4 + wave) * 64));
         } else {
             const char *b = PANELS > 1 && q >= PER ? base2 : base;
             dma16(b + (size_t)s * (SK * 2) + off[KF ? 0 : q % PER],
-                  st + (wave + 4 * q) * 64);
+                  st + (u0 + (wave + 4 * q) * 64));
         }
     }
 
-    // part h of fragment (16 rows from row r0 of the slot), sub-step kk
-    static __device__ __forceinline__ void read(bf16x8 &f, const u32x4 *st, int kk,
-                                                int r0, int h, int lane) {
+    // Slot index of this lane's part of fragment q (16 rows from row
+    // r0 + 16 q) at sub-step 0, in reads (8 bytes for K_FIRST, else 16),
+    // K_LAST: for both sub-steps.  Opaque, so that a read is one index off
+    // the slot: through longer address arithmetic the compiler loses track
+    // of which slot is read, and waits for every load in flight.
+    int rd[KF ? NQ : 2];
+    __device__ __forceinline__ void init_reads(int u0, int r0, int lane) {
+        const int l16 = lane & 15, b = lane >> 4;
+#pragma unroll
+        for (int q = 0; q < (KF ? NQ : 2); ++q) {
+            if (KF) {
+                const int k = 8 * b + (l16 >> 2);
+                rd[q] = u0 * 2 + k * (W / 4) + ((((r0 >> 4) + q) ^ swz(k)) * 4) + (l16 & 3);
+            } else {
+                rd[q] = u0 + (r0 + l16) * 8 + ((q * 4 + b) ^ ((l16 >> 1) & 7));
+            }
+            asm("" : "+v"(rd[q]));
+        }
+    }
+    // part h of fragment q, sub-step kk; row0: rows from r0 on (K_LAST)
+    __device__ __forceinline__ void read(bf16x8 &f, const u32x4 *st, int kk, int q,
+                                         int row0, int h) const {
         if (KF) {
-            const int i = lane & 15, b = lane >> 4;
-            const int k = kk * 32 + 8 * b + 4 * h + (i >> 2);
-            const int piece = (r0 >> 4) ^ swz(8 * b + (i >> 2));
-            const char *p = (const char *)st + k * (W * 2) + piece * 32 + (i & 3) * 8;
             const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4 *)p);
+                (__attribute__((address_space(3))) s16x4 *)st +
+                (rd[KF ? q : 0] + (kk * 32 + 4 * h) * (W / 4)));
             s16x8 w = __builtin_bit_cast(s16x8, f);
             const s16x8 x = __builtin_shufflevector(v, v, 0, 1, 2, 3, 0, 1, 2, 3);
             w = h == 0 ? __builtin_shufflevector(x, w, 0, 1, 2, 3, 12, 13, 14, 15)
                        : __builtin_shufflevector(w, x, 0, 1, 2, 3, 12, 13, 14, 15);
             f = __builtin_bit_cast(bf16x8, w);
         } else {
-            const int l16 = lane & 15;
-            const int c = (kk * 4 + (lane >> 4)) ^ ((l16 >> 1) & 7);
-            f = as_bf16x8(st[(r0 + l16) * 8 + c]);
+            f = as_bf16x8(st[rd[kk] + row0 * 8]);
         }
     }
 };
@@ -155,8 +170,8 @@ template <int RB, int TN, int WM, int WN, int PANELS, bool AF, bool BF, bool ZK,
 struct Product {
     static_assert(WM * WN == 4, "four waves");
     static constexpr int BM = RB * 16 * WM, BN = TN * 16 * WN;
-    typedef Side<AF, BM, 1, ZK> SA;
-    typedef Side<BF, BN, PANELS, ZK> SB;
+    typedef Side<AF, BM, 1, RB, ZK> SA;
+    typedef Side<BF, BN, PANELS, TN, ZK> SB;
     static constexpr int STAGE = SA::UNITS + SB::UNITS;
     static constexpr int NC = TN * PANELS;           // column blocks a wave
     static constexpr int NM = RB * NC;               // MFMAs per sub-step
@@ -186,20 +201,21 @@ struct Product {
         SB b;
         a.init(oa, wave, lane);
         b.init(ob, wave, lane);
+        a.init_reads(0, wm * RB * 16, lane);
+        b.init_reads(SA::UNITS, wn * TN * 16, lane);
         auto load = [&](int s, u32x4 *st, int q) __attribute__((always_inline)) {
-            if (q < SA::LOADS) a.load(s, q, st, wave);
-            else b.load(s, q - SA::LOADS, st + SA::UNITS, wave);
+            if (q < SA::LOADS) a.load(s, q, st, 0, wave);
+            else b.load(s, q - SA::LOADS, st, SA::UNITS, wave);
         };
         auto read = [&](bf16x8 (&fa)[RB], bf16x8 (&fb)[NC], const u32x4 *st, int kk,
                         int r) __attribute__((always_inline)) {
             if (r < NA) {
                 const int q = r / SA::READS;
-                SA::read(fa[q], st, kk, wm * RB * 16 + q * 16, r % SA::READS, lane);
+                a.read(fa[q], st, kk, q, q * 16, r % SA::READS);
             } else {
                 const int q = (r - NA) / SB::READS;
-                SB::read(fb[q], st + SA::UNITS, kk,
-                         (q / TN) * BN + wn * TN * 16 + (q % TN) * 16,
-                         (r - NA) % SB::READS, lane);
+                b.read(fb[q], st, kk, q % TN, (q / TN) * BN + (q % TN) * 16,
+                       (r - NA) % SB::READS);
             }
         };
         bf16x8 fa0[RB], fb0[NC], fa1[RB], fb1[NC];
