@@ -38,4 +38,4 @@ inline long long ffn_row_tiles(const FfnGradParams &p, int bm) {
 hipError_t launch_act_grad_mfma(const FfnGradParams &p, hipStream_t s);
 hipError_t launch_row_grad_mfma(const FfnGradParams &p, hipStream_t s);
 hipError_t launch_weight_grad_mfma(const FfnGradParams &p, hipStream_t s);
-int mfma_dw_tiles(int d_ff);
+int mfma_dw_tiles(int d_ff, int act);

@@ -257,8 +257,8 @@ void act_grad_simt(const FfnGradParams &p, hipStream_t s) {
 
 }  // namespace
 
-int ffn_grad_dw_tiles(int dtype, int d_ff) {
-    return dtype == 1 ? mfma_dw_tiles(d_ff) : d_ff / simt::BN;
+int ffn_grad_dw_tiles(int dtype, int d_ff, int act) {
+    return dtype == 1 ? mfma_dw_tiles(d_ff, act) : d_ff / simt::BN;
 }
 
 hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype,

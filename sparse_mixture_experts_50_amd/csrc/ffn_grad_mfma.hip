@@ -1,10 +1,14 @@
 // The bf16 layer's gradient GEMMs on the matrix cores (formulas in
 // ffn_grad.hip, the tile product in mfma_tile.h):
-//   act grad     z = x W1^T, u = x W3^T, q = dy W2 on one output tile, then
+//   rows by weights  q = dy W2 (fp32), and at the end dx = dz W1 + du W3
+//   act grad     z = x W1^T and u = x W3^T on one output tile, then with q
 //                r h, dz, du and the parts of <q, h> from the accumulators
-//   row grad     dx = dz W1 + du W3
 //   weight grad  dW1 = dz^T x, dW3 = du^T x, dW2 = dy^T (r h) over the rows
 //                of a group
+// q passes through memory in fp32 (4 bytes a value, written and read once:
+// 0.2 ms of the Mixtral-shaped 4096-token gradient) so that every product
+// has a 256 x 256 tile: with z and q accumulated side by side a block's
+// tile is 256 x 128, whose fragment reads take longer than its MFMAs.
 // All three are persistent: one block per CU, whose tiles of a round lie
 // side by side in each XCD (consecutive tile numbers), where they share
 // operand panels through that XCD's L2.
@@ -96,19 +100,17 @@ __device__ __forceinline__ RowTile row_tile(const TileTable &tt, int G, int L) {
     return r;
 }
 
-template <int RB, int TN, int WM, int WN, int ACT>
-__global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
-    constexpr int PANELS = ACT == ACT_SWIGLU ? 2 : 1;
-    // gated: z and u fill the AGPRs, q goes to VGPRs
-    typedef mt::Product<RB, TN, WM, WN, PANELS, false, false, false, true> PZ;
-    typedef mt::Product<RB, TN, WM, WN, 1, false, true, false, PANELS == 1> PQ;
-    constexpr int BM = PZ::BM, BN = PZ::BN;
-    constexpr int STAGE = PZ::STAGE > PQ::STAGE ? PZ::STAGE : PQ::STAGE;
-    __shared__ u32x4 slot0[STAGE], slot1[STAGE];
+// out[rows][N] (fp32) = the sum of one or two products A B of a group's rows
+// with its weights, stored along K.  Q: q = dy W2; else dx = dz W1 + du W3.
+template <int RB, int TN, int WM, int WN, bool Q, bool ODD>
+__global__ __launch_bounds__(256, 1) void ffn_rows_by_weights(FfnGradParams p) {
+    typedef mt::Product<RB, TN, WM, WN, 1, false, true, false, ODD> P;
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
     __shared__ TileTable tt;
-    const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
-    build_tile_table(tt, p.offsets, p.E, p.n_shared, p.shared_base, p.T, BM,
-                     (F + BN - 1) / BN);
+    const int G = p.E + p.n_shared;
+    const int N = Q ? p.d_ff : p.d, K = Q ? p.d : p.d_ff;
+    build_tile_table(tt, p.offsets, p.E, p.n_shared, p.shared_base, p.T, P::BM,
+                     (N + P::BN - 1) / P::BN);
     const int total = __builtin_amdgcn_readfirstlane(tt.base[G]);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -119,54 +121,115 @@ __global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
         int tid = threadIdx.x;
         asm volatile("" : "+v"(tid));
         const int lane = tid & 63;
-        const RowTile t = row_tile<BM>(tt, G, L);
-        const int n0 = t.n_tile * BN;
+        const RowTile t = row_tile<P::BM>(tt, G, L);
+        const int n0 = t.n_tile * P::BN;
+        const size_t mat = (size_t)p.d_ff * p.d, at = (size_t)t.row0 * K;
+        mt::Operand a = {(const char *)((const bf16 *)(Q ? p.dys : p.dz) + at), nullptr,
+                         (size_t)K * 2, t.nrows, 0};
+        mt::Operand b = {(const char *)(of_group<bf16>(Q ? p.w2 : p.w1, Q ? p.ws2 : p.ws1,
+                                                       t.g, p.E, mat) + n0),
+                         nullptr, (size_t)N * 2, min(P::BN, N - n0), 0};
+        floatx4 acc[RB][TN];
+        mt::clear(acc);
+        P::run(acc, a, b, slot0, slot1, K / mt::SK, wave, lane);
+        if (!Q && p.act == ACT_SWIGLU) {
+            a.base = (const char *)((const bf16 *)p.du + at);
+            b.base = (const char *)(of_group<bf16>(p.w3, p.ws3, t.g, p.E, mat) + n0);
+            P::run(acc, a, b, slot0, slot1, K / mt::SK, wave, lane);
+        }
+        const int l16 = lane & 15, c0 = n0 + wn * TN * 16;
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            const int m = (wm * RB + i) * 16 + l16;
+            if (m >= t.nrows) continue;
+            float *out = (Q ? p.q : p.dxs) + (size_t)(t.row0 + m) * N + c0 + 4 * (lane >> 4);
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                if (c0 + 16 * j < N) *(floatx4 *)(out + 16 * j) = acc[i][j];
+        }
+    }
+}
+
+// z (and u) of a tile, then with q: r h, dz, du and the parts of <q, h>.  A
+// gated tile has TN column blocks of z and the same TN of u per wave.
+template <int RB, int TN, int WM, int WN, int ACT, bool ODD>
+__global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
+    constexpr int PANELS = ACT == ACT_SWIGLU ? 2 : 1;
+    typedef mt::Product<RB, TN, WM, WN, PANELS, false, false, false, ODD> P;
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
+    __shared__ TileTable tt;
+    const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
+    build_tile_table(tt, p.offsets, p.E, p.n_shared, p.shared_base, p.T, P::BM,
+                     (F + P::BN - 1) / P::BN);
+    const int total = __builtin_amdgcn_readfirstlane(tt.base[G]);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    for (int r = 0;; ++r) {
+        const int L = tile_of(r);
+        if (L >= total) break;
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63;
+        const RowTile t = row_tile<P::BM>(tt, G, L);
+        const int n0 = t.n_tile * P::BN;
         const size_t mat = (size_t)F * d;
         const bf16 *w1 = of_group<bf16>(p.w1, p.ws1, t.g, p.E, mat);
-        const bf16 *w2 = of_group<bf16>(p.w2, p.ws2, t.g, p.E, mat);
         const bf16 *w3 = PANELS > 1 ? of_group<bf16>(p.w3, p.ws3, t.g, p.E, mat) : w1;
-        const int nv = min(BN, F - n0);
-        mt::Operand a = {(const char *)((const bf16 *)p.xs + (size_t)t.row0 * d),
-                         nullptr, (size_t)d * 2, t.nrows, 0};
-        mt::Operand b = {(const char *)(w1 + (size_t)n0 * d),
-                         (const char *)(w3 + (size_t)n0 * d), (size_t)d * 2, nv, 0};
-        floatx4 z[RB][TN * PANELS], q[RB][TN];
-        mt::clear(z);
-        mt::clear(q);
-        PZ::run(z, a, b, slot0, slot1, d / mt::SK, wave, lane);
-        a.base = (const char *)((const bf16 *)p.dys + (size_t)t.row0 * d);
-        b = {(const char *)(w2 + n0), nullptr, (size_t)F * 2, nv, 0};
-        PQ::run(q, a, b, slot0, slot1, d / mt::SK, wave, lane);
-        __builtin_amdgcn_s_waitcnt(0);
-        __builtin_amdgcn_s_barrier();        // the slots are free
-
+        const mt::Operand a = {(const char *)((const bf16 *)p.xs + (size_t)t.row0 * d),
+                               nullptr, (size_t)d * 2, t.nrows, 0};
+        const mt::Operand b = {(const char *)(w1 + (size_t)n0 * d),
+                               (const char *)(w3 + (size_t)n0 * d), (size_t)d * 2,
+                               min(P::BN, F - n0), 0};
         const int l16 = lane & 15, c0 = n0 + wn * TN * 16;
         const int cols = F - c0;             // columns of this wave
-        if (cols <= 0) continue;
         const int cq = c0 + 4 * (lane >> 4);
-        const bf16 *b1 = of_group<bf16>(p.b1, p.bs1, t.g, p.E, F);
-        const bf16 *b3 = PANELS > 1 ? of_group<bf16>(p.b3, p.bs3, t.g, p.E, F) : nullptr;
+        // the sums start from the biases
+        floatx4 z[RB][TN * PANELS];
+        mt::clear(z);
+        const bf16 *bias[2] = {of_group<bf16>(p.b1, p.bs1, t.g, p.E, F),
+                               PANELS > 1 ? of_group<bf16>(p.b3, p.bs3, t.g, p.E, F) : nullptr};
+#pragma unroll
+        for (int k = 0; k < PANELS; ++k)
+            if (bias[k]) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    if (16 * j >= cols) continue;    // whole blocks: F % 64 == 0
+                    const u32x2 v = *(const u32x2 *)(bias[k] + cq + 16 * j);
+                    const floatx4 f = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) z[i][k * TN + j] = f;
+                }
+            }
+        P::run(z, a, b, slot0, slot1, d / mt::SK, wave, lane);
+        __builtin_amdgcn_s_waitcnt(0);
+        __builtin_amdgcn_s_barrier();        // the slots are free
+        if (cols <= 0) continue;
         char *scr = (char *)slot0 + wave * (TN * 512);
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
             const int m0 = (wm * RB + i) * 16;
             const int rows = t.nrows - m0;
             if (rows <= 0) continue;
-            const int row = t.row0 + m0 + l16;
-            const float w = l16 < rows ? p.row_w[row] : 0.0f;
+            // rows past the group's end read its last row and store nothing
+            const int row = t.row0 + m0 + min(l16, rows - 1);
+            const float w = p.row_w[row];
+            const float *qp = p.q + (size_t)row * F + cq;
+            floatx4 q[TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                q[j] = *(const floatx4 *)(qp + (16 * j < cols ? 16 * j : 0));
             float vh[TN][4], vz[TN][4], vu[TN][4], dot = 0.0f;
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                const bool in = 16 * j < cols;       // whole blocks: F % 64 == 0
+                const float in = 16 * j < cols ? 1.0f : 0.0f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float zz = z[i][j][e], uu = PANELS > 1 ? z[i][j + TN * (PANELS - 1)][e] : 0.0f;
-                    if (b1 && in) zz += bf16_to_f32(b1[cq + 16 * j + e]);
-                    if (b3 && in) uu += bf16_to_f32(b3[cq + 16 * j + e]);
                     float h, hz, hu;
-                    act_grad<ACT>(zz, uu, h, hz, hu);
-                    const float qq = q[i][j][e];
-                    if (in) dot = fmaf(qq, h, dot);
+                    act_grad<ACT>(z[i][j][e],
+                                  PANELS > 1 ? z[i][j + TN * (PANELS - 1)][e] : 0.0f, h,
+                                  hz, hu);
+                    const float qq = q[j][e] * in;
+                    dot = fmaf(qq, h, dot);
                     vh[j][e] = w * h;
                     vz[j][e] = w * qq * hz;
                     if (PANELS > 1) vu[j][e] = w * qq * hu;
@@ -180,52 +243,9 @@ __global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
             store_rows<TN>(scr, vh, (bf16 *)p.h + at, F, rows, cols, lane);
             store_rows<TN>(scr, vz, (bf16 *)p.dz + at, F, rows, cols, lane);
             if (PANELS > 1) store_rows<TN>(scr, vu, (bf16 *)p.du + at, F, rows, cols, lane);
-        }
-    }
-}
-
-template <int RB, int TN, int WM, int WN>
-__global__ __launch_bounds__(256, 1) void ffn_row_grad(FfnGradParams p) {
-    typedef mt::Product<RB, TN, WM, WN, 1, false, true, false, true> P;
-    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
-    __shared__ TileTable tt;
-    const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
-    build_tile_table(tt, p.offsets, p.E, p.n_shared, p.shared_base, p.T, P::BM,
-                     (d + P::BN - 1) / P::BN);
-    const int total = __builtin_amdgcn_readfirstlane(tt.base[G]);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / WN, wn = wave % WN;
-    for (int r = 0;; ++r) {
-        const int L = tile_of(r);
-        if (L >= total) break;
-        int tid = threadIdx.x;
-        asm volatile("" : "+v"(tid));
-        const int lane = tid & 63;
-        const RowTile t = row_tile<P::BM>(tt, G, L);
-        const int n0 = t.n_tile * P::BN;
-        const size_t mat = (size_t)F * d, at = (size_t)t.row0 * F;
-        const int nv = min(P::BN, d - n0);
-        mt::Operand a = {(const char *)((const bf16 *)p.dz + at), nullptr,
-                         (size_t)F * 2, t.nrows, 0};
-        mt::Operand b = {(const char *)(of_group<bf16>(p.w1, p.ws1, t.g, p.E, mat) + n0),
-                         nullptr, (size_t)d * 2, nv, 0};
-        floatx4 acc[RB][TN];
-        mt::clear(acc);
-        P::run(acc, a, b, slot0, slot1, F / mt::SK, wave, lane);
-        if (p.act == ACT_SWIGLU) {
-            a.base = (const char *)((const bf16 *)p.du + at);
-            b.base = (const char *)(of_group<bf16>(p.w3, p.ws3, t.g, p.E, mat) + n0);
-            P::run(acc, a, b, slot0, slot1, F / mt::SK, wave, lane);
-        }
-        const int l16 = lane & 15, c0 = n0 + wn * TN * 16;
-#pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            const int m = (wm * RB + i) * 16 + l16;
-            if (m >= t.nrows) continue;
-            float *out = p.dxs + (size_t)(t.row0 + m) * d + c0 + 4 * (lane >> 4);
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                if (c0 + 16 * j < d) *(floatx4 *)(out + 16 * j) = acc[i][j];
+            // one row block at a time: the accumulators are read as they are
+            // used, not all at once
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
@@ -234,7 +254,7 @@ __global__ __launch_bounds__(256, 1) void ffn_row_grad(FfnGradParams p) {
 // consecutive tiles of an XCD's round are 8 x 4 and read 12 operand panels.
 template <int RB, int TN, int WM, int WN>
 __global__ __launch_bounds__(256, 1) void ffn_weight_grad(FfnGradParams p) {
-    typedef mt::Product<RB, TN, WM, WN, 1, true, true, true, true> P;
+    typedef mt::Product<RB, TN, WM, WN, 1, true, true, true, false> P;
     __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
     const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -283,7 +303,9 @@ __global__ __launch_bounds__(256, 1) void ffn_weight_grad(FfnGradParams p) {
                                (size_t)N * 2, min(P::BN, N - n0), rows};
         floatx4 acc[RB][TN];
         mt::clear(acc);
-        P::run(acc, a, b, slot0, slot1, (rows + mt::SK - 1) / mt::SK, wave, lane);
+        // whole pairs of stages: rows past the group's end are zeros
+        P::run(acc, a, b, slot0, slot1, (rows + 2 * mt::SK - 1) / (2 * mt::SK) * 2,
+               wave, lane);
         __builtin_amdgcn_s_waitcnt(0);
         __builtin_amdgcn_s_barrier();
         const int c0 = n0 + wn * TN * 16;
@@ -322,24 +344,39 @@ template <int RB, int TN, int WM, int WN, int ACT>
 void act_as(const FfnGradParams &p, hipStream_t s) {
     const int grid = grid_for(ffn_row_tiles(p, RB * 16 * WM) *
                               ((p.d_ff + TN * 16 * WN - 1) / (TN * 16 * WN)));
-    hipLaunchKernelGGL((ffn_act_grad<RB, TN, WM, WN, ACT>), dim3(grid), dim3(256), 0, s, p);
+    if (p.d / mt::SK & 1)
+        hipLaunchKernelGGL((ffn_act_grad<RB, TN, WM, WN, ACT, true>), dim3(grid), dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((ffn_act_grad<RB, TN, WM, WN, ACT, false>), dim3(grid), dim3(256), 0, s, p);
+}
+
+template <int RB, int TN, int WM, int WN, bool Q>
+void rows_as(const FfnGradParams &p, hipStream_t s) {
+    const int N = Q ? p.d_ff : p.d, bn = TN * 16 * WN;
+    const int grid = grid_for(ffn_row_tiles(p, RB * 16 * WM) * ((N + bn - 1) / bn));
+    if ((Q ? p.d : p.d_ff) / mt::SK & 1)
+        hipLaunchKernelGGL((ffn_rows_by_weights<RB, TN, WM, WN, Q, true>), dim3(grid), dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((ffn_rows_by_weights<RB, TN, WM, WN, Q, false>), dim3(grid), dim3(256), 0, s, p);
 }
 
 }  // namespace
 
-// 64 columns per wave in every form.
-int mfma_dw_tiles(int d_ff) { return d_ff / 64; }
+// Columns of a wave's tile: 64 gated, 128 else.
+int mfma_dw_tiles(int d_ff, int act) {
+    return act == ACT_SWIGLU ? d_ff / 64 : (d_ff + 127) / 128;
+}
 
 hipError_t launch_act_grad_mfma(const FfnGradParams &p, hipStream_t s) {
-    if (p.act == ACT_GELU) act_as<8, 4, 2, 2, ACT_GELU>(p, s);
-    else if (p.act == ACT_SILU) act_as<8, 4, 2, 2, ACT_SILU>(p, s);
-    else act_as<6, 4, 2, 2, ACT_SWIGLU>(p, s);
+    rows_as<8, 8, 2, 2, true>(p, s);
+    if (p.act == ACT_GELU) act_as<8, 8, 2, 2, ACT_GELU>(p, s);
+    else if (p.act == ACT_SILU) act_as<8, 8, 2, 2, ACT_SILU>(p, s);
+    else act_as<8, 4, 2, 2, ACT_SWIGLU>(p, s);
     return hipGetLastError();
 }
 
 hipError_t launch_row_grad_mfma(const FfnGradParams &p, hipStream_t s) {
-    const int grid = grid_for(ffn_row_tiles(p, 256) * ((p.d + 255) / 256));
-    hipLaunchKernelGGL((ffn_row_grad<8, 8, 2, 2>), dim3(grid), dim3(256), 0, s, p);
+    rows_as<8, 8, 2, 2, false>(p, s);
     return hipGetLastError();
 }
 

@@ -45,6 +45,7 @@ struct FfnGradParams {
     // h times the row weight, and the gradients of the pre-activations,
     // [rows][d_ff] each (du: SwiGLU)
     void *h, *dz, *du;
+    float *q;                 // bf16: [rows][d_ff], dy W2
     float *dw_part;           // [rows][dw_tiles]: <dy W2, h> by column tile
     int dw_tiles;
     float *dxs;               // [rows][d] fp32
@@ -54,7 +55,7 @@ struct FfnGradParams {
     int rows;                 // shared_base + n_shared * T
 };
 // Column tiles that launch_ffn_act_grad writes to dw_part.
-int ffn_grad_dw_tiles(int dtype, int d_ff);
+int ffn_grad_dw_tiles(int dtype, int d_ff, int act);
 hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype, hipStream_t s);
 hipError_t launch_ffn_row_grad(const FfnGradParams &p, int dtype, hipStream_t s);
 hipError_t launch_ffn_weight_grad(const FfnGradParams &p, int dtype, hipStream_t s);

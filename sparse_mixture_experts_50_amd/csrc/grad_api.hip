@@ -11,7 +11,7 @@ using namespace moe_host;
 struct GradLayout {
     // the router's part, then the experts'
     size_t logits, dl, db_part, wr_part, router_total;
-    size_t row_w, xs, dys, h, dz, du, dw_part, dxs, total;
+    size_t row_w, xs, dys, h, dz, du, q, dw_part, dxs, total;
     size_t rows;
     int ep, splits, dw_tiles;
 };
@@ -35,13 +35,14 @@ GradLayout layout(const moe_desc *d) {
     L.router_total = off > 0 ? off : kAlign;
     L.rows = (size_t)routed_rows(d) + (size_t)d->n_shared * d->T;
     // column tiles of <dy W2, h>, and <dy, b2>
-    L.dw_tiles = ffn_grad_dw_tiles(d->dtype, d->d_ff);
+    L.dw_tiles = ffn_grad_dw_tiles(d->dtype, d->d_ff, d->activation);
     L.row_w = take(L.rows * 4);
     L.xs = take(L.rows * d->d * es);
     L.dys = take(L.rows * d->d * es);
     L.h = take(L.rows * d->d_ff * es);
     L.dz = take(L.rows * d->d_ff * es);
     L.du = take(d->activation == MOE_ACT_SWIGLU ? L.rows * d->d_ff * es : 0);
+    L.q = take(d->dtype == MOE_BF16 ? L.rows * d->d_ff * 4 : 0);
     L.dw_part = take(L.rows * (L.dw_tiles + 1) * 4);
     L.dxs = take(L.rows * d->d * 4);
     L.total = off > 0 ? off : kAlign;
@@ -293,6 +294,7 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
     p.h = at(ws, L.h);
     p.dz = at(ws, L.dz);
     p.du = at(ws, L.du);
+    p.q = (float *)at(ws, L.q);
     p.dw_part = (float *)at(ws, L.dw_part);
     p.dw_tiles = L.dw_tiles + (p.b2 || p.bs2 ? 1 : 0);
     p.dxs = (float *)at(ws, L.dxs);

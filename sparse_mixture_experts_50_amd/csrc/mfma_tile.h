@@ -39,13 +39,8 @@ template <int N> __device__ __forceinline__ void wait_vmcnt() {
     __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
 
-// AG: accumulator in AGPRs (else VGPRs).
-template <bool AG>
 __device__ __forceinline__ void mfma(floatx4 &acc, const bf16x8 &a, const bf16x8 &b) {
-    if (AG)
-        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
-    else
-        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(a), "v"(b));
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 
 // A zeroed line that lanes past the end of a K_FIRST operand read from.
@@ -166,7 +161,7 @@ struct Side {
 
 // A tile of WM x WN waves of RB x TN 16 x 16 blocks (times B's PANELS).
 template <int RB, int TN, int WM, int WN, int PANELS, bool AF, bool BF, bool ZK,
-          bool AG>
+          bool ODD>
 struct Product {
     static_assert(WM * WN == 4, "four waves");
     static constexpr int BM = RB * 16 * WM, BN = TN * 16 * WN;
@@ -234,7 +229,7 @@ struct Product {
             __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
 #pragma unroll
             for (int q = 0; q < NM; ++q) {
-                mfma<AG>(acc[q / NC][q % NC], fb0[q % NC], fa0[q / NC]);
+                mfma(acc[q / NC][q % NC], fb0[q % NC], fa0[q / NC]);
 #pragma unroll
                 for (int u = 0; u < MAXR; ++u)
                     if (first(q, NR, RSPAN) + u < first(q + 1, NR, RSPAN))
@@ -246,7 +241,7 @@ struct Product {
             const int nx = min(s + 2, KT - 1);
 #pragma unroll
             for (int q = 0; q < NM; ++q) {
-                mfma<AG>(acc[q / NC][q % NC], fb1[q % NC], fa1[q / NC]);
+                mfma(acc[q / NC][q % NC], fb1[q % NC], fa1[q / NC]);
 #pragma unroll
                 for (int u = 0; u < MAXR; ++u)
                     if (first(q, NR, RSPAN) + u < first(q + 1, NR, RSPAN))
@@ -260,10 +255,12 @@ struct Product {
         // wait states that the compiler does not know the asm needs: before
         // the first MFMA (a VALU write of its accumulator) and after the
         // last (a read of its result)
+        // ODD: KT may be odd.  (A way round the loop that skips a stage
+        // leaves loads into slot0 to be waited for at its head.)
         for (int s = 0; s < KT; s += 2) {
             asm volatile("s_nop 4");
             stage(s, slot0, slot1);
-            if (s + 1 < KT) stage(s + 1, slot1, slot0);
+            if (!ODD || s + 1 < KT) stage(s + 1, slot1, slot0);
             asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7");
         }
     }
