@@ -16,7 +16,7 @@
 // computed again from x (2 or 4 d d_ff operations a row) instead of being
 // kept by the forward (4 or 8 bytes a value, written and read).
 #include "ffn_grad.h"
-#include "simt.h"
+#include "f32_tile.h"
 
 namespace {
 
@@ -57,131 +57,131 @@ __device__ __forceinline__ bool row_tile(const TileTable &tt, int G, int L,
     const int local = L - tt.base[r.g], mt = tt.mt[r.g];
     r.n_tile = local / mt;
     const int m = local - r.n_tile * mt;
-    r.row0 = tt.start[r.g] + m * simt::BM;
-    r.nrows = min(simt::BM, tt.rows[r.g] - m * simt::BM);
+    r.row0 = tt.start[r.g] + m * f32t::BM;
+    r.nrows = min(f32t::BM, tt.rows[r.g] - m * f32t::BM);
     return true;
 }
 
-template <typename T, int ACT>
-__global__ __launch_bounds__(256) void ffn_act_grad_simt(FfnGradParams p) {
-    __shared__ simt::Stage st;
+template <int ACT>
+__global__ __launch_bounds__(256) void ffn_act_grad_f32(FfnGradParams p) {
+    __shared__ f32t::Stage st;
     __shared__ TileTable tt;
     const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
     build_tile_table(tt, p.offsets, p.E, p.n_shared, p.shared_base, p.T,
-                     simt::BM, F / simt::BN);
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+                     f32t::BM, F / f32t::BN);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     RowTile r;
     for (int L = blockIdx.x; row_tile(tt, G, L, r); L += gridDim.x) {
-        const int n0 = r.n_tile * simt::BN;
-        const T *x = (const T *)p.xs + (size_t)r.row0 * d;
-        const T *dy = (const T *)p.dys + (size_t)r.row0 * d;
+        const int n0 = r.n_tile * f32t::BN;
+        const float *x = (const float *)p.xs + (size_t)r.row0 * d;
+        const float *dy = (const float *)p.dys + (size_t)r.row0 * d;
         const size_t mat = (size_t)F * d;
-        const T *w1 = of_group<T>(p.w1, p.ws1, r.g, p.E, mat);
-        const T *w2 = of_group<T>(p.w2, p.ws2, r.g, p.E, mat);
-        float z[4][4], u[4][4], q[4][4];
-        simt::clear(z);
-        simt::clear(u);
-        simt::clear(q);
-        simt::product<true, true>(z, st, x, d, r.nrows, w1 + (size_t)n0 * d, d,
-                                  simt::BN, d);
+        const float *w1 = of_group<float>(p.w1, p.ws1, r.g, p.E, mat);
+        const float *w2 = of_group<float>(p.w2, p.ws2, r.g, p.E, mat);
+        f32t::Acc z, u, q;
+        f32t::clear(z);
+        f32t::clear(u);
+        f32t::clear(q);
+        f32t::product<true, true>(z, st, x, d, r.nrows, w1 + (size_t)n0 * d, d,
+                                  f32t::BN, d);
         if (ACT == ACT_SWIGLU) {
-            const T *w3 = of_group<T>(p.w3, p.ws3, r.g, p.E, mat);
-            simt::product<true, true>(u, st, x, d, r.nrows,
-                                      w3 + (size_t)n0 * d, d, simt::BN, d);
+            const float *w3 = of_group<float>(p.w3, p.ws3, r.g, p.E, mat);
+            f32t::product<true, true>(u, st, x, d, r.nrows, w3 + (size_t)n0 * d, d,
+                                      f32t::BN, d);
         }
-        simt::product<true, false>(q, st, dy, d, r.nrows, w2 + n0, F, d, d);
-        const T *b1 = of_group<T>(p.b1, p.bs1, r.g, p.E, F);
-        const T *b3 = of_group<T>(p.b3, p.bs3, r.g, p.E, F);
-        const int c = n0 + tx * 4;
+        f32t::product<true, false>(q, st, dy, d, r.nrows, w2 + n0, F, d, d);
+        const float *b1 = of_group<float>(p.b1, p.bs1, r.g, p.E, F);
+        const float *b3 = of_group<float>(p.b3, p.bs3, r.g, p.E, F);
+        const int c0 = n0 + (wave & 1) * 32;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = ty * 4 + i;
+        for (int i = 0; i < 2; ++i) {
+            const int m = (wave >> 1) * 32 + 16 * i + (lane & 15);
             const bool live = m < r.nrows;
             const int row = r.row0 + m;
             const float w = live ? p.row_w[row] : 0.0f;
-            float vh[4], vz[4], vu[4], dot = 0.0f;
+            float dot = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float h, hz, hu;
-                const float zz = z[i][j] + (b1 ? simt::load1(b1 + c + j) : 0.0f);
-                const float uu = u[i][j] + (b3 ? simt::load1(b3 + c + j) : 0.0f);
-                act_grad<ACT>(zz, uu, h, hz, hu);
-                dot = fmaf(q[i][j], h, dot);
-                const float wq = w * q[i][j];
-                vh[j] = w * h;
-                vz[j] = wq * hz;
-                vu[j] = wq * hu;
+            for (int j = 0; j < 2; ++j) {
+                const int c = c0 + 16 * j + 4 * (lane >> 4);
+                floatx4 vh, vz, vu;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float h, hz, hu;
+                    act_grad<ACT>(z[i][j][e] + (b1 ? b1[c + e] : 0.0f),
+                                  u[i][j][e] + (b3 ? b3[c + e] : 0.0f), h, hz, hu);
+                    dot = fmaf(q[i][j][e], h, dot);
+                    const float wq = w * q[i][j][e];
+                    vh[e] = w * h;
+                    vz[e] = wq * hz;
+                    vu[e] = wq * hu;
+                }
+                if (!live) continue;
+                const size_t at = (size_t)row * F + c;
+                *(floatx4 *)((float *)p.h + at) = vh;
+                *(floatx4 *)((float *)p.dz + at) = vz;
+                if (ACT == ACT_SWIGLU) *(floatx4 *)((float *)p.du + at) = vu;
             }
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) dot += __shfl_xor(dot, o, 64);
-            if (!live) continue;
-            const size_t at = (size_t)row * F + c;
-            simt::store4((T *)p.h + at, vh);
-            simt::store4((T *)p.dz + at, vz);
-            if (ACT == ACT_SWIGLU) simt::store4((T *)p.du + at, vu);
-            if (tx == 0) p.dw_part[(size_t)row * p.dw_tiles + r.n_tile] = dot;
+            dot += __shfl_xor(dot, 16, 64);
+            dot += __shfl_xor(dot, 32, 64);
+            if (live && lane < 16) p.dw_part[(size_t)row * p.dw_tiles + c0 / 32] = dot;
         }
     }
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void ffn_row_grad_simt(FfnGradParams p) {
-    __shared__ simt::Stage st;
+__global__ __launch_bounds__(256) void ffn_row_grad_f32(FfnGradParams p) {
+    __shared__ f32t::Stage st;
     __shared__ TileTable tt;
     const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
     build_tile_table(tt, p.offsets, p.E, p.n_shared, p.shared_base, p.T,
-                     simt::BM, d / simt::BN);
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+                     f32t::BM, d / f32t::BN);
     RowTile r;
     for (int L = blockIdx.x; row_tile(tt, G, L, r); L += gridDim.x) {
-        const int n0 = r.n_tile * simt::BN;
+        const int n0 = r.n_tile * f32t::BN;
         const size_t mat = (size_t)F * d, at = (size_t)r.row0 * F;
-        float acc[4][4];
-        simt::clear(acc);
-        simt::product<true, false>(
-            acc, st, (const T *)p.dz + at, F, r.nrows,
-            of_group<T>(p.w1, p.ws1, r.g, p.E, mat) + n0, d, F, F);
+        f32t::Acc acc;
+        f32t::clear(acc);
+        f32t::product<true, false>(acc, st, (const float *)p.dz + at, F, r.nrows,
+                                   of_group<float>(p.w1, p.ws1, r.g, p.E, mat) + n0, d,
+                                   F, F);
         if (p.act == ACT_SWIGLU)
-            simt::product<true, false>(
-                acc, st, (const T *)p.du + at, F, r.nrows,
-                of_group<T>(p.w3, p.ws3, r.g, p.E, mat) + n0, d, F, F);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = ty * 4 + i;
-            if (m < r.nrows)
-                simt::store4(p.dxs + (size_t)(r.row0 + m) * d + n0 + tx * 4, acc[i]);
-        }
+            f32t::product<true, false>(acc, st, (const float *)p.du + at, F, r.nrows,
+                                       of_group<float>(p.w3, p.ws3, r.g, p.E, mat) + n0,
+                                       d, F, F);
+        f32t::each(acc, [&](int m, int c, floatx4 v) {
+            if (m < r.nrows) *(floatx4 *)(p.dxs + (size_t)(r.row0 + m) * d + n0 + c) = v;
+        });
     }
 }
 
 // dW[m][n] = sum over the group's rows s of L[s][m] R[s][n]; blockIdx.z:
 // dW1 (dz, x), dW2 (dy, r h), dW3 (du, x).  A group without rows gets
 // zeros.
-template <typename T>
-__global__ __launch_bounds__(256) void ffn_weight_grad_simt(FfnGradParams p) {
-    __shared__ simt::Stage st;
+__global__ __launch_bounds__(256) void ffn_weight_grad_f32(FfnGradParams p) {
+    __shared__ f32t::Stage st;
     const int g = blockIdx.y, which = blockIdx.z, d = p.d, F = p.d_ff;
     const int M = which == 1 ? d : F, N = which == 1 ? F : d;
     const size_t mat = (size_t)F * d;
-    T *out = which == 0 ? of_group<T>(p.g_w1, p.g_ws1, g, p.E, mat)
-             : which == 1 ? of_group<T>(p.g_w2, p.g_ws2, g, p.E, mat)
-                          : of_group<T>(p.g_w3, p.g_ws3, g, p.E, mat);
+    float *out = which == 0 ? of_group<float>(p.g_w1, p.g_ws1, g, p.E, mat)
+                 : which == 1 ? of_group<float>(p.g_w2, p.g_ws2, g, p.E, mat)
+                              : of_group<float>(p.g_w3, p.g_ws3, g, p.E, mat);
     if (!out) return;
-    const int m0 = blockIdx.x / (N / simt::BN) * simt::BM;
-    const int n0 = blockIdx.x % (N / simt::BN) * simt::BN;
+    const int m0 = blockIdx.x / (N / f32t::BN) * f32t::BM;
+    const int n0 = blockIdx.x % (N / f32t::BN) * f32t::BN;
     int start, rows;
     group_rows(p, g, start, rows);
-    const T *L = (const T *)(which == 0 ? p.dz : which == 1 ? p.dys : p.du);
-    const T *R = (const T *)(which == 1 ? p.h : p.xs);
-    float acc[4][4];
-    simt::clear(acc);
-    simt::product<false, false>(acc, st, L + (size_t)start * M + m0, M, rows,
+    const float *L = (const float *)(which == 0 ? p.dz : which == 1 ? p.dys : p.du);
+    const float *R = (const float *)(which == 1 ? p.h : p.xs);
+    f32t::Acc acc;
+    f32t::clear(acc);
+    f32t::product<false, false>(acc, st, L + (size_t)start * M + m0, M, rows,
                                 R + (size_t)start * N + n0, N, rows, rows);
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        simt::store4(out + (size_t)(m0 + ty * 4 + i) * N + n0 + tx * 4, acc[i]);
+    f32t::each(acc, [&](int m, int c, floatx4 v) {
+        *(floatx4 *)(out + (size_t)(m0 + m) * N + n0 + c) = v;
+    });
 }
+
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t *p) { return bf16_to_f32(*p); }
 
 // Column sums over a group's rows; blockIdx.z: db1 (dz), db2 (r dy), db3
 // (du).  64 columns per block, 16 row lanes added in order.
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(1024) void ffn_bias_grad(FfnGradParams p) {
     float sum = 0.0f;
 #pragma unroll 4
     for (int s = rl; s < rows; s += 16) {
-        const float v = simt::load1(src + (size_t)s * n);
+        const float v = load1(src + (size_t)s * n);
         sum = which == 1 ? fmaf(p.row_w[start + s], v, sum) : sum + v;
     }
     part[rl][lane] = sum;
@@ -232,8 +232,8 @@ __global__ __launch_bounds__(256) void ffn_bias_dot(FfnGradParams p) {
         float dot = 0.0f;
         if (b2)
             for (int c = lane; c < p.d; c += 64)
-                dot = fmaf(simt::load1((const T *)p.dys + (size_t)row * p.d + c),
-                           simt::load1(b2 + c), dot);
+                dot = fmaf(load1((const T *)p.dys + (size_t)row * p.d + c),
+                           load1(b2 + c), dot);
         dot = wave_sum(dot);
         if (lane == 0) p.dw_part[(size_t)row * p.dw_tiles + p.dw_tiles - 1] = dot;
     }
@@ -244,21 +244,20 @@ int row_tiles(const FfnGradParams &p, int bm, int ncols) {
     return (int)(n < 65536 ? n : 65536);
 }
 
-template <typename T>
-void act_grad_simt(const FfnGradParams &p, hipStream_t s) {
-    const dim3 grid(row_tiles(p, simt::BM, p.d_ff / simt::BN)), block(256);
+void act_grad_f32(const FfnGradParams &p, hipStream_t s) {
+    const dim3 grid(row_tiles(p, f32t::BM, p.d_ff / f32t::BN)), block(256);
     if (p.act == ACT_GELU)
-        hipLaunchKernelGGL((ffn_act_grad_simt<T, ACT_GELU>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((ffn_act_grad_f32<ACT_GELU>), grid, block, 0, s, p);
     else if (p.act == ACT_SILU)
-        hipLaunchKernelGGL((ffn_act_grad_simt<T, ACT_SILU>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((ffn_act_grad_f32<ACT_SILU>), grid, block, 0, s, p);
     else
-        hipLaunchKernelGGL((ffn_act_grad_simt<T, ACT_SWIGLU>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((ffn_act_grad_f32<ACT_SWIGLU>), grid, block, 0, s, p);
 }
 
 }  // namespace
 
 int ffn_grad_dw_tiles(int dtype, int d_ff, int act) {
-    return dtype == 1 ? mfma_dw_tiles(d_ff, act) : d_ff / simt::BN;
+    return dtype == 1 ? mfma_dw_tiles(d_ff, act) : d_ff / 32;
 }
 
 hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype,
@@ -271,24 +270,24 @@ hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype,
             hipLaunchKernelGGL((ffn_bias_dot<float>), grid, dim3(256), 0, s, p);
     }
     if (dtype == 1) return launch_act_grad_mfma(p, s);
-    act_grad_simt<float>(p, s);
+    act_grad_f32(p, s);
     return hipGetLastError();
 }
 
 hipError_t launch_ffn_row_grad(const FfnGradParams &p, int dtype,
                                hipStream_t s) {
     if (dtype == 1) return launch_row_grad_mfma(p, s);
-    const dim3 grid(row_tiles(p, simt::BM, p.d / simt::BN));
-    hipLaunchKernelGGL((ffn_row_grad_simt<float>), grid, dim3(256), 0, s, p);
+    const dim3 grid(row_tiles(p, f32t::BM, p.d / f32t::BN));
+    hipLaunchKernelGGL(ffn_row_grad_f32, grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
 hipError_t launch_ffn_weight_grad(const FfnGradParams &p, int dtype,
                                   hipStream_t s) {
     if (dtype == 1) return launch_weight_grad_mfma(p, s);
-    const dim3 grid(p.d / simt::BM * (p.d_ff / simt::BN), p.E + p.n_shared,
+    const dim3 grid(p.d / f32t::BM * (p.d_ff / f32t::BN), p.E + p.n_shared,
                     p.act == ACT_SWIGLU ? 3 : 2);
-    hipLaunchKernelGGL((ffn_weight_grad_simt<float>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL(ffn_weight_grad_f32, grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 

@@ -72,8 +72,11 @@ struct RouterGradParams {
     const float *dw;          // [T][k], or null: from the row partials
     const float *dw_part;     // [rows][dw_tiles]
     int dw_tiles;
-    float *logits;            // [T][ep] (where the losses need them)
-    float *dl;                // [T][ep], columns E.. zero
+    // logits without the biases (where the losses need them): logit_splits
+    // partial sums [T][E] over depth ranges of logit_depth
+    float *logits;
+    int logit_splits, logit_depth;
+    void *dl;                 // [T][ep] in the layer's type, columns E.. zero
     float *db_part;           // [ceil(T / MOE_ROUTER_GRAD_TOKENS)][E]
     float *wr_part;           // [splits][E][d]
     int splits;
@@ -88,7 +91,11 @@ struct RouterGradParams {
 // Tokens of one partial sum of the bias gradient.
 #define MOE_ROUTER_GRAD_TOKENS 32
 // Token ranges that the router weight gradient is split into.
-int router_grad_splits(int T, int d, int E);
+int router_grad_splits(int dtype, int T, int d, int E);
+// The forward's split bf16 router alone: partial logits of p.S ranges into
+// p.part (router.hip).
+struct RouterParams;
+hipError_t launch_router_logits(const RouterParams &p, hipStream_t s);
 hipError_t launch_router_grad(const RouterGradParams &p, int dtype, hipStream_t s);
 
 // Zero bytes [0, n) (n a multiple of 2) with a kernel.

@@ -14,6 +14,7 @@ struct GradLayout {
     size_t row_w, xs, dys, h, dz, du, q, dw_part, dxs, total;
     size_t rows;
     int ep, splits, dw_tiles;
+    RouterPlan logit_plan;
 };
 
 GradLayout layout(const moe_desc *d) {
@@ -26,9 +27,11 @@ GradLayout layout(const moe_desc *d) {
         return at;
     };
     L.ep = (d->E + 63) / 64 * 64;
-    L.splits = router_grad_splits(d->T, d->d, d->E);
-    L.logits = take((size_t)d->T * L.ep * 4);
-    L.dl = take((size_t)d->T * L.ep * 4);
+    L.splits = router_grad_splits(d->dtype, d->T, d->d, d->E);
+    L.logit_plan = router_plan(d->T, d->d, d->E, 256);
+    if (d->dtype == MOE_F32) L.logit_plan.S = 1;
+    L.logits = take((size_t)L.logit_plan.S * d->T * d->E * 4);
+    L.dl = take((size_t)d->T * L.ep * es);
     L.db_part = take((size_t)((d->T + MOE_ROUTER_GRAD_TOKENS - 1) /
                               MOE_ROUTER_GRAD_TOKENS) * d->E * 4);
     L.wr_part = take(L.splits > 1 ? (size_t)L.splits * d->E * d->d * 4 : 0);
@@ -67,6 +70,26 @@ bool have_rows(const moe_desc *d) {
     return routed_rows(d) + (long long)d->n_shared * d->T > 0;
 }
 
+// Vectors of 16 bytes are moved: operands are aligned to them.
+template <typename... P> bool aligned(const P *...p) {
+    return ((((uintptr_t)p & 15) == 0) && ...);
+}
+bool aligned_weights(const moe_weights *w) {
+    return aligned(w->w_router, w->w1, w->w2, w->w3, w->ws1, w->ws2, w->ws3, w->b1,
+                   w->b2, w->b3, w->bs1, w->bs2, w->bs3);
+}
+bool aligned_grads(const moe_grads *g) {
+    return aligned(g->x, g->w_router, g->w1, g->w2, g->w3, g->ws1, g->ws2, g->ws3,
+                   g->b1, g->b2, g->b3, g->bs1, g->bs2, g->bs3);
+}
+
+// The gradient's kernels hold row offsets within a tile in 32 bits.
+int check_grad_desc(const moe_desc *d) {
+    const int st = check_desc(d);
+    if (st != MOE_OK) return st;
+    return d->d > (1 << 20) || d->d_ff > (1 << 20) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
 int check_router(const moe_desc *d, const moe_weights *w,
                  const moe_routing *r, float aux_scale) {
     if (!w || !w->w_router || !r || !r->topk_w || !r->slot_of ||
@@ -90,7 +113,9 @@ RouterGradParams router_params(const moe_desc *d, const void *x,
     p.slot_of = r->slot_of;
     p.f = r->f;
     p.logits = (float *)at(ws, L.logits);
-    p.dl = (float *)at(ws, L.dl);
+    p.logit_splits = L.logit_plan.S;
+    p.logit_depth = L.logit_plan.kc;
+    p.dl = at(ws, L.dl);
     p.db_part = (float *)at(ws, L.db_part);
     p.wr_part = (float *)at(ws, L.wr_part);
     p.splits = L.splits;
@@ -158,7 +183,7 @@ int moe_dispatch_rows(const moe_desc *desc, const moe_routing *r,
     int st = check_desc(desc);
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
-    if (!x || !r || !r->slot_of || (!xs && have_rows(desc)))
+    if (!x || !r || !r->slot_of || (!xs && have_rows(desc)) || !aligned(x, xs))
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.tok = x;
@@ -171,7 +196,7 @@ int moe_dispatch_rows_grad(const moe_desc *desc, const moe_routing *r,
     int st = check_desc(desc);
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
-    if (!dx || !r || !r->slot_of || (!dxs && have_rows(desc)))
+    if (!dx || !r || !r->slot_of || (!dxs && have_rows(desc)) || !aligned(dx, dxs))
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.rows_in = dxs;
@@ -184,7 +209,8 @@ int moe_combine_rows(const moe_desc *desc, const moe_routing *r,
     int st = check_desc(desc);
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
-    if (!y || !r || !r->slot_of || !r->topk_w || (!ys && have_rows(desc)))
+    if (!y || !r || !r->slot_of || !r->topk_w || (!ys && have_rows(desc)) ||
+        !aligned(y, ys))
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.rows_in = ys;
@@ -199,7 +225,7 @@ int moe_combine_rows_grad(const moe_desc *desc, const moe_routing *r,
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
     if (!dy || !dw || !r || !r->slot_of || !r->topk_w ||
-        ((!ys || !dys) && have_rows(desc)))
+        ((!ys || !dys) && have_rows(desc)) || !aligned(dy, ys, dys))
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.tok = dy;
@@ -210,12 +236,12 @@ int moe_combine_rows_grad(const moe_desc *desc, const moe_routing *r,
 }
 
 size_t moe_router_grad_workspace_size(const moe_desc *desc) {
-    if (check_desc(desc) != MOE_OK) return 0;
+    if (check_grad_desc(desc) != MOE_OK) return 0;
     return layout(desc).router_total;
 }
 
 size_t moe_grad_workspace_size(const moe_desc *desc) {
-    if (check_desc(desc) != MOE_OK || desc->expert_fp8) return 0;
+    if (check_grad_desc(desc) != MOE_OK || desc->expert_fp8) return 0;
     return layout(desc).total;
 }
 
@@ -223,7 +249,7 @@ int moe_router_grad(const moe_desc *desc, const void *x, const moe_weights *w,
                     const moe_routing *r, const float *dw, const void *dx_add,
                     float aux_scale, float z_scale, const moe_grads *g,
                     void *ws, size_t ws_bytes, void *stream) {
-    int st = check_desc(desc);
+    int st = check_grad_desc(desc);
     if (st != MOE_OK) return st;
     if (!g) return MOE_ERR_INVALID_ARG;
     if (desc->T == 0) {
@@ -234,8 +260,9 @@ int moe_router_grad(const moe_desc *desc, const void *x, const moe_weights *w,
     }
     if (!x || !dw) return MOE_ERR_INVALID_ARG;
     if ((st = check_router(desc, w, r, aux_scale)) != MOE_OK) return st;
+    if (!aligned(x, dx_add, w->w_router, g->x, g->w_router)) return MOE_ERR_INVALID_ARG;
     const GradLayout L = layout(desc);
-    if (!ws || ws_bytes < L.router_total) return MOE_ERR_WORKSPACE;
+    if (!ws || ws_bytes < L.router_total || !aligned(ws)) return MOE_ERR_WORKSPACE;
     RouterGradParams p =
         router_params(desc, x, w, r, aux_scale, z_scale, g, ws, L);
     p.dw = dw;
@@ -247,7 +274,7 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
                  const moe_routing *r, const void *dy, float aux_scale,
                  float z_scale, const moe_grads *g, void *ws, size_t ws_bytes,
                  void *stream) {
-    int st = check_desc(desc);
+    int st = check_grad_desc(desc);
     if (st != MOE_OK) return st;
     if (desc->expert_fp8) return MOE_ERR_UNSUPPORTED;
     if (!g) return MOE_ERR_INVALID_ARG;
@@ -256,8 +283,10 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
     if (!x || !dy) return MOE_ERR_INVALID_ARG;
     if ((st = check_router(desc, w, r, aux_scale)) != MOE_OK) return st;
     if ((st = check_ffn(desc, w, r)) != MOE_OK) return st;
+    if (!aligned(x, dy) || !aligned_weights(w) || !aligned_grads(g))
+        return MOE_ERR_INVALID_ARG;
     const GradLayout L = layout(desc);
-    if (!ws || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    if (!ws || ws_bytes < L.total || !aligned(ws)) return MOE_ERR_WORKSPACE;
 
     RowsParams rp = rows_params(desc, r);
     rp.tok = x;

@@ -24,6 +24,7 @@
 // its slot row to -1, and the block writes its logits transposed to [E][T]
 // (32 consecutive tokens per expert row), the layout in which each expert
 // later ranks its column.
+#include "grad.h"
 #include "kernels.h"
 #include "permute_block.h"
 
@@ -734,6 +735,19 @@ RouterPlan router_plan(int T, int d, int E, int cus) {
     return r;
 }
 
+hipError_t launch_router_logits(const RouterParams &p, hipStream_t s) {
+    const int EP = p.E <= 32 ? 32 : p.E <= 64 ? 64 : p.E <= 128 ? 128 : 256;
+    const int tokens = EP <= 64 ? 32 : 128;
+    const dim3 lgrid((p.T + tokens - 1) / tokens, p.S);
+    switch (EP) {
+    case 32: hipLaunchKernelGGL(router_logits<32>, lgrid, dim3(256), 0, s, p); break;
+    case 64: hipLaunchKernelGGL(router_logits<64>, lgrid, dim3(256), 0, s, p); break;
+    case 128: hipLaunchKernelGGL((router_logits_lds<128, 1>), lgrid, dim3(256), 0, s, p); break;
+    default: hipLaunchKernelGGL((router_logits_lds<256, 1>), lgrid, dim3(256), 0, s, p); break;
+    }
+    return hipGetLastError();
+}
+
 hipError_t launch_router(const RouterParams &p, int dtype, hipStream_t s) {
     const int blocks = (p.T + RT - 1) / RT;
     const dim3 grid(blocks), block(RW * 64);
@@ -748,25 +762,13 @@ hipError_t launch_router(const RouterParams &p, int dtype, hipStream_t s) {
         return hipGetLastError();
     }
     if (dtype == 1) {
-        const int tokens = EP <= 64 ? 32 : 128;
-        const dim3 lgrid((p.T + tokens - 1) / tokens, p.S);
+        const hipError_t err = launch_router_logits(p, s);
+        if (err != hipSuccess) return err;
         switch (EP) {
-        case 32:
-            hipLaunchKernelGGL(router_logits<32>, lgrid, dim3(256), 0, s, p);
-            hipLaunchKernelGGL(router_route<32>, grid, dim3(256), 0, s, p);
-            break;
-        case 64:
-            hipLaunchKernelGGL(router_logits<64>, lgrid, dim3(256), 0, s, p);
-            hipLaunchKernelGGL(router_route<64>, grid, block, 0, s, p);
-            break;
-        case 128:
-            hipLaunchKernelGGL((router_logits_lds<128, 1>), lgrid, dim3(256), 0, s, p);
-            hipLaunchKernelGGL(router_route<128>, grid, block, 0, s, p);
-            break;
-        default:
-            hipLaunchKernelGGL((router_logits_lds<256, 1>), lgrid, dim3(256), 0, s, p);
-            hipLaunchKernelGGL(router_route<256>, grid, block, 0, s, p);
-            break;
+        case 32: hipLaunchKernelGGL(router_route<32>, grid, dim3(256), 0, s, p); break;
+        case 64: hipLaunchKernelGGL(router_route<64>, grid, block, 0, s, p); break;
+        case 128: hipLaunchKernelGGL(router_route<128>, grid, block, 0, s, p); break;
+        default: hipLaunchKernelGGL(router_route<256>, grid, block, 0, s, p); break;
         }
         return hipGetLastError();
     }

@@ -14,46 +14,45 @@
 // Without losses top-k routing needs no logits: dl depends on the k weights
 // alone.
 #include "grad.h"
-#include "simt.h"
+#include "kernels.h"
+#include "f32_tile.h"
+#include "mfma_tile.h"
 
 namespace {
 
-template <typename T>
-__global__ __launch_bounds__(256) void router_grad_logits(RouterGradParams p) {
-    __shared__ simt::Stage st;
-    const int t0 = blockIdx.x * simt::BM, e0 = blockIdx.y * simt::BN;
-    float acc[4][4];
-    simt::clear(acc);
-    simt::product<true, true>(acc, st, (const T *)p.x + (size_t)t0 * p.d, p.d,
-                              p.T - t0, (const T *)p.wr + (size_t)e0 * p.d,
-                              p.d, p.E - e0, p.d);
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = t0 + ty * 4 + i;
-        if (t >= p.T) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int e = e0 + tx * 4 + j;
-            if (e < p.E) {
-                acc[i][j] += p.add ? p.add[e] : 0.0f;
-                acc[i][j] -= p.sub ? p.sub[e] : 0.0f;
-            }
-        }
-        simt::store4(p.logits + (size_t)t * p.ep + e0 + tx * 4, acc[i]);
-    }
+__global__ __launch_bounds__(256) void router_grad_logits_f32(RouterGradParams p) {
+    __shared__ f32t::Stage st;
+    const int t0 = blockIdx.x * f32t::BM, e0 = blockIdx.y * f32t::BN;
+    f32t::Acc acc;
+    f32t::clear(acc);
+    f32t::product<true, true>(acc, st, (const float *)p.x + (size_t)t0 * p.d, p.d,
+                              p.T - t0, (const float *)p.wr + (size_t)e0 * p.d, p.d,
+                              p.E - e0, p.d);
+    f32t::each(acc, [&](int m, int c, floatx4 v) {
+        if (t0 + m >= p.T) return;
+        for (int e = 0; e < 4; ++e)
+            if (e0 + c + e < p.E)
+                p.logits[(size_t)(t0 + m) * p.E + e0 + c + e] = v[e];
+    });
 }
 
 __device__ __forceinline__ float lane_f(float v, int l) {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), l));
 }
 
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t *p, float v) {
+    *p = (uint16_t)f32_to_bf16_bits(v);
+}
+
 // A wave per token, experts lane + 64 i.  Each block also leaves the column
-// sums of its tokens for the bias gradient.
-template <bool CHOICE>
-__global__ __launch_bounds__(256) void router_grad_dlogits(RouterGradParams p) {
-    constexpr int NE = MOE_MAX_E / 64;
-    __shared__ float part[4][MOE_MAX_E];
+// sums of its tokens for the bias gradient (before dl is rounded to the
+// layer's type, which feeds its two products).  Sixteen waves for 32 tokens:
+// the kernel waits for a few dependent loads and reductions a token.
+template <typename T, bool CHOICE>
+__global__ __launch_bounds__(1024) void router_grad_dlogits(RouterGradParams p) {
+    constexpr int NE = MOE_MAX_E / 64, WAVES = 16;
+    __shared__ float part[WAVES][MOE_MAX_E];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const bool aux = p.aux != 0.0f, zl = p.z != 0.0f;
@@ -61,10 +60,28 @@ __global__ __launch_bounds__(256) void router_grad_dlogits(RouterGradParams p) {
     float db[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) db[i] = 0.0f;
-    for (int n = wave; n < MOE_ROUTER_GRAD_TOKENS; n += 4) {
+    for (int n = wave; n < MOE_ROUTER_GRAD_TOKENS; n += WAVES) {
         const int t = blockIdx.x * MOE_ROUTER_GRAD_TOKENS + n;
         if (t >= p.T) break;
         const size_t at = (size_t)t * p.k;
+        // the token's logits, summed over the depth ranges
+        float l[NE];
+        if (logits) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                const int e = lane + 64 * i;
+                l[i] = -INFINITY;
+                if (e < p.E) {
+                    const float *q = p.logits + (size_t)t * p.E + e;
+                    const size_t plane = (size_t)p.T * p.E;
+                    float a = q[0];
+                    for (int s = 1; s < p.logit_splits; ++s) a += q[s * plane];
+                    if (p.add) a += p.add[e];
+                    if (p.sub) a -= p.sub[e];
+                    l[i] = a;
+                }
+            }
+        }
         // gradient and weight of assignment lane + 64 i
         float dw[NE], w[NE];
 #pragma unroll
@@ -77,19 +94,32 @@ __global__ __launch_bounds__(256) void router_grad_dlogits(RouterGradParams p) {
             }
         }
         if (!p.dw) {
+            // four rows' partial sums in flight
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
                 const int j = lane + 64 * i;
                 const int s = j < p.k ? p.slot_of[at + j] : -1;
                 unsigned long long m = __ballot(s >= 0);
                 while (m) {
-                    const int l = __builtin_ctzll(m);
-                    m &= m - 1;
-                    const float *q = p.dw_part + (size_t)__builtin_amdgcn_readlane(s, l) * p.dw_tiles;
-                    float sum = 0.0f;
-                    for (int c = lane; c < p.dw_tiles; c += 64) sum += q[c];
-                    sum = wave_sum(sum);
-                    if (lane == l) dw[i] = sum;
+                    int who[4];
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float *q[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        who[u] = m ? __builtin_ctzll(m) : who[0];
+                        m &= m - 1;
+                        q[u] = p.dw_part +
+                               (size_t)__builtin_amdgcn_readlane(s, who[u]) * p.dw_tiles;
+                    }
+                    for (int c = lane; c < p.dw_tiles; c += 64) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) sum[u] += q[u][c];
+                    }
+#pragma unroll
+                    for (int u = 3; u >= 0; --u) {
+                        const float v = wave_sum(sum[u]);
+                        if (lane == who[u]) dw[i] = v;
+                    }
                 }
             }
         }
@@ -97,13 +127,9 @@ __global__ __launch_bounds__(256) void router_grad_dlogits(RouterGradParams p) {
 #pragma unroll
         for (int i = 0; i < NE; ++i) dl[i] = pe[i] = 0.0f;
         if (logits) {
-            const float *q = p.logits + (size_t)t * p.ep;
-            float l[NE], mx = -INFINITY, sum = 0.0f;
+            float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                l[i] = lane + 64 * i < p.E ? q[lane + 64 * i] : -INFINITY;
-                mx = fmaxf(mx, l[i]);
-            }
+            for (int i = 0; i < NE; ++i) mx = fmaxf(mx, l[i]);
             mx = wave_max(mx);
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
@@ -152,7 +178,7 @@ __global__ __launch_bounds__(256) void router_grad_dlogits(RouterGradParams p) {
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             const int e = lane + 64 * i;
-            if (e < p.ep) p.dl[(size_t)t * p.ep + e] = dl[i];
+            if (e < p.ep) store1((T *)p.dl + (size_t)t * p.ep + e, dl[i]);
             db[i] += dl[i];
         }
     }
@@ -161,9 +187,10 @@ __global__ __launch_bounds__(256) void router_grad_dlogits(RouterGradParams p) {
     for (int i = 0; i < NE; ++i) part[wave][lane + 64 * i] = db[i];
     __syncthreads();
     const int e = threadIdx.x;
-    if (e < p.E)
-        p.db_part[(size_t)blockIdx.x * p.E + e] =
-            (part[0][e] + part[1][e]) + (part[2][e] + part[3][e]);
+    if (e >= p.E) return;
+    float sum = part[0][e];
+    for (int i = 1; i < WAVES; ++i) sum += part[i][e];
+    p.db_part[(size_t)blockIdx.x * p.E + e] = sum;
 }
 
 // db[e]: the blocks' partial sums, 64 lanes in a fixed order.
@@ -176,69 +203,164 @@ __global__ __launch_bounds__(64) void router_grad_bias(RouterGradParams p) {
     if (threadIdx.x == 0) p.db[e] = sum;
 }
 
-// dx = dl Wr, plus what reaches the token through the experts: a given
-// [T][d] tensor, or the fp32 row gradients of its slots in j order and of
-// its shared row.
-template <typename T>
-__global__ __launch_bounds__(256) void router_grad_x(RouterGradParams p) {
-    __shared__ simt::Stage st;
-    const int t0 = blockIdx.x * simt::BM, c0 = blockIdx.y * simt::BN;
-    float acc[4][4];
-    simt::clear(acc);
-    simt::product<true, false>(acc, st, p.dl + (size_t)t0 * p.ep, p.ep,
-                               p.T - t0, (const T *)p.wr + c0, p.d, p.E, p.ep);
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+__device__ __forceinline__ floatx4 load4(const float *p) { return *(const floatx4 *)p; }
+__device__ __forceinline__ floatx4 load4(const uint16_t *p) {
+    const u32x2 q = *(const u32x2 *)p;
+    return floatx4{bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
+}
+__device__ __forceinline__ void store4(float *p, floatx4 v) { *(floatx4 *)p = v; }
+__device__ __forceinline__ void store4(uint16_t *p, floatx4 v) {
+    u32x2 q;
+    q.x = pack_bf16x2(v[0], v[1]);
+    q.y = pack_bf16x2(v[2], v[3]);
+    *(u32x2 *)p = q;
+}
+
+// What reaches token t through the experts, NB runs of 4 columns, 16
+// columns apart from c on: the fp32 row gradients of its slots in j order
+// and of its shared row, or a given [T][d] tensor.
+template <typename T, int NB>
+__device__ __forceinline__ void expert_part(const RouterGradParams &p, int t, int c,
+                                            floatx4 (&v)[NB]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = t0 + ty * 4 + i;
-        if (t >= p.T) continue;
-        const int c = c0 + tx * 4;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        auto add = [&](float4 q) __attribute__((always_inline)) {
-            v[0] += q.x;
-            v[1] += q.y;
-            v[2] += q.z;
-            v[3] += q.w;
-        };
-        if (p.dxs) {
-            for (int j = 0; j < p.k; ++j) {
-                const int s = p.slot_of[(size_t)t * p.k + j];
-                if (s >= 0) add(simt::load4(p.dxs + (size_t)s * p.d + c));
-            }
-            if (p.n_shared)
-                add(simt::load4(p.dxs + (size_t)(p.shared_base + t) * p.d + c));
+    for (int b = 0; b < NB; ++b) v[b] = floatx4{0.f, 0.f, 0.f, 0.f};
+    if (p.dxs) {
+        const int32_t *so = p.slot_of + (size_t)t * p.k;
+#pragma unroll 4
+        for (int j = 0; j < p.k; ++j) {
+            const int s = so[j];
+            if (s < 0) continue;
+            const float *q = p.dxs + (size_t)s * p.d + c;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) v[b] += load4(q + 16 * b);
         }
-        if (p.dx_add)
-            add(simt::load4((const T *)p.dx_add + (size_t)t * p.d + c));
+        if (p.n_shared) {
+            const float *q = p.dxs + (size_t)(p.shared_base + t) * p.d + c;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += acc[i][j];
-        simt::store4((T *)p.dx + (size_t)t * p.d + c, v);
+            for (int b = 0; b < NB; ++b) v[b] += load4(q + 16 * b);
+        }
+    }
+    if (p.dx_add) {
+        const T *q = (const T *)p.dx_add + (size_t)t * p.d + c;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) v[b] += load4(q + 16 * b);
     }
 }
 
+// dx = dl Wr + what comes through the experts, 64 tokens x 64 columns.
+__global__ __launch_bounds__(256) void router_grad_x_f32(RouterGradParams p) {
+    __shared__ f32t::Stage st;
+    const int t0 = blockIdx.x * f32t::BM, c0 = blockIdx.y * f32t::BN;
+    f32t::Acc acc;
+    f32t::clear(acc);
+    f32t::product<true, false>(acc, st, (const float *)p.dl + (size_t)t0 * p.ep, p.ep,
+                               p.T - t0, (const float *)p.wr + c0, p.d, p.E, p.ep);
+    f32t::each(acc, [&](int m, int c, floatx4 a) {
+        if (t0 + m >= p.T) return;
+        floatx4 v[1];
+        expert_part<float, 1>(p, t0 + m, c0 + c, v);
+        store4((float *)p.dx + (size_t)(t0 + m) * p.d + c0 + c, v[0] + a);
+    });
+}
+
+// The same for bf16 layers, 16 tokens per wave: dl's fragments straight from
+// memory, the router rows of the 64 columns staged in LDS (zeros past E) and
+// transposed on the way to the MFMAs.  The rows of dx through the experts,
+// k fp32 rows a token, are what takes its time.
+template <int KS>                              // 64-deep stages: ep / 64
+__global__ __launch_bounds__(256) void router_grad_x_bf16(RouterGradParams p) {
+    typedef mt::Side<true, 64, 1, 4, true> SB;
+    __shared__ u32x4 slot[KS * SB::UNITS];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t0 = blockIdx.x * 64 + wave * 16, c0 = blockIdx.y * 64;
+    SB b;
+    b.init({(const char *)((const uint16_t *)p.wr + c0), nullptr, (size_t)p.d * 2, 64, p.E},
+           wave, lane);
+    b.init_reads(0, 0, lane);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int q = 0; q < SB::LOADS; ++q) b.load(s, q, slot, s * SB::UNITS, wave);
+    const int t = t0 + (lane & 15);
+    const uint16_t *dl = (const uint16_t *)p.dl + (size_t)min(t, p.T - 1) * p.ep +
+                         8 * (lane >> 4);
+    bf16x8 fa[2 * KS];
+#pragma unroll
+    for (int k = 0; k < 2 * KS; ++k) fa[k] = as_bf16x8(*(const u32x4 *)(dl + 32 * k));
+    const int c = c0 + 4 * (lane >> 4);
+    floatx4 v[4];
+    expert_part<uint16_t, 4>(p, min(t, p.T - 1), c, v);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    floatx4 acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 2 * KS; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            bf16x8 fb = {};
+            b.read(fb, slot + (k >> 1) * SB::UNITS, k & 1, j, 0, 0);
+            b.read(fb, slot + (k >> 1) * SB::UNITS, k & 1, j, 0, 1);
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fa[k], acc[j], 0, 0, 0);
+        }
+    if (t >= p.T) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        store4((uint16_t *)p.dx + (size_t)t * p.d + c + 16 * j, v[j] + acc[j]);
+}
+
 // dWr over one token range (of p.splits), in fp32 or, undivided, rounded.
-template <typename T>
-__global__ __launch_bounds__(256) void router_grad_w(RouterGradParams p) {
-    __shared__ simt::Stage st;
-    const int e0 = blockIdx.x * simt::BM, c0 = blockIdx.y * simt::BN;
+__global__ __launch_bounds__(256) void router_grad_w_f32(RouterGradParams p) {
+    __shared__ f32t::Stage st;
+    const int e0 = blockIdx.x * f32t::BM, c0 = blockIdx.y * f32t::BN;
     const int per = (p.T + p.splits - 1) / p.splits;
     const int t0 = blockIdx.z * per;
     const int n = min(per, p.T - t0);       // may be <= 0: zeros
-    float acc[4][4];
-    simt::clear(acc);
-    simt::product<false, false>(acc, st, p.dl + (size_t)t0 * p.ep + e0, p.ep, n,
-                                (const T *)p.x + (size_t)t0 * p.d + c0, p.d, n,
-                                n);
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    f32t::Acc acc;
+    f32t::clear(acc);
+    f32t::product<false, false>(acc, st, (const float *)p.dl + (size_t)t0 * p.ep + e0,
+                                p.ep, n, (const float *)p.x + (size_t)t0 * p.d + c0,
+                                p.d, n, n);
+    float *out = p.splits > 1 ? p.wr_part + blockIdx.z * (size_t)p.E * p.d
+                              : (float *)p.dwr;
+    f32t::each(acc, [&](int m, int c, floatx4 v) {
+        if (e0 + m < p.E) store4(out + (size_t)(e0 + m) * p.d + c0 + c, v);
+    });
+}
+
+// 64 experts x 256 columns on the matrix cores, both operands along tokens.
+__global__ __launch_bounds__(256, 2) void router_grad_w_bf16(RouterGradParams p) {
+    typedef mt::Product<4, 4, 1, 4, 1, true, true, true, true> P;
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int e0 = blockIdx.x * P::BM, c0 = blockIdx.y * P::BN;
+    const int per = (p.T + p.splits - 1) / p.splits;
+    const int t0 = blockIdx.z * per;
+    const int n = min(per, p.T - t0);       // may be <= 0: zeros
+    const mt::Operand a = {(const char *)((const uint16_t *)p.dl + (size_t)t0 * p.ep + e0),
+                           nullptr, (size_t)p.ep * 2, P::BM, n};
+    const mt::Operand b = {(const char *)((const uint16_t *)p.x + (size_t)t0 * p.d + c0),
+                           nullptr, (size_t)p.d * 2, min(P::BN, p.d - c0), n};
+    floatx4 acc[4][4];
+    mt::clear(acc);
+    P::run(acc, a, b, slot0, slot1, n > 0 ? (n + mt::SK - 1) / mt::SK : 0, wave, lane);
+    const int c = c0 + wave * 64 + 4 * (lane >> 4);
+    if (c0 + wave * 64 >= p.d) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int e = e0 + ty * 4 + i;
+        const int e = e0 + 16 * i + (lane & 15);
         if (e >= p.E) continue;
-        const size_t at = (size_t)e * p.d + c0 + tx * 4;
-        if (p.splits > 1)
-            simt::store4(p.wr_part + blockIdx.z * (size_t)p.E * p.d + at, acc[i]);
-        else
-            simt::store4((T *)p.dwr + at, acc[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const size_t at = (size_t)e * p.d + c + 16 * j;
+            if (p.splits > 1)
+                store4(p.wr_part + blockIdx.z * (size_t)p.E * p.d + at, acc[i][j]);
+            else
+                store4((uint16_t *)p.dwr + at, acc[i][j]);
+        }
     }
 }
 
@@ -247,15 +369,10 @@ __global__ __launch_bounds__(256) void router_grad_w_sum(RouterGradParams p) {
     const size_t n = (size_t)p.E * p.d;
     const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= n) return;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < p.splits; ++s) {
-        const float4 q = simt::load4(p.wr_part + s * n + i);
-        v[0] += q.x;
-        v[1] += q.y;
-        v[2] += q.z;
-        v[3] += q.w;
-    }
-    simt::store4((T *)p.dwr + i, v);
+    floatx4 v = load4(p.wr_part + i);
+#pragma unroll 4
+    for (int s = 1; s < p.splits; ++s) v += load4(p.wr_part + s * n + i);
+    store4((T *)p.dwr + i, v);
 }
 
 __global__ __launch_bounds__(256) void zero_fill(uint16_t *p, size_t n) {
@@ -264,47 +381,96 @@ __global__ __launch_bounds__(256) void zero_fill(uint16_t *p, size_t n) {
         p[i] = 0;
 }
 
-template <typename T>
-hipError_t router_grad(const RouterGradParams &p, hipStream_t s) {
-    const int tt = (p.T + simt::BM - 1) / simt::BM;
-    if (p.z != 0.0f || (p.aux != 0.0f && !p.choice))
-        hipLaunchKernelGGL((router_grad_logits<T>), dim3(tt, p.ep / simt::BN),
-                           dim3(256), 0, s, p);
+template <typename T> void dlogits(const RouterGradParams &p, hipStream_t s) {
     const int nb = (p.T + MOE_ROUTER_GRAD_TOKENS - 1) / MOE_ROUTER_GRAD_TOKENS;
     if (p.choice)
-        hipLaunchKernelGGL((router_grad_dlogits<true>), dim3(nb), dim3(256), 0, s, p);
+        hipLaunchKernelGGL((router_grad_dlogits<T, true>), dim3(nb), dim3(1024), 0, s, p);
     else
-        hipLaunchKernelGGL((router_grad_dlogits<false>), dim3(nb), dim3(256), 0, s, p);
+        hipLaunchKernelGGL((router_grad_dlogits<T, false>), dim3(nb), dim3(1024), 0, s, p);
     if (p.db)
         hipLaunchKernelGGL(router_grad_bias, dim3(p.E), dim3(64), 0, s, p);
-    if (p.dx)
-        hipLaunchKernelGGL((router_grad_x<T>), dim3(tt, p.d / simt::BN), dim3(256), 0, s, p);
-    if (p.dwr) {
-        hipLaunchKernelGGL((router_grad_w<T>),
-                           dim3(p.ep / simt::BM, p.d / simt::BN, p.splits),
+}
+
+template <typename T> void sum_splits(const RouterGradParams &p, hipStream_t s) {
+    if (p.splits > 1)
+        hipLaunchKernelGGL((router_grad_w_sum<T>),
+                           dim3((unsigned)(((size_t)p.E * p.d / 4 + 255) / 256)),
                            dim3(256), 0, s, p);
-        if (p.splits > 1)
-            hipLaunchKernelGGL((router_grad_w_sum<T>),
-                               dim3((unsigned)(((size_t)p.E * p.d / 4 + 255) / 256)),
-                               dim3(256), 0, s, p);
+}
+
+bool need_logits(const RouterGradParams &p) {
+    return p.z != 0.0f || (p.aux != 0.0f && !p.choice);
+}
+
+void router_grad_f32(const RouterGradParams &p, hipStream_t s) {
+    const int tt = (p.T + f32t::BM - 1) / f32t::BM;
+    if (need_logits(p))
+        hipLaunchKernelGGL(router_grad_logits_f32, dim3(tt, p.ep / f32t::BN), dim3(256),
+                           0, s, p);
+    dlogits<float>(p, s);
+    if (p.dx)
+        hipLaunchKernelGGL(router_grad_x_f32, dim3(tt, p.d / f32t::BN), dim3(256), 0, s, p);
+    if (p.dwr) {
+        hipLaunchKernelGGL(router_grad_w_f32,
+                           dim3(p.ep / f32t::BM, p.d / f32t::BN, p.splits), dim3(256), 0,
+                           s, p);
+        sum_splits<float>(p, s);
     }
-    return hipGetLastError();
+}
+
+hipError_t router_grad_bf16(const RouterGradParams &p, hipStream_t s) {
+    if (need_logits(p)) {
+        // the forward's partial logits
+        RouterParams q = {};
+        q.x = p.x;
+        q.wr = p.wr;
+        q.part = p.logits;
+        q.S = p.logit_splits;
+        q.kc = p.logit_depth;
+        q.T = p.T;
+        q.d = p.d;
+        q.E = p.E;
+        const hipError_t e = launch_router_logits(q, s);
+        if (e != hipSuccess) return e;
+    }
+    dlogits<uint16_t>(p, s);
+    if (p.dx) {
+        const dim3 grid((p.T + 63) / 64, p.d / 64);
+        switch (p.ep / 64) {
+        case 1: hipLaunchKernelGGL(router_grad_x_bf16<1>, grid, dim3(256), 0, s, p); break;
+        case 2: hipLaunchKernelGGL(router_grad_x_bf16<2>, grid, dim3(256), 0, s, p); break;
+        case 3: hipLaunchKernelGGL(router_grad_x_bf16<3>, grid, dim3(256), 0, s, p); break;
+        default: hipLaunchKernelGGL(router_grad_x_bf16<4>, grid, dim3(256), 0, s, p); break;
+        }
+    }
+    if (p.dwr) {
+        hipLaunchKernelGGL(router_grad_w_bf16,
+                           dim3(p.ep / 64, (p.d + 255) / 256, p.splits), dim3(256), 0, s, p);
+        sum_splits<uint16_t>(p, s);
+    }
+    return hipSuccess;
 }
 
 }  // namespace
 
 // Enough ranges for two blocks per CU, of at least 128 tokens each.
-int router_grad_splits(int T, int d, int E) {
-    const long long tiles = (long long)((E + 63) / 64) * (d / simt::BN);
+int router_grad_splits(int dtype, int T, int d, int E) {
+    const int bn = dtype == 1 ? 256 : f32t::BN;
+    const long long tiles = (long long)((E + 63) / 64) * ((d + bn - 1) / bn);
     long long n = (512 + tiles - 1) / tiles;
     const long long most = (T + 127) / 128;
     if (n > most) n = most;
     return (int)(n < 1 ? 1 : n);
 }
 
-hipError_t launch_router_grad(const RouterGradParams &p, int dtype,
-                              hipStream_t s) {
-    return dtype == 1 ? router_grad<uint16_t>(p, s) : router_grad<float>(p, s);
+hipError_t launch_router_grad(const RouterGradParams &p, int dtype, hipStream_t s) {
+    if (dtype == 1) {
+        const hipError_t e = router_grad_bf16(p, s);
+        if (e != hipSuccess) return e;
+    } else {
+        router_grad_f32(p, s);
+    }
+    return hipGetLastError();
 }
 
 hipError_t launch_zero(void *dst, size_t n, hipStream_t s) {
