@@ -24,7 +24,7 @@ __device__ __forceinline__ void group_rows(const FfnGradParams &p, int g,
         start = p.offsets[g];
         rows = p.offsets[g + 1] - start;
     } else {
-        start = p.shared_base;
+        start = 0;
         rows = p.T;
     }
 }

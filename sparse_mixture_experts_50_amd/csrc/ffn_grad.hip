@@ -46,6 +46,53 @@ __device__ __forceinline__ void act_grad(float z, float u, float &h, float &hz,
     }
 }
 
+// Block (g, c): the padding rows of group g, a c-th of their columns.  Every
+// block adds up the group sizes before its own by itself.
+constexpr int PAD_PARTS = 8;
+__global__ __launch_bounds__(256) void pad_groups(PadParams p, int elem_bytes) {
+    __shared__ int part[4];
+    const int g = blockIdx.x, tid = threadIdx.x;
+    constexpr int M = MOE_GRAD_ROWS - 1;
+    int start = 0, rows = p.T;
+    if (g < p.E) {
+        // padded sizes of the groups, the sum up to this lane's in `incl`
+        const int n = tid < p.E ? p.offsets[tid + 1] - p.offsets[tid] : 0;
+        int incl = (n + M) & ~M;
+        const int own = incl;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(incl, o, 64);
+            if ((tid & 63) >= o) incl += v;
+        }
+        if ((tid & 63) == 63) part[tid >> 6] = incl;
+        __syncthreads();
+        for (int w = 0; w < (tid >> 6); ++w) incl += part[w];
+        const int first = p.n_shared ? (p.T + M) & ~M : 0;
+        if (g == 0 && blockIdx.y == 0 && tid < p.E) {
+            p.pad[tid] = first + incl - own;
+            if (tid == p.E - 1) p.pad[p.E] = first + incl;
+        }
+        __shared__ int mine[2];
+        if (tid == g) {
+            mine[0] = first + incl - own;
+            mine[1] = n;
+        }
+        __syncthreads();
+        start = mine[0];
+        rows = mine[1];
+    }
+    const int n = ((rows + M) & ~M) - rows;
+    if (n == 0) return;
+    const size_t row_bytes = (size_t)p.d * elem_bytes;
+    const size_t bytes = n * row_bytes, at = (size_t)(start + rows) * row_bytes;
+    const u32x4 zero = {0, 0, 0, 0};
+    for (size_t b = ((size_t)blockIdx.y * 256 + tid) * 16; b < bytes; b += PAD_PARTS * 256 * 16) {
+        *(u32x4 *)((char *)p.xs + at + b) = zero;
+        *(u32x4 *)((char *)p.dys + at + b) = zero;
+    }
+    if (blockIdx.y == 0 && tid < n) p.row_w[start + rows + tid] = 0.0f;
+}
+
 // Row tiles: 64 rows of one group by 64 columns.
 struct RowTile {
     int g, row0, nrows, n_tile;
@@ -67,7 +114,7 @@ __global__ __launch_bounds__(256) void ffn_act_grad_f32(FfnGradParams p) {
     __shared__ f32t::Stage st;
     __shared__ TileTable tt;
     const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
-    build_tile_table(tt, p.offsets, p.E, p.n_shared, p.shared_base, p.T,
+    build_tile_table(tt, p.offsets, p.E, p.n_shared, 0, p.T,
                      f32t::BM, F / f32t::BN);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     RowTile r;
@@ -132,7 +179,7 @@ __global__ __launch_bounds__(256) void ffn_row_grad_f32(FfnGradParams p) {
     __shared__ f32t::Stage st;
     __shared__ TileTable tt;
     const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
-    build_tile_table(tt, p.offsets, p.E, p.n_shared, p.shared_base, p.T,
+    build_tile_table(tt, p.offsets, p.E, p.n_shared, 0, p.T,
                      f32t::BM, d / f32t::BN);
     RowTile r;
     for (int L = blockIdx.x; row_tile(tt, G, L, r); L += gridDim.x) {
@@ -221,7 +268,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void ffn_bias_dot(FfnGradParams p) {
     __shared__ TileTable tt;
     const int G = p.E + p.n_shared;
-    build_tile_table(tt, p.offsets, p.E, p.n_shared, p.shared_base, p.T, 4, 1);
+    build_tile_table(tt, p.offsets, p.E, p.n_shared, 0, p.T, 4, 1);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int L = blockIdx.x; L < tt.base[G]; L += gridDim.x) {
         const int g = find_group(tt, G, L);
@@ -255,6 +302,18 @@ void act_grad_f32(const FfnGradParams &p, hipStream_t s) {
 }
 
 }  // namespace
+
+size_t padded_rows(long long T, int n_shared, long long R, int E) {
+    const long long m = MOE_GRAD_ROWS;
+    const long long shared = n_shared ? (T + m - 1) / m * m : 0;
+    return (size_t)(shared + R + (m - 1) * (R < E ? R : E));
+}
+
+hipError_t launch_pad_groups(const PadParams &p, int dtype, hipStream_t s) {
+    hipLaunchKernelGGL(pad_groups, dim3(p.E + p.n_shared, PAD_PARTS), dim3(256), 0, s, p,
+                       dtype == 1 ? 2 : 4);
+    return hipGetLastError();
+}
 
 int ffn_grad_dw_tiles(int dtype, int d_ff, int act) {
     return dtype == 1 ? mfma_dw_tiles(d_ff, act) : d_ff / 32;

@@ -48,30 +48,35 @@ __device__ __forceinline__ void act_grad(float z, float u, float &h, float &hz,
     }
 }
 
-// Writes 16 rows of a wave's TN column blocks as bf16, whole rows of
-// 32 TN bytes at a time: the MFMA layout (lane: row l % 16, 4 columns from
-// 4 (l / 16)) goes through the wave's own 512 TN bytes of LDS.
+// Writes 16 rows of a wave's TN column blocks, columns lo..hi of them, as
+// bf16, whole rows of 32 TN bytes at a time: the MFMA layout (lane: row l % 16, 4 columns from
+// 4 (l / 16)) goes through the wave's own 32 TN 16-byte units of LDS, from
+// unit u0.  (Opaque indexes for the same reason as in mfma_tile.h: the next
+// tile's loads are in flight.)
 template <int TN>
-__device__ __forceinline__ void store_rows(char *scr, const float (&v)[TN][4],
-                                           bf16 *out, size_t ld, int rows,
-                                           int cols, int lane) {
+__device__ __forceinline__ void store_rows(u32x4 *scr, int u0, const float (&v)[TN][4],
+                                           bf16 *out, size_t ld, int lo, int hi,
+                                           int lane) {
     constexpr int CPR = TN * 2;                  // 16-byte chunks per row
     const int l16 = lane & 15, hq = lane >> 4;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-        const int c = (j * 2 + (hq >> 1)) ^ (l16 & (CPR - 1));
         u32x2 o;
         o.x = pack_bf16x2(v[j][0], v[j][1]);
         o.y = pack_bf16x2(v[j][2], v[j][3]);
-        *(u32x2 *)(scr + l16 * (CPR * 16) + c * 16 + (hq & 1) * 8) = o;
+        int at = (u0 + l16 * CPR + ((j * 2 + (hq >> 1)) ^ (l16 & (CPR - 1)))) * 2 + (hq & 1);
+        asm("" : "+v"(at));
+        ((u32x2 *)scr)[at] = o;
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < CPR / 4; ++i) {
         const int r = i * (64 / CPR) + lane / CPR, c = lane % CPR;
-        const u32x4 q = *(const u32x4 *)(scr + r * (CPR * 16) + ((c ^ (r & (CPR - 1))) * 16));
-        if (r < rows && c * 8 < cols) *(u32x4 *)(out + (size_t)r * ld + c * 8) = q;
+        int at = u0 + r * CPR + (c ^ (r & (CPR - 1)));
+        asm("" : "+v"(at));
+        const u32x4 q = scr[at];
+        if (c * 8 >= lo && c * 8 < hi) *(u32x4 *)(out + (size_t)r * ld + c * 8) = q;
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
@@ -84,245 +89,351 @@ __device__ __forceinline__ int tile_of(int r) {
     return r * nb + (blockIdx.x & 7) * per + (blockIdx.x >> 3);
 }
 
+// (Groups are padded to 64 rows, see pad_groups.)
+// A group's rows in ceil(rows / 256) tiles of one height, 32 rb rows: rb
+// (16-row blocks per wave) is what an even split needs, rounded up to 2, 4,
+// 6, 7 or 8.  (Full tiles and a remainder instead would run a group of 384
+// rows as 512 and one of 1030 as 1280, here 384 and 1120.)
+__device__ __forceinline__ int split_blocks(int rows) {
+    const int m = (rows + 255) >> 8;
+    const int rb = ((rows + m - 1) / m + 31) >> 5;
+    return rb <= 6 ? (rb + 1) & ~1 : rb;
+}
+
 struct RowTile {
-    int g, row0, nrows, n_tile;
+    int g, row0, nrows, rb, n_tile;
 };
-template <int BM>
 __device__ __forceinline__ RowTile row_tile(const TileTable &tt, int G, int L) {
     RowTile r;
     r.g = __builtin_amdgcn_readfirstlane(find_group(tt, G, L));
     const int local = L - __builtin_amdgcn_readfirstlane(tt.base[r.g]);
     const int mt = __builtin_amdgcn_readfirstlane(tt.mt[r.g]);
+    const int rows = __builtin_amdgcn_readfirstlane(tt.rows[r.g]);
+    r.rb = split_blocks(rows);
     r.n_tile = local / mt;
     const int m = local - r.n_tile * mt;
-    r.row0 = __builtin_amdgcn_readfirstlane(tt.start[r.g]) + m * BM;
-    r.nrows = min(BM, __builtin_amdgcn_readfirstlane(tt.rows[r.g]) - m * BM);
+    r.row0 = __builtin_amdgcn_readfirstlane(tt.start[r.g]) + m * 32 * r.rb;
+    r.nrows = min(32 * r.rb, rows - m * 32 * r.rb);
     return r;
 }
 
+// f(integral_constant<rb>)
+template <typename F> __device__ __forceinline__ void by_height(int rb, F f) {
+    if (rb == 8) f(std::integral_constant<int, 8>{});
+    else if (rb == 7) f(std::integral_constant<int, 7>{});
+    else if (rb == 6) f(std::integral_constant<int, 6>{});
+    else if (rb == 4) f(std::integral_constant<int, 4>{});
+    else f(std::integral_constant<int, 2>{});
+}
+
+// The lane index, opaque, so that per-lane addresses are not kept across
+// tiles.
+__device__ __forceinline__ int tile_lane() {
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    return tid & 63;
+}
+
+// First column of a tile: the last of an axis of n >= size ends with it (and
+// computes the columns that it shares with the one before again, storing
+// only its own), so that no operand is read past its end.
+__device__ __forceinline__ int tile_start(int i, int size, int n) {
+    return n >= size ? min(i * size, n - size) : 0;
+}
+
 // out[rows][N] (fp32) = the sum of one or two products A B of a group's rows
-// with its weights, stored along K.  Q: q = dy W2; else dx = dz W1 + du W3.
-template <int RB, int TN, int WM, int WN, bool Q, bool ODD>
+// with its weights, stored along K.  Q: q = dy W2; else dx = dz W1 + du W3
+// (GATED).
+template <bool Q, bool GATED, mt::Stages KIND>
 __global__ __launch_bounds__(256, 1) void ffn_rows_by_weights(FfnGradParams p) {
-    typedef mt::Product<RB, TN, WM, WN, 1, false, true, false, ODD> P;
+    typedef mt::Tiles<256, 256, 2, 2, 1, false, true, GATED> P;
+    constexpr int TN = P::TN;
     __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
     __shared__ TileTable tt;
     const int G = p.E + p.n_shared;
     const int N = Q ? p.d_ff : p.d, K = Q ? p.d : p.d_ff;
-    build_tile_table(tt, p.offsets, p.E, p.n_shared, p.shared_base, p.T, P::BM,
-                     (N + P::BN - 1) / P::BN);
+    build_tile_table(tt, p.offsets, p.E, p.n_shared, 0, p.T, 256, (N + 255) / 256);
     const int total = __builtin_amdgcn_readfirstlane(tt.base[G]);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / WN, wn = wave % WN;
-    for (int r = 0;; ++r) {
-        const int L = tile_of(r);
-        if (L >= total) break;
-        // opaque, so that per-lane addresses are not kept across tiles
-        int tid = threadIdx.x;
-        asm volatile("" : "+v"(tid));
-        const int lane = tid & 63;
-        const RowTile t = row_tile<P::BM>(tt, G, L);
-        const int n0 = t.n_tile * P::BN;
-        const size_t mat = (size_t)p.d_ff * p.d, at = (size_t)t.row0 * K;
-        mt::Operand a = {(const char *)((const bf16 *)(Q ? p.dys : p.dz) + at), nullptr,
-                         (size_t)K * 2, t.nrows, 0};
-        mt::Operand b = {(const char *)(of_group<bf16>(Q ? p.w2 : p.w1, Q ? p.ws2 : p.ws1,
-                                                       t.g, p.E, mat) + n0),
-                         nullptr, (size_t)N * 2, min(P::BN, N - n0), 0};
-        floatx4 acc[RB][TN];
-        mt::clear(acc);
-        P::run(acc, a, b, slot0, slot1, K / mt::SK, wave, lane);
-        if (!Q && p.act == ACT_SWIGLU) {
-            a.base = (const char *)((const bf16 *)p.du + at);
-            b.base = (const char *)(of_group<bf16>(p.w3, p.ws3, t.g, p.E, mat) + n0);
-            P::run(acc, a, b, slot0, slot1, K / mt::SK, wave, lane);
-        }
-        const int l16 = lane & 15, c0 = n0 + wn * TN * 16;
+    const int wm = wave / 2, wn = wave % 2;
+    const int kt = (GATED ? 2 : 1) * K / mt::SK;
+    const size_t mat = (size_t)p.d_ff * p.d;
+    auto source = [&](const RowTile &t) __attribute__((always_inline)) {
+        const int n0 = tile_start(t.n_tile, 256, N);
+        const size_t at = (size_t)t.row0 * K;
+        typename P::Source s;
+        s.a = (uint64_t)((const bf16 *)(Q ? p.dys : p.dz) + at);
+        s.b = (uint64_t)(of_group<bf16>(Q ? p.w2 : p.w1, Q ? p.ws2 : p.ws1, t.g, p.E, mat) + n0);
+        s.a2 = GATED ? (uint64_t)((const bf16 *)p.du + at) : s.a;
+        s.b2 = GATED ? (uint64_t)(of_group<bf16>(p.w3, p.ws3, t.g, p.E, mat) + n0) : s.b;
+        s.kt = kt;
+        return s;
+    };
+    int L = tile_of(0);
+    if (L >= total) return;
+    typename P::Lanes ln;
+    ln.init(K * 2, 256, N * 2, min(N, 256), wave, threadIdx.x & 63);
+    ln.split = K / mt::SK;
+    RowTile t = row_tile(tt, G, L);
+    typename P::Source src = source(t);
+    P::load_stage(src, ln, 0, slot0, wave);
+    P::load_stage(src, ln, 1, slot1, wave);
+    for (int r = 1;; ++r) {
+        const int lane = tile_lane();
+        L = tile_of(r);
+        const bool more = L < total;
+        const RowTile tn = more ? row_tile(tt, G, L) : t;
+        const typename P::Source next = source(tn);
+        by_height(t.rb, [&](auto height) __attribute__((always_inline)) {
+            constexpr int RB = decltype(height)::value;
+            floatx4 acc[RB][TN];
+            mt::clear(acc);
+            P::template run<RB, RB, KIND>(acc, src, ln, next, ln, slot0, slot1, wave, lane);
+            const int lo = t.n_tile * 256;
+            const int c0 = tile_start(t.n_tile, 256, N) + wn * TN * 16;
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            const int m = (wm * RB + i) * 16 + l16;
-            if (m >= t.nrows) continue;
-            float *out = (Q ? p.q : p.dxs) + (size_t)(t.row0 + m) * N + c0 + 4 * (lane >> 4);
+            for (int i = 0; i < RB; ++i) {
+                const int m = (wm * RB + i) * 16;
+                if (m >= t.nrows) continue;
+                float *out = (Q ? p.q : p.dxs) + (size_t)(t.row0 + m + (lane & 15)) * N + c0 +
+                             4 * (lane >> 4);
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
-                if (c0 + 16 * j < N) *(floatx4 *)(out + 16 * j) = acc[i][j];
-        }
+                for (int j = 0; j < TN; ++j)
+                    if (c0 + 16 * j >= lo && c0 + 16 * j < N)
+                        *(floatx4 *)(out + 16 * j) = acc[i][j];
+            }
+        });
+        if (!more) break;
+        t = tn;
+        src = next;
     }
+    __builtin_amdgcn_s_waitcnt(0);
 }
 
 // z (and u) of a tile, then with q: r h, dz, du and the parts of <q, h>.  A
-// gated tile has TN column blocks of z and the same TN of u per wave.
-template <int RB, int TN, int WM, int WN, int ACT, bool ODD>
+// gated tile is 128 columns of z and the same 128 of u.
+template <int ACT, mt::Stages KIND>
 __global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
-    constexpr int PANELS = ACT == ACT_SWIGLU ? 2 : 1;
-    typedef mt::Product<RB, TN, WM, WN, PANELS, false, false, false, ODD> P;
-    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
+    constexpr int PANELS = ACT == ACT_SWIGLU ? 2 : 1, BN = 256 / PANELS;
+    typedef mt::Tiles<256, BN, 2, 2, PANELS, false, false> P;
+    constexpr int TN = P::TN;
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], scr[4 * 32 * TN];
     __shared__ TileTable tt;
     const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
-    build_tile_table(tt, p.offsets, p.E, p.n_shared, p.shared_base, p.T, P::BM,
-                     (F + P::BN - 1) / P::BN);
+    build_tile_table(tt, p.offsets, p.E, p.n_shared, 0, p.T, 256, (F + BN - 1) / BN);
     const int total = __builtin_amdgcn_readfirstlane(tt.base[G]);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / WN, wn = wave % WN;
-    for (int r = 0;; ++r) {
-        const int L = tile_of(r);
-        if (L >= total) break;
-        int tid = threadIdx.x;
-        asm volatile("" : "+v"(tid));
-        const int lane = tid & 63;
-        const RowTile t = row_tile<P::BM>(tt, G, L);
-        const int n0 = t.n_tile * P::BN;
-        const size_t mat = (size_t)F * d;
-        const bf16 *w1 = of_group<bf16>(p.w1, p.ws1, t.g, p.E, mat);
-        const bf16 *w3 = PANELS > 1 ? of_group<bf16>(p.w3, p.ws3, t.g, p.E, mat) : w1;
-        const mt::Operand a = {(const char *)((const bf16 *)p.xs + (size_t)t.row0 * d),
-                               nullptr, (size_t)d * 2, t.nrows, 0};
-        const mt::Operand b = {(const char *)(w1 + (size_t)n0 * d),
-                               (const char *)(w3 + (size_t)n0 * d), (size_t)d * 2,
-                               min(P::BN, F - n0), 0};
-        const int l16 = lane & 15, c0 = n0 + wn * TN * 16;
-        const int cols = F - c0;             // columns of this wave
+    const int wm = wave / 2, wn = wave % 2;
+    const int kt = d / mt::SK;
+    const size_t mat = (size_t)F * d;
+    auto source = [&](const RowTile &t) __attribute__((always_inline)) {
+        const size_t at = (size_t)tile_start(t.n_tile, BN, F) * d;
+        typename P::Source s;
+        s.a = s.a2 = (uint64_t)((const bf16 *)p.xs + (size_t)t.row0 * d);
+        s.b = (uint64_t)(of_group<bf16>(p.w1, p.ws1, t.g, p.E, mat) + at);
+        s.b2 = PANELS > 1 ? (uint64_t)(of_group<bf16>(p.w3, p.ws3, t.g, p.E, mat) + at) : s.b;
+        s.kt = kt;
+        return s;
+    };
+    int L = tile_of(0);
+    if (L >= total) return;
+    typename P::Lanes ln;
+    ln.init(d * 2, 256, d * 2, min(F, BN), wave, threadIdx.x & 63);
+    ln.split = kt;
+    RowTile t = row_tile(tt, G, L);
+    typename P::Source src = source(t);
+    P::load_stage(src, ln, 0, slot0, wave);
+    P::load_stage(src, ln, 1, slot1, wave);
+    for (int r = 1;; ++r) {
+        const int lane = tile_lane();
+        L = tile_of(r);
+        const bool more = L < total;
+        const RowTile tn = more ? row_tile(tt, G, L) : t;
+        const typename P::Source next = source(tn);
+        const int l16 = lane & 15;
+        const int c0 = tile_start(t.n_tile, BN, F) + wn * TN * 16;
+        // this wave's columns of the tile's own, from c0: lo..hi
+        const int lo = t.n_tile * BN - c0, hi = F - c0;
         const int cq = c0 + 4 * (lane >> 4);
-        // the sums start from the biases
-        floatx4 z[RB][TN * PANELS];
-        mt::clear(z);
         const bf16 *bias[2] = {of_group<bf16>(p.b1, p.bs1, t.g, p.E, F),
                                PANELS > 1 ? of_group<bf16>(p.b3, p.bs3, t.g, p.E, F) : nullptr};
+        by_height(t.rb, [&](auto height) __attribute__((always_inline)) {
+            constexpr int RB = decltype(height)::value;
+            // the sums start from the biases
+            floatx4 z[RB][TN * PANELS];
+            mt::clear(z);
 #pragma unroll
-        for (int k = 0; k < PANELS; ++k)
-            if (bias[k]) {
+            for (int k = 0; k < PANELS; ++k)
+                if (bias[k]) {
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) {
+                        if (16 * j >= hi) continue;      // whole blocks: F % 64 == 0
+                        const u32x2 v = *(const u32x2 *)(bias[k] + cq + 16 * j);
+                        const floatx4 f = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y),
+                                           bf16_hi(v.y)};
+#pragma unroll
+                        for (int i = 0; i < RB; ++i) z[i][k * TN + j] = f;
+                    }
+                }
+            P::template run<RB, RB, KIND>(z, src, ln, next, ln, slot0, slot1, wave, lane);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                const int m0 = (wm * RB + i) * 16;
+                if (m0 >= t.nrows) continue;
+                const int row = t.row0 + m0 + l16;
+                const float w = p.row_w[row];
+                const float *qp = p.q + (size_t)row * F + cq;
+                floatx4 q[TN];
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    q[j] = 16 * j >= lo && 16 * j < hi ? *(const floatx4 *)(qp + 16 * j)
+                                                       : floatx4{0.f, 0.f, 0.f, 0.f};
+                float vh[TN][4], vz[TN][4], vu[TN][4], dot = 0.0f;
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
-                    if (16 * j >= cols) continue;    // whole blocks: F % 64 == 0
-                    const u32x2 v = *(const u32x2 *)(bias[k] + cq + 16 * j);
-                    const floatx4 f = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
 #pragma unroll
-                    for (int i = 0; i < RB; ++i) z[i][k * TN + j] = f;
+                    for (int e = 0; e < 4; ++e) {
+                        float h, hz, hu;
+                        act_grad<ACT>(z[i][j][e],
+                                      PANELS > 1 ? z[i][j + TN * (PANELS - 1)][e] : 0.0f,
+                                      h, hz, hu);
+                        const float qq = q[j][e];
+                        dot = fmaf(qq, h, dot);
+                        vh[j][e] = w * h;
+                        vz[j][e] = w * qq * hz;
+                        if (PANELS > 1) vu[j][e] = w * qq * hu;
+                    }
                 }
+                dot += __shfl_xor(dot, 16, 64);
+                dot += __shfl_xor(dot, 32, 64);
+                if (lane < 16) p.dw_part[(size_t)row * p.dw_tiles + t.n_tile * 2 + wn] = dot;
+                const size_t at = (size_t)(t.row0 + m0) * F + c0;
+                const int u0 = wave * 32 * TN;
+                store_rows<TN>(scr, u0, vh, (bf16 *)p.h + at, F, lo, hi, lane);
+                store_rows<TN>(scr, u0, vz, (bf16 *)p.dz + at, F, lo, hi, lane);
+                if (PANELS > 1) store_rows<TN>(scr, u0, vu, (bf16 *)p.du + at, F, lo, hi, lane);
+                // one row block at a time: the accumulators are read as they
+                // are used, not all at once
+                __builtin_amdgcn_sched_barrier(0);
             }
-        P::run(z, a, b, slot0, slot1, d / mt::SK, wave, lane);
-        __builtin_amdgcn_s_waitcnt(0);
-        __builtin_amdgcn_s_barrier();        // the slots are free
-        if (cols <= 0) continue;
-        char *scr = (char *)slot0 + wave * (TN * 512);
-#pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            const int m0 = (wm * RB + i) * 16;
-            const int rows = t.nrows - m0;
-            if (rows <= 0) continue;
-            // rows past the group's end read its last row and store nothing
-            const int row = t.row0 + m0 + min(l16, rows - 1);
-            const float w = p.row_w[row];
-            const float *qp = p.q + (size_t)row * F + cq;
-            floatx4 q[TN];
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                q[j] = *(const floatx4 *)(qp + (16 * j < cols ? 16 * j : 0));
-            float vh[TN][4], vz[TN][4], vu[TN][4], dot = 0.0f;
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const float in = 16 * j < cols ? 1.0f : 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float h, hz, hu;
-                    act_grad<ACT>(z[i][j][e],
-                                  PANELS > 1 ? z[i][j + TN * (PANELS - 1)][e] : 0.0f, h,
-                                  hz, hu);
-                    const float qq = q[j][e] * in;
-                    dot = fmaf(qq, h, dot);
-                    vh[j][e] = w * h;
-                    vz[j][e] = w * qq * hz;
-                    if (PANELS > 1) vu[j][e] = w * qq * hu;
-                }
-            }
-            dot += __shfl_xor(dot, 16, 64);
-            dot += __shfl_xor(dot, 32, 64);
-            if (lane < 16 && l16 < rows)
-                p.dw_part[(size_t)row * p.dw_tiles + c0 / (TN * 16)] = dot;
-            const size_t at = (size_t)(t.row0 + m0) * F + c0;
-            store_rows<TN>(scr, vh, (bf16 *)p.h + at, F, rows, cols, lane);
-            store_rows<TN>(scr, vz, (bf16 *)p.dz + at, F, rows, cols, lane);
-            if (PANELS > 1) store_rows<TN>(scr, vu, (bf16 *)p.du + at, F, rows, cols, lane);
-            // one row block at a time: the accumulators are read as they are
-            // used, not all at once
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        });
+        if (!more) break;
+        t = tn;
+        src = next;
     }
+    __builtin_amdgcn_s_waitcnt(0);
 }
 
 // Tiles of one matrix's gradient go in strips of 8 row tiles, so that the 32
 // consecutive tiles of an XCD's round are 8 x 4 and read 12 operand panels.
-template <int RB, int TN, int WM, int WN>
+// Groups are whole stages of rows, their last rows zero.
+struct WeightTile {
+    int g, which, mi, ni;                // which: 0 dW1, 1 dW2, 2 dW3
+};
+
 __global__ __launch_bounds__(256, 1) void ffn_weight_grad(FfnGradParams p) {
-    typedef mt::Product<RB, TN, WM, WN, 1, true, true, true, false> P;
-    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
+    typedef mt::Tiles<256, 256, 2, 2, 1, true, true> P;
+    constexpr int TN = P::TN, RB = 8;
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], scr[4 * 32 * TN];
     const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / WN, wn = wave % WN;
+    const int wm = wave / 2, wn = wave % 2;
     const int mats = p.act == ACT_SWIGLU ? 3 : 2;
-    const int t_up = (F + P::BM - 1) / P::BM * ((d + P::BN - 1) / P::BN);
-    const int t_down = (d + P::BM - 1) / P::BM * ((F + P::BN - 1) / P::BN);
-    const int per_group = t_down + (mats - 1) * t_up;
-    const long long total = (long long)G * per_group;
-    for (int r = 0;; ++r) {
-        const long long L = (long long)r * gridDim.x + tile_of(0);
-        if (L >= total) break;
-        int tid = threadIdx.x;
-        asm volatile("" : "+v"(tid));
-        const int lane = tid & 63;
-        const int g = (int)(L / per_group);
-        int local = (int)(L - (long long)g * per_group);
-        // dW1, dW3 (F x d), then dW2 (d x F)
-        int which = 0;
-        if (local >= t_up * (mats - 1)) {
-            which = 1;
-            local -= t_up * (mats - 1);
-        } else if (local >= t_up) {
-            which = 2;
-            local -= t_up;
-        }
-        const int M = which == 1 ? d : F, N = which == 1 ? F : d;
-        const int mtiles = (M + P::BM - 1) / P::BM, ntiles = (N + P::BN - 1) / P::BN;
+    const int tiles = (F + 255) / 256 * ((d + 255) / 256);      // of a matrix
+    const int total = G * tiles * mats;
+    const size_t mat = (size_t)F * d;
+    auto tile = [&](int L) __attribute__((always_inline)) {
+        WeightTile t;
+        t.g = L / (tiles * mats);
+        int local = L - t.g * (tiles * mats);
+        const int k = local / tiles;         // dW1, dW3, dW2
+        t.which = k == mats - 1 ? 1 : 2 * k;
+        local -= k * tiles;
+        const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
+        const int mtiles = (M + 255) / 256, ntiles = (N + 255) / 256;
         const int strip = local / (8 * ntiles), in = local - strip * 8 * ntiles;
         const int sm = min(8, mtiles - strip * 8);
-        const int m0 = (strip * 8 + in % sm) * P::BM, n0 = in / sm * P::BN;
-        const size_t mat = (size_t)F * d;
-        bf16 *out = which == 0 ? of_group<bf16>(p.g_w1, p.g_ws1, g, p.E, mat)
-                    : which == 1 ? of_group<bf16>(p.g_w2, p.g_ws2, g, p.E, mat)
-                                 : of_group<bf16>(p.g_w3, p.g_ws3, g, p.E, mat);
-        if (!out) continue;
+        t.mi = strip * 8 + in % sm;
+        t.ni = in / sm;
+        return t;
+    };
+    auto result = [&](const WeightTile &t) __attribute__((always_inline)) {
+        return t.which == 0 ? of_group<bf16>(p.g_w1, p.g_ws1, t.g, p.E, mat)
+               : t.which == 1 ? of_group<bf16>(p.g_w2, p.g_ws2, t.g, p.E, mat)
+                              : of_group<bf16>(p.g_w3, p.g_ws3, t.g, p.E, mat);
+    };
+    // the first wanted tile from round r on (r is left after it); false: none
+    auto find = [&](int &r, WeightTile &t) __attribute__((always_inline)) {
+        for (;; ++r) {
+            const int L = tile_of(r);
+            if (L >= total) return false;
+            t = tile(L);
+            if (result(t)) {
+                ++r;
+                return true;
+            }
+        }
+    };
+    auto source = [&](const WeightTile &t) __attribute__((always_inline)) {
+        const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
+        const bf16 *A = (const bf16 *)(t.which == 0 ? p.dz : t.which == 1 ? p.dys : p.du);
+        const bf16 *B = (const bf16 *)(t.which == 1 ? p.h : p.xs);
         int start, rows;
-        group_rows(p, g, start, rows);
+        group_rows(p, t.g, start, rows);
         start = __builtin_amdgcn_readfirstlane(start);
-        rows = __builtin_amdgcn_readfirstlane(rows);
-        const bf16 *A = (const bf16 *)(which == 0 ? p.dz : which == 1 ? p.dys : p.du);
-        const bf16 *B = (const bf16 *)(which == 1 ? p.h : p.xs);
-        const mt::Operand a = {(const char *)(A + (size_t)start * M + m0), nullptr,
-                               (size_t)M * 2, min(P::BM, M - m0), rows};
-        const mt::Operand b = {(const char *)(B + (size_t)start * N + n0), nullptr,
-                               (size_t)N * 2, min(P::BN, N - n0), rows};
+        P::Source s;
+        s.a = s.a2 = (uint64_t)(A + (size_t)start * M + tile_start(t.mi, 256, M));
+        s.b = s.b2 = (uint64_t)(B + (size_t)start * N + tile_start(t.ni, 256, N));
+        s.kt = __builtin_amdgcn_readfirstlane(rows) / mt::SK;
+        return s;
+    };
+    auto lanes = [&](const WeightTile &t, int lane) __attribute__((always_inline)) {
+        const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
+        P::Lanes ln;
+        ln.init(M * 2, min(M, 256), N * 2, min(N, 256), wave, lane);
+        ln.split = 0;
+        return ln;
+    };
+    int r = 0;
+    WeightTile t;
+    if (!find(r, t)) return;
+    P::Source src = source(t);
+    P::Lanes ln = lanes(t, threadIdx.x & 63);
+    P::load_stage(src, ln, 0, slot0, wave);
+    P::load_stage(src, ln, 1, slot1, wave);
+    for (;;) {
+        const int lane = tile_lane();
+        WeightTile tn = t;
+        const bool more = find(r, tn);
+        if (!more) tn = t;
+        const P::Source next = source(tn);
+        const P::Lanes lnext = lanes(tn, lane);
         floatx4 acc[RB][TN];
         mt::clear(acc);
-        // whole pairs of stages: rows past the group's end are zeros
-        P::run(acc, a, b, slot0, slot1, (rows + 2 * mt::SK - 1) / (2 * mt::SK) * 2,
-               wave, lane);
-        __builtin_amdgcn_s_waitcnt(0);
-        __builtin_amdgcn_s_barrier();
-        const int c0 = n0 + wn * TN * 16;
-        char *scr = (char *)slot0 + wave * (TN * 512);
+        P::run<RB, 8, mt::ANY>(acc, src, ln, next, lnext, slot0, slot1, wave, lane);
+        const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
+        bf16 *out = result(t);
+        const int m0 = tile_start(t.mi, 256, M) + wm * RB * 16;
+        const int c0 = tile_start(t.ni, 256, N) + wn * TN * 16;
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
-            const int mi = m0 + (wm * RB + i) * 16;
-            if (mi >= M || c0 >= N) continue;
+            const int mi = m0 + i * 16;
+            if (mi < t.mi * 256 || mi >= M) continue;
             float v[TN][4];
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[j][e] = acc[i][j][e];
-            store_rows<TN>(scr, v, out + (size_t)mi * N + c0, N, 16, N - c0, lane);
+            store_rows<TN>(scr, wave * 32 * TN, v, out + (size_t)mi * N + c0, N,
+                           t.ni * 256 - c0, N - c0, lane);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        // run() of the next tile waits for every wave before it loads
+        if (!more) break;
+        t = tn;
+        src = next;
+        ln = lnext;
     }
+    __builtin_amdgcn_s_waitcnt(0);
 }
 
 int cus() {
@@ -340,49 +451,55 @@ int grid_for(long long tiles) {
     return (int)(g < n ? (g < 8 ? 8 : g) : n);
 }
 
-template <int RB, int TN, int WM, int WN, int ACT>
-void act_as(const FfnGradParams &p, hipStream_t s) {
-    const int grid = grid_for(ffn_row_tiles(p, RB * 16 * WM) *
-                              ((p.d_ff + TN * 16 * WN - 1) / (TN * 16 * WN)));
-    if (p.d / mt::SK & 1)
-        hipLaunchKernelGGL((ffn_act_grad<RB, TN, WM, WN, ACT, true>), dim3(grid), dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL((ffn_act_grad<RB, TN, WM, WN, ACT, false>), dim3(grid), dim3(256), 0, s, p);
-}
-
-template <int RB, int TN, int WM, int WN, bool Q>
-void rows_as(const FfnGradParams &p, hipStream_t s) {
-    const int N = Q ? p.d_ff : p.d, bn = TN * 16 * WN;
-    const int grid = grid_for(ffn_row_tiles(p, RB * 16 * WM) * ((N + bn - 1) / bn));
-    if ((Q ? p.d : p.d_ff) / mt::SK & 1)
-        hipLaunchKernelGGL((ffn_rows_by_weights<RB, TN, WM, WN, Q, true>), dim3(grid), dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL((ffn_rows_by_weights<RB, TN, WM, WN, Q, false>), dim3(grid), dim3(256), 0, s, p);
+// Row tiles of 256 rows by n columns in tiles of bn.
+int row_grid(const FfnGradParams &p, int n, int bn) {
+    return grid_for(ffn_row_tiles(p, 256) * ((n + bn - 1) / bn));
 }
 
 }  // namespace
 
-// Columns of a wave's tile: 64 gated, 128 else.
+// Two waves side by side in each column tile: 128 columns gated, 256 else.
 int mfma_dw_tiles(int d_ff, int act) {
-    return act == ACT_SWIGLU ? d_ff / 64 : (d_ff + 127) / 128;
+    const int bn = act == ACT_SWIGLU ? 128 : 256;
+    return (d_ff + bn - 1) / bn * 2;
+}
+
+template <bool Q, bool GATED>
+static void rows_by_weights(const FfnGradParams &p, hipStream_t s) {
+    const int N = Q ? p.d_ff : p.d;
+    const dim3 grid(row_grid(p, N, 256));
+    if (!GATED && ((Q ? p.d : p.d_ff) / mt::SK & 1))
+        hipLaunchKernelGGL((ffn_rows_by_weights<Q, GATED, GATED ? mt::EVEN : mt::ODD>), grid,
+                           dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((ffn_rows_by_weights<Q, GATED, mt::EVEN>), grid, dim3(256), 0, s, p);
+}
+
+template <int ACT> static void act_grad_as(const FfnGradParams &p, hipStream_t s) {
+    const dim3 grid(row_grid(p, p.d_ff, ACT == ACT_SWIGLU ? 128 : 256));
+    if (p.d / mt::SK & 1)
+        hipLaunchKernelGGL((ffn_act_grad<ACT, mt::ODD>), grid, dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((ffn_act_grad<ACT, mt::EVEN>), grid, dim3(256), 0, s, p);
 }
 
 hipError_t launch_act_grad_mfma(const FfnGradParams &p, hipStream_t s) {
-    rows_as<8, 8, 2, 2, true>(p, s);
-    if (p.act == ACT_GELU) act_as<8, 8, 2, 2, ACT_GELU>(p, s);
-    else if (p.act == ACT_SILU) act_as<8, 8, 2, 2, ACT_SILU>(p, s);
-    else act_as<8, 4, 2, 2, ACT_SWIGLU>(p, s);
+    rows_by_weights<true, false>(p, s);
+    if (p.act == ACT_GELU) act_grad_as<ACT_GELU>(p, s);
+    else if (p.act == ACT_SILU) act_grad_as<ACT_SILU>(p, s);
+    else act_grad_as<ACT_SWIGLU>(p, s);
     return hipGetLastError();
 }
 
 hipError_t launch_row_grad_mfma(const FfnGradParams &p, hipStream_t s) {
-    rows_as<8, 8, 2, 2, false>(p, s);
+    if (p.act == ACT_SWIGLU) rows_by_weights<false, true>(p, s);
+    else rows_by_weights<false, false>(p, s);
     return hipGetLastError();
 }
 
 hipError_t launch_weight_grad_mfma(const FfnGradParams &p, hipStream_t s) {
-    const long long up = (long long)((p.d_ff + 255) / 256) * ((p.d + 255) / 256);
-    const int grid = grid_for(up * (p.E + p.n_shared) * (p.act == ACT_SWIGLU ? 3 : 2));
-    hipLaunchKernelGGL((ffn_weight_grad<8, 8, 2, 2>), dim3(grid), dim3(256), 0, s, p);
+    const long long tiles = (long long)((p.d_ff + 255) / 256) * ((p.d + 255) / 256);
+    const int grid = grid_for(tiles * (p.E + p.n_shared) * (p.act == ACT_SWIGLU ? 3 : 2));
+    hipLaunchKernelGGL(ffn_weight_grad, dim3(grid), dim3(256), 0, s, p);
     return hipGetLastError();
 }

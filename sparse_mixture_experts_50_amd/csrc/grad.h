@@ -20,8 +20,12 @@ struct RowsParams {
     void *tok_out;            // [T][d] (dispatch_grad, combine)
     const int32_t *slot_of;   // [T][k]
     const float *topk_w;      // [T][k]
-    float *row_w;             // dispatch: [rows] routing weight of each row
-                              // (1 for shared rows), or null
+    // dispatch of two inputs (the gradient's): the padded row space of
+    // FfnGradParams, whose offsets are pad
+    const int32_t *topk_idx;  // [T][k] (null: expert choice)
+    const int32_t *offsets, *pad;   // [E+1]
+    int32_t *pad_slot;        // [T][k]: slot_of in the padded space
+    float *row_w;             // [rows] routing weight of each row (1: shared)
     float *dw;                // combine_grad: [T][k]
     int T, d, k, n_shared, shared_base;
 };
@@ -34,12 +38,16 @@ hipError_t launch_combine_rows_grad(const RowsParams &p, int dtype,
                                     hipStream_t s);
 
 // ------------------------------------------------ the layer's gradient
+// Row space: the shared expert's T rows, then the routed groups, every group
+// padded with zero rows to a multiple of MOE_GRAD_ROWS, so that the products
+// that sum over a group's rows take whole stages.
+#define MOE_GRAD_ROWS 64
 // Weight matrices and gradients by group: routed experts stacked, the
 // shared expert apart.
 struct FfnGradParams {
-    const int32_t *offsets;   // [E+1]
-    const void *xs, *dys;     // [rows][d] dispatched x and dy
-    const float *row_w;       // [rows]
+    const int32_t *offsets;   // [E+1]: padded group starts
+    const void *xs, *dys;     // [rows][d] dispatched x and dy, zero in padding
+    const float *row_w;       // [rows], zero in padding
     const void *w1, *w2, *w3, *ws1, *ws2, *ws3;
     const void *b1, *b2, *b3, *bs1, *bs2, *bs3;
     // h times the row weight, and the gradients of the pre-activations,
@@ -51,9 +59,21 @@ struct FfnGradParams {
     float *dxs;               // [rows][d] fp32
     void *g_w1, *g_w2, *g_w3, *g_ws1, *g_ws2, *g_ws3;
     void *g_b1, *g_b2, *g_b3, *g_bs1, *g_bs2, *g_bs3;
-    int E, n_shared, T, shared_base, d, d_ff, act;
-    int rows;                 // shared_base + n_shared * T
+    int E, n_shared, d, d_ff, act;
+    int T;                    // shared rows, padded: [0, T)
+    int rows;                 // upper bound of all rows
 };
+// Rows of the padded space for T tokens and R routed rows of E experts.
+size_t padded_rows(long long T, int n_shared, long long R, int E);
+// Group starts of the padded space, and its padding rows zeroed.
+struct PadParams {
+    const int32_t *offsets;   // [E+1]
+    int32_t *pad;             // [E+1]
+    void *xs, *dys;
+    float *row_w;
+    int E, n_shared, T, d;
+};
+hipError_t launch_pad_groups(const PadParams &p, int dtype, hipStream_t s);
 // Column tiles that launch_ffn_act_grad writes to dw_part.
 int ffn_grad_dw_tiles(int dtype, int d_ff, int act);
 hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype, hipStream_t s);

@@ -11,7 +11,7 @@ using namespace moe_host;
 struct GradLayout {
     // the router's part, then the experts'
     size_t logits, dl, db_part, wr_part, router_total;
-    size_t row_w, xs, dys, h, dz, du, q, dw_part, dxs, total;
+    size_t pad, pad_slot, row_w, xs, dys, h, dz, du, q, dw_part, dxs, total;
     size_t rows;
     int ep, splits, dw_tiles;
     RouterPlan logit_plan;
@@ -36,7 +36,9 @@ GradLayout layout(const moe_desc *d) {
                               MOE_ROUTER_GRAD_TOKENS) * d->E * 4);
     L.wr_part = take(L.splits > 1 ? (size_t)L.splits * d->E * d->d * 4 : 0);
     L.router_total = off > 0 ? off : kAlign;
-    L.rows = (size_t)routed_rows(d) + (size_t)d->n_shared * d->T;
+    L.rows = padded_rows(d->T, d->n_shared, routed_rows(d), d->E);
+    L.pad = take((size_t)(d->E + 1) * 4);
+    L.pad_slot = take((size_t)d->T * d->k * 4);
     // column tiles of <dy W2, h>, and <dy, b2>
     L.dw_tiles = ffn_grad_dw_tiles(d->dtype, d->d_ff, d->activation);
     L.row_w = take(L.rows * 4);
@@ -48,7 +50,9 @@ GradLayout layout(const moe_desc *d) {
     L.q = take(d->dtype == MOE_BF16 ? L.rows * d->d_ff * 4 : 0);
     L.dw_part = take(L.rows * (L.dw_tiles + 1) * 4);
     L.dxs = take(L.rows * d->d * 4);
-    L.total = off > 0 ? off : kAlign;
+    // a row tile of 256 may reach past the last row of any operand
+    take((size_t)256 * (d->d > d->d_ff ? d->d : d->d_ff) * es);
+    L.total = off;
     return L;
 }
 
@@ -294,9 +298,25 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
     rp.rows_out = at(ws, L.xs);
     rp.rows_out2 = at(ws, L.dys);
     rp.row_w = (float *)at(ws, L.row_w);
+    rp.topk_idx = expert_choice(desc) ? nullptr : r->topk_idx;
+    rp.offsets = r->offsets;
+    rp.pad = (const int32_t *)at(ws, L.pad);
+    rp.pad_slot = (int32_t *)at(ws, L.pad_slot);
+    rp.shared_base = 0;
+
+    PadParams pp;
+    pp.offsets = r->offsets;
+    pp.pad = (int32_t *)at(ws, L.pad);
+    pp.xs = rp.rows_out;
+    pp.dys = rp.rows_out2;
+    pp.row_w = rp.row_w;
+    pp.E = desc->E;
+    pp.n_shared = desc->n_shared;
+    pp.T = desc->T;
+    pp.d = desc->d;
 
     FfnGradParams p = {};
-    p.offsets = r->offsets;
+    p.offsets = pp.pad;
     p.xs = at(ws, L.xs);
     p.dys = at(ws, L.dys);
     p.row_w = rp.row_w;
@@ -340,8 +360,7 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
     }
     p.E = desc->E;
     p.n_shared = desc->n_shared;
-    p.T = desc->T;
-    p.shared_base = (int)routed_rows(desc);
+    p.T = (desc->T + MOE_GRAD_ROWS - 1) / MOE_GRAD_ROWS * MOE_GRAD_ROWS;
     p.d = desc->d;
     p.d_ff = desc->d_ff;
     p.act = desc->activation;
@@ -352,6 +371,7 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
     const bool router = g->x || g->w_router || g->b_router;
     if (!weights && !biases && !router) return MOE_OK;
     const int dt = desc->dtype;
+    if (launch_pad_groups(pp, dt, s) != hipSuccess) return MOE_ERR_HIP;
     if (launch_dispatch_rows(rp, dt, s) != hipSuccess) return MOE_ERR_HIP;
     if (launch_ffn_act_grad(p, dt, s) != hipSuccess) return MOE_ERR_HIP;
     if (g->x && launch_ffn_row_grad(p, dt, s) != hipSuccess) return MOE_ERR_HIP;
@@ -364,6 +384,8 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
         q.dw_part = p.dw_part;
         q.dw_tiles = p.dw_tiles;
         q.dxs = p.dxs;
+        q.slot_of = rp.pad_slot;
+        q.shared_base = 0;
         if (launch_router_grad(q, dt, s) != hipSuccess) return MOE_ERR_HIP;
     }
     return MOE_OK;

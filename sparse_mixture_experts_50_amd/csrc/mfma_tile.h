@@ -19,124 +19,116 @@
 // fall on the same banks, so they are XOR-swizzled by k.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace mt {
 
 constexpr int SK = 64;                   // stage depth
 
+// What is known of a tile's number of stages (ANY: maybe none).
+enum Stages { EVEN, ODD, ANY };
+
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ void dma16(const char *src, u32x4 *lds) {
+// 64 lanes' 16 bytes at base (uniform) + off (the lane's) to LDS.
+__device__ __forceinline__ void dma16(uint64_t base, uint32_t off, u32x4 *lds) {
+    typedef const __attribute__((address_space(1))) char *gptr;
     __builtin_amdgcn_global_load_lds(
-        (const void *)src, (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+        (const __attribute__((address_space(1))) void *)((gptr)base + off),
+        (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
 }
 
-// s_waitcnt vmcnt(n) only.
-template <int N> __device__ __forceinline__ void wait_vmcnt() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+// The same from any address of the lane's.
+__device__ __forceinline__ void dma16_lanes(const char *src, u32x4 *lds) {
+    __builtin_amdgcn_global_load_lds(
+        (const void *)src, (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
 }
 
 __device__ __forceinline__ void mfma(floatx4 &acc, const bf16x8 &a, const bf16x8 &b) {
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 
-// A zeroed line that lanes past the end of a K_FIRST operand read from.
-static __device__ __align__(1024) const char zero_line[1024] = {};
-
-// One operand of a tile.  base: element (0, 0) of the tile (uniform); ld:
-// bytes.  K_LAST: rows >= valid re-read row 0.  K_FIRST: columns >= valid
-// (a multiple of 8) re-read column 0, and rows of k >= kvalid are zero.
-// base2: second panel (K_LAST B of a gated product).
-struct Operand {
-    const char *base, *base2;
-    size_t ld;
-    int valid, kvalid;
-};
-
-// W rows (columns) of one operand in a slot, PANELS of them: the addresses
-// of its loads and of a wave's NQ fragments (of one panel).  ZK: K is ragged
-// (kvalid holds).
-template <bool KF, int W, int PANELS, int NQ, bool ZK>
-struct Side {
+// W rows (columns) of one operand in a slot from unit U0 on, PANELS of them:
+// a wave's loads of a stage.  A load's address is a uniform base, one per
+// operand and stage, and a 32-bit lane offset that stays in a register for
+// the whole kernel: with one wave per SIMD an MFMA leaves issue slots for
+// about three other instructions, and address arithmetic would take them.
+template <bool KF, int W, int PANELS, int U0>
+struct Loader {
     static constexpr int UNITS = W * 8 * PANELS;     // 16-byte units a stage
     static constexpr int LOADS = UNITS / 256;        // per wave and stage
     static constexpr int PER = W / 32;               // loads of one panel
-    static constexpr int READS = KF ? 2 : 1;         // per fragment
     static constexpr int CPK = W / 8;                // K_FIRST: chunks per k
     static constexpr int KSTEP = 256 / CPK;          // K_FIRST: k per load
     static_assert(!KF || ((W == 64 || W == 128 || W == 256) && PANELS == 1), "");
     static_assert(W % 32 == 0, "whole loads");
 
-    const char *base, *base2;
-    size_t ld;
-    uint32_t off[KF ? 2 : PER];
-    int kl, kvalid;
+    uint32_t off[PER];
 
     // the swizzle of k row k, in 32-byte pieces
     static __device__ __forceinline__ int swz(int k) {
         return W == 64 ? ((k >> 1) & 1) | ((k >> 2) & 2) : (k & 3) | ((k >> 1) & 4);
     }
 
-    __device__ __forceinline__ void init(const Operand &o, int wave, int lane) {
-        base = o.base;
-        base2 = PANELS > 1 ? o.base2 : o.base;
-        ld = o.ld;
-        kvalid = ZK ? o.kvalid : 0;
-        if (KF) {
-            kl = (wave * 64 + lane) / CPK;           // + KSTEP q
-            const int cs = lane % CPK;
+    // ld: bytes between rows (of k: K_FIRST); valid < W: rows (K_FIRST:
+    // columns, a multiple of 8) from valid on re-read the first
+    __device__ __forceinline__ void init(uint32_t ld, int valid, int wave, int lane) {
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {            // even and odd loads
-                const int f = swz(kl + v * KSTEP);
-                int c = ((cs >> 1) ^ f) * 2 + (cs & 1);
-                if (c * 8 >= o.valid) c = 0;
-                off[v] = (uint32_t)(kl * (uint32_t)ld + c * 16);
-            }
-        } else {
-            kl = 0;
-            const int lr = lane >> 3;
-            const int ch = (lane & 7) ^ ((4 * wave + (lr >> 1)) & 7);
-#pragma unroll
-            for (int q = 0; q < PER; ++q) {
+        for (int q = 0; q < PER; ++q) {
+            if (KF) {
+                const int k = (wave * 64 + lane) / CPK + KSTEP * q;
+                const int cs = lane % CPK;
+                int c = ((cs >> 1) ^ swz(k)) * 2 + (cs & 1);
+                if (c * 8 >= valid) c = 0;
+                off[q] = (uint32_t)k * ld + (uint32_t)(c * 16);
+            } else {
+                const int lr = lane >> 3;
+                const int ch = (lane & 7) ^ ((4 * wave + (lr >> 1)) & 7);
                 int rr = (wave + 4 * q) * 8 + lr;
-                if (rr >= o.valid) rr = 0;
-                off[KF ? 0 : q] = (uint32_t)(rr * (uint32_t)ld + ch * 16);
+                if (rr >= valid) rr = 0;
+                off[q] = (uint32_t)rr * ld + (uint32_t)(ch * 16);
             }
         }
     }
-
-    // load q of stage s into the slot's part of this operand (at unit u0)
-    __device__ __forceinline__ void load(int s, int q, u32x4 *st, int u0, int wave) const {
-        if (KF) {
-            const int k0 = s * SK + q * KSTEP;
-            const char *p = base + (size_t)k0 * ld + off[q & 1];
-            if (ZK && k0 + kl >= kvalid) p = zero_line + (threadIdx.x & 63) * 16;
-            dma16(p, st + (u0 + (q * 4 + wave) * 64));
-        } else {
-            const char *b = PANELS > 1 && q >= PER ? base2 : base;
-            dma16(b + (size_t)s * (SK * 2) + off[KF ? 0 : q % PER],
-                  st + (u0 + (wave + 4 * q) * 64));
-        }
+    // bytes from a stage to the next
+    static __device__ __forceinline__ uint32_t step(uint32_t ld) {
+        return KF ? SK * ld : SK * 2;
     }
+    // load q of the stage at base (and base2, the second panel's)
+    __device__ __forceinline__ void load(uint64_t base, uint64_t base2, int q, u32x4 *st,
+                                         int wave) const {
+        uint32_t o = off[q % PER];
+        // opaque: else the offsets, widened to 64 bits, are kept as well
+        asm("" : "+v"(o));
+        dma16(PANELS > 1 && q >= PER ? base2 : base, o,
+              st + (U0 + (KF ? q * 4 + wave : wave + 4 * q) * 64));
+    }
+};
 
-    // Slot index of this lane's part of fragment q (16 rows from row
-    // r0 + 16 q) at sub-step 0, in reads (8 bytes for K_FIRST, else 16),
-    // K_LAST: for both sub-steps.  Opaque, so that a read is one index off
-    // the slot: through longer address arithmetic the compiler loses track
-    // of which slot is read, and waits for every load in flight.
+// A wave's NQ fragments (16 rows each from row r0 on) of one operand (of
+// one panel).
+template <bool KF, int W, int U0, int NQ>
+struct Reader {
+    static constexpr int READS = KF ? 2 : 1;         // per fragment
+    // Slot index of this lane's part of fragment q at sub-step 0, in reads
+    // (8 bytes for K_FIRST, else 16); K_LAST: of fragment 0, both sub-steps.
+    // Opaque, so that a read is one index off the slot: through longer
+    // address arithmetic the compiler loses track of which slot is read, and
+    // waits for every load in flight.
     int rd[KF ? NQ : 2];
-    __device__ __forceinline__ void init_reads(int u0, int r0, int lane) {
+    __device__ __forceinline__ void init(int r0, int lane) {
         const int l16 = lane & 15, b = lane >> 4;
 #pragma unroll
         for (int q = 0; q < (KF ? NQ : 2); ++q) {
             if (KF) {
                 const int k = 8 * b + (l16 >> 2);
-                rd[q] = u0 * 2 + k * (W / 4) + ((((r0 >> 4) + q) ^ swz(k)) * 4) + (l16 & 3);
+                rd[q] = U0 * 2 + k * (W / 4) +
+                        ((((r0 >> 4) + q) ^ (Loader<KF, W, 1, U0>::swz(k))) * 4) + (l16 & 3);
             } else {
-                rd[q] = u0 + (r0 + l16) * 8 + ((q * 4 + b) ^ ((l16 >> 1) & 7));
+                rd[q] = U0 + (r0 + l16) * 8 + ((q * 4 + b) ^ ((l16 >> 1) & 7));
             }
             asm("" : "+v"(rd[q]));
         }
@@ -159,73 +151,125 @@ struct Side {
     }
 };
 
-// A tile of WM x WN waves of RB x TN 16 x 16 blocks (times B's PANELS).
-template <int RB, int TN, int WM, int WN, int PANELS, bool AF, bool BF, bool ZK,
-          bool ODD>
-struct Product {
+// Tiles of up to BM x BN (times B's PANELS), WM x WN waves.  SPLIT: the sum
+// of two products one after the other.
+template <int BM, int BN, int WM, int WN, int PANELS, bool AF, bool BF, bool SPLIT = false>
+struct Tiles {
     static_assert(WM * WN == 4, "four waves");
-    static constexpr int BM = RB * 16 * WM, BN = TN * 16 * WN;
-    typedef Side<AF, BM, 1, RB, ZK> SA;
-    typedef Side<BF, BN, PANELS, TN, ZK> SB;
-    static constexpr int STAGE = SA::UNITS + SB::UNITS;
-    static constexpr int NC = TN * PANELS;           // column blocks a wave
-    static constexpr int NM = RB * NC;               // MFMAs per sub-step
-    static constexpr int NA = RB * SA::READS, NR = NA + NC * SB::READS;
-    static constexpr int NL = SA::LOADS + SB::LOADS;
-    // reads go between the first three quarters of the MFMAs, loads between
-    // all of them
-    // (item z of n in `span` slots goes to slot z * span / n; first(q) is
-    // the first item at or after slot q)
-    static constexpr int RSPAN = NM * 3 / 4;
+    static constexpr int TN = BN / 16 / WN, NC = TN * PANELS;   // column blocks a wave
+    typedef Loader<AF, BM, 1, 0> LA;
+    typedef Loader<BF, BN, PANELS, LA::UNITS> LB;
+    static constexpr int STAGE = LA::UNITS + LB::UNITS;
+
+    // The operands of one tile: element (0, 0) of each (uniform).  SPLIT:
+    // a2, b2 of the second product; PANELS 2: b2 of the second panel.  kt:
+    // stages (maybe 0; a stage's worth of either operand can be read all the
+    // same).
+    struct Source {
+        uint64_t a, b, a2, b2;
+        int kt;
+    };
+    // What the loads of every tile share.
+    struct Lanes {
+        LA a;
+        LB b;
+        uint32_t step_a, step_b;
+        int split;                      // stages of the first product
+        __device__ __forceinline__ void init(uint32_t lda, int valid_a, uint32_t ldb,
+                                             int valid_b, int wave, int lane) {
+            a.init(lda, valid_a, wave, lane);
+            b.init(ldb, valid_b, wave, lane);
+            step_a = LA::step(lda);
+            step_b = LB::step(ldb);
+        }
+    };
+    // A stage to load: the bases of its loads.  (Past the last stage, the
+    // last again.)
+    struct Stage {
+        uint64_t a, b, b2;
+        __device__ __forceinline__ void set(const Source &src, const Lanes &ln, int s) {
+            s = max(min(s, src.kt - 1), 0);
+            const bool second = SPLIT && s >= ln.split;
+            const int n = second ? s - ln.split : s;
+            a = (second ? src.a2 : src.a) + (uint64_t)n * ln.step_a;
+            b = (second ? src.b2 : src.b) + (uint64_t)n * ln.step_b;
+            b2 = PANELS > 1 ? src.b2 + (uint64_t)n * ln.step_b : b;
+            // opaque: else the compiler adds lane offset and first base ahead
+            // of the loop, and the rest by 64-bit vector additions in it
+            asm("" : "+s"(a), "+s"(b));
+            if (PANELS > 1) asm("" : "+s"(b2));
+        }
+    };
+    // load l of a stage of RBA 32-row parts of A (of BM / 32) and all of B
+    template <int RBA>
+    static __device__ __forceinline__ void load(const Stage &g, const Lanes &ln, int l,
+                                                u32x4 *st, int wave) {
+        if (l < RBA) ln.a.load(g.a, g.a, l, st, wave);
+        else ln.b.load(g.b, g.b2, l - RBA, st, wave);
+    }
+    // Asks for stage s at once.
+    static __device__ __forceinline__ void load_stage(const Source &src, const Lanes &ln,
+                                                      int s, u32x4 *st, int wave) {
+        Stage g;
+        g.set(src, ln, s);
+#pragma unroll
+        for (int l = 0; l < LA::LOADS + LB::LOADS; ++l) load<LA::LOADS>(g, ln, l, st, wave);
+    }
+
+    // item z of n in `span` slots goes to slot z * span / n; first(q) is the
+    // first item at or after slot q
     static constexpr int first(int q, int n, int span) {
         const int z = (q * n + span - 1) / span;
         return z < n ? z : n;
     }
-    static constexpr int MAXR = (NR + RSPAN - 1) / RSPAN;
-    static constexpr int MAXL = (NL + NM - 1) / NM;
 
-    // acc += A B over KT stages.  Leaves loads in flight and both slots in
-    // use: wait and barrier before using the slots for anything else.
-    static __device__ __forceinline__ void run(floatx4 (&acc)[RB][NC], const Operand &oa,
-                                               const Operand &ob, u32x4 *slot0,
-                                               u32x4 *slot1, int KT, int wave,
-                                               int lane) {
-        if (KT <= 0) return;
+    // acc += A B of a tile of RB 16-row blocks per wave over its src.kt
+    // stages, the first two of which have been asked for into slot0 and slot1
+    // (by load_stage(), or by this function for the tile before): while the
+    // last two are worked on, the first two of `next` are loaded.
+    // RBA: 32-row parts of A that the tile's rows need.  KIND: of src.kt.
+    template <int RB, int RBA, Stages KIND>
+    static __device__ __forceinline__ void run(floatx4 (&acc)[RB][NC], const Source &src,
+                                               const Lanes &ln, const Source &next,
+                                               const Lanes &lnext, u32x4 *slot0,
+                                               u32x4 *slot1, int wave, int lane) {
+        typedef Reader<AF, BM, 0, RB> RA;
+        typedef Reader<BF, BN, LA::UNITS, TN> RBd;
+        constexpr int NM = RB * NC;                      // MFMAs per sub-step
+        constexpr int NA = RB * RA::READS, NR = NA + NC * RBd::READS;
+        // reads go between the first three quarters of the MFMAs, loads
+        // between all of them
+        constexpr int RSPAN = NM * 3 / 4, MAXR = (NR + RSPAN - 1) / RSPAN;
         const int wm = wave / WN, wn = wave % WN;
-        SA a;
-        SB b;
-        a.init(oa, wave, lane);
-        b.init(ob, wave, lane);
-        a.init_reads(0, wm * RB * 16, lane);
-        b.init_reads(SA::UNITS, wn * TN * 16, lane);
-        auto load = [&](int s, u32x4 *st, int q) __attribute__((always_inline)) {
-            if (q < SA::LOADS) a.load(s, q, st, 0, wave);
-            else b.load(s, q - SA::LOADS, st, SA::UNITS, wave);
-        };
+        RA a;
+        RBd b;
+        a.init(wm * RB * 16, lane);
+        b.init(wn * TN * 16, lane);
         auto read = [&](bf16x8 (&fa)[RB], bf16x8 (&fb)[NC], const u32x4 *st, int kk,
                         int r) __attribute__((always_inline)) {
             if (r < NA) {
-                const int q = r / SA::READS;
-                a.read(fa[q], st, kk, q, q * 16, r % SA::READS);
+                const int q = r / RA::READS;
+                a.read(fa[q], st, kk, q, q * 16, r % RA::READS);
             } else {
-                const int q = (r - NA) / SB::READS;
+                const int q = (r - NA) / RBd::READS;
                 b.read(fb[q], st, kk, q % TN, (q / TN) * BN + (q % TN) * 16,
-                       (r - NA) % SB::READS);
+                       (r - NA) % RBd::READS);
             }
         };
         bf16x8 fa0[RB], fb0[NC], fa1[RB], fb1[NC];
         __builtin_amdgcn_s_waitcnt(0);
         __builtin_amdgcn_s_barrier();
 #pragma unroll
-        for (int q = 0; q < NL; ++q) load(0, slot0, q);
-#pragma unroll
-        for (int q = 0; q < NL; ++q) load(min(1, KT - 1), slot1, q);
-        wait_vmcnt<NL>();
-        __builtin_amdgcn_s_barrier();
-#pragma unroll
         for (int r = 0; r < NR; ++r) read(fa0, fb0, slot0, 0, r);
 
-        auto stage = [&](int s, u32x4 *cur, u32x4 *nxt) __attribute__((always_inline)) {
+        // Stage in cur: its sub-step 0 on fa0 while the other half is read
+        // into fa1, then sub-step 1 while nxt's first half is read into fa0
+        // (unless LAST) and stage g is loaded into cur.
+        auto stage = [&](const Stage &g, const Lanes &gl, u32x4 *cur, u32x4 *nxt, auto last,
+                         auto parts) __attribute__((always_inline)) {
+            constexpr bool LAST = decltype(last)::value;
+            constexpr int NL = decltype(parts)::value + LB::LOADS;
+            constexpr int MAXL = (NL + NM - 1) / NM;
             __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
 #pragma unroll
             for (int q = 0; q < NM; ++q) {
@@ -235,34 +279,61 @@ struct Product {
                     if (first(q, NR, RSPAN) + u < first(q + 1, NR, RSPAN))
                         read(fa1, fb1, cur, 1, first(q, NR, RSPAN) + u);
             }
-            // own reads done, stage s + 1 landed, then every wave's part
+            // own reads done, the next stage landed, then every wave's part
             __builtin_amdgcn_s_waitcnt(0x0 | (0x7 << 4));
             __builtin_amdgcn_s_barrier();
-            const int nx = min(s + 2, KT - 1);
 #pragma unroll
             for (int q = 0; q < NM; ++q) {
                 mfma(acc[q / NC][q % NC], fb1[q % NC], fa1[q / NC]);
+                if (!LAST) {
 #pragma unroll
-                for (int u = 0; u < MAXR; ++u)
-                    if (first(q, NR, RSPAN) + u < first(q + 1, NR, RSPAN))
-                        read(fa0, fb0, nxt, 0, first(q, NR, RSPAN) + u);
+                    for (int u = 0; u < MAXR; ++u)
+                        if (first(q, NR, RSPAN) + u < first(q + 1, NR, RSPAN))
+                            read(fa0, fb0, nxt, 0, first(q, NR, RSPAN) + u);
+                }
 #pragma unroll
                 for (int u = 0; u < MAXL; ++u)
                     if (first(q, NL, NM) + u < first(q + 1, NL, NM))
-                        load(nx, cur, first(q, NL, NM) + u);
+                        load<decltype(parts)::value>(g, gl, first(q, NL, NM) + u, cur, wave);
             }
         };
+        typedef std::integral_constant<int, RBA> Part;
+        typedef std::integral_constant<int, LA::LOADS> Whole;
+        Stage g, h;
         // wait states that the compiler does not know the asm needs: before
         // the first MFMA (a VALU write of its accumulator) and after the
         // last (a read of its result)
-        // ODD: KT may be odd.  (A way round the loop that skips a stage
-        // leaves loads into slot0 to be waited for at its head.)
-        for (int s = 0; s < KT; s += 2) {
+        const int kt = src.kt;
+        for (int s = 0; s + 2 < kt; s += 2) {
+            g.set(src, ln, s + 2);
+            h.set(src, ln, s + 3);
             asm volatile("s_nop 4");
-            stage(s, slot0, slot1);
-            if (!ODD || s + 1 < KT) stage(s + 1, slot1, slot0);
+            stage(g, ln, slot0, slot1, std::false_type{}, Part{});
+            stage(h, ln, slot1, slot0, std::false_type{}, Part{});
             asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7");
         }
+        g.set(next, lnext, 0);
+        h.set(next, lnext, 1);
+        if (KIND != ANY || kt > 0) {
+            asm volatile("s_nop 4");
+            stage(g, lnext, slot0, slot1, std::integral_constant<bool, KIND == ODD>{}, Whole{});
+            asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7");
+        } else {
+#pragma unroll
+            for (int l = 0; l < LA::LOADS + LB::LOADS; ++l)
+                load<LA::LOADS>(g, lnext, l, slot0, wave);
+        }
+        if (KIND == EVEN || (KIND == ANY && kt > 0 && (kt & 1) == 0)) {
+            asm volatile("s_nop 4");
+            stage(h, lnext, slot1, slot0, std::true_type{}, Whole{});
+            asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7");
+        } else {
+#pragma unroll
+            for (int l = 0; l < LA::LOADS + LB::LOADS; ++l)
+                load<LA::LOADS>(h, lnext, l, slot1, wave);
+        }
+        // nothing that reads the results moves above the wait states
+        __builtin_amdgcn_sched_barrier(0);
     }
 };
 

@@ -269,19 +269,28 @@ __global__ __launch_bounds__(256) void router_grad_x_f32(RouterGradParams p) {
 // k fp32 rows a token, are what takes its time.
 template <int KS>                              // 64-deep stages: ep / 64
 __global__ __launch_bounds__(256) void router_grad_x_bf16(RouterGradParams p) {
-    typedef mt::Side<true, 64, 1, 4, true> SB;
-    __shared__ u32x4 slot[KS * SB::UNITS];
+    typedef mt::Loader<true, 64, 1, 0> LB;
+    __shared__ u32x4 slot[KS * LB::UNITS];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t0 = blockIdx.x * 64 + wave * 16, c0 = blockIdx.y * 64;
-    SB b;
-    b.init({(const char *)((const uint16_t *)p.wr + c0), nullptr, (size_t)p.d * 2, 64, p.E},
-           wave, lane);
-    b.init_reads(0, 0, lane);
+    LB lb;
+    mt::Reader<true, 64, 0, 4> b;
+    b.init(0, lane);
+    // (rows past E, where dl is zero: the router's first again)
+    {
+        const uint64_t wr = (uint64_t)((const uint16_t *)p.wr + c0);
+        lb.init(p.d * 2, 64, wave, lane);
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int q = 0; q < SB::LOADS; ++q) b.load(s, q, slot, s * SB::UNITS, wave);
+            for (int q = 0; q < LB::LOADS; ++q) {
+                const int e = s * 64 + (wave * 64 + lane) / 8 + 32 * q;
+                const uint32_t back = e < p.E ? 0 : (uint32_t)e * (uint32_t)p.d * 2;
+                mt::dma16(wr, lb.off[q] + (uint32_t)s * 128u * (uint32_t)p.d - back,
+                          slot + s * LB::UNITS + (q * 4 + wave) * 64);
+            }
+    }
     const int t = t0 + (lane & 15);
     const uint16_t *dl = (const uint16_t *)p.dl + (size_t)min(t, p.T - 1) * p.ep +
                          8 * (lane >> 4);
@@ -301,8 +310,8 @@ __global__ __launch_bounds__(256) void router_grad_x_bf16(RouterGradParams p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             bf16x8 fb = {};
-            b.read(fb, slot + (k >> 1) * SB::UNITS, k & 1, j, 0, 0);
-            b.read(fb, slot + (k >> 1) * SB::UNITS, k & 1, j, 0, 1);
+            b.read(fb, slot + (k >> 1) * LB::UNITS, k & 1, j, 0, 0);
+            b.read(fb, slot + (k >> 1) * LB::UNITS, k & 1, j, 0, 1);
             acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fa[k], acc[j], 0, 0, 0);
         }
     if (t >= p.T) return;
@@ -330,23 +339,52 @@ __global__ __launch_bounds__(256) void router_grad_w_f32(RouterGradParams p) {
     });
 }
 
+static __device__ __align__(1024) const char zero_line[1024] = {};
+
 // 64 experts x 256 columns on the matrix cores, both operands along tokens.
 __global__ __launch_bounds__(256, 2) void router_grad_w_bf16(RouterGradParams p) {
-    typedef mt::Product<4, 4, 1, 4, 1, true, true, true, true> P;
+    typedef mt::Tiles<64, 256, 1, 4, 1, true, true> P;
     __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int e0 = blockIdx.x * P::BM, c0 = blockIdx.y * P::BN;
+    const int e0 = blockIdx.x * 64, c0 = blockIdx.y * 256;
     const int per = (p.T + p.splits - 1) / p.splits;
     const int t0 = blockIdx.z * per;
-    const int n = min(per, p.T - t0);       // may be <= 0: zeros
-    const mt::Operand a = {(const char *)((const uint16_t *)p.dl + (size_t)t0 * p.ep + e0),
-                           nullptr, (size_t)p.ep * 2, P::BM, n};
-    const mt::Operand b = {(const char *)((const uint16_t *)p.x + (size_t)t0 * p.d + c0),
-                           nullptr, (size_t)p.d * 2, min(P::BN, p.d - c0), n};
+    const int n = max(0, min(per, p.T - t0));       // may be 0: zeros
+    // stage 0 holds what the whole stages of 64 tokens leave over
+    const int over = n % mt::SK, head = over ? over : min(n, mt::SK);
+    const uint16_t *A = (const uint16_t *)p.dl + (size_t)t0 * p.ep + e0;
+    const uint16_t *B = (const uint16_t *)p.x + (size_t)t0 * p.d + c0;
+    P::Source src;
+    src.a = src.a2 = (uint64_t)A + ((int64_t)head - mt::SK) * p.ep * 2;
+    src.b = src.b2 = (uint64_t)B + ((int64_t)head - mt::SK) * p.d * 2;
+    src.kt = (n + mt::SK - 1) / mt::SK;
+    P::Lanes ln;
+    ln.init(p.ep * 2, 64, p.d * 2, min(256, p.d - c0), wave, lane);
+    ln.split = 0;
+    auto head_load = [&](const void *base, uint32_t off, int k, u32x4 *to) __attribute__((always_inline)) {
+        const char *from = (const char *)base + off;
+        if (k >= head) from = zero_line + lane * 16;
+        mt::dma16_lanes(from, to);
+    };
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        head_load(A, ln.a.off[q], (wave * 64 + lane) / 8 + 32 * q, slot0 + (q * 4 + wave) * 64);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        head_load(B, ln.b.off[q], (wave * 64 + lane) / 32 + 8 * q,
+                  slot0 + (P::LA::UNITS + (q * 4 + wave) * 64));
+    // no stage after the last: every lane a zeroed line (x may end anywhere)
+    P::Source none;
+    none.a = none.a2 = none.b = none.b2 = (uint64_t)zero_line;
+    none.kt = 0;
+    P::Lanes still = {};
+    if (src.kt > 1) P::load_stage(src, ln, 1, slot1, wave);
+    else P::load_stage(none, still, 1, slot1, wave);
     floatx4 acc[4][4];
     mt::clear(acc);
-    P::run(acc, a, b, slot0, slot1, n > 0 ? (n + mt::SK - 1) / mt::SK : 0, wave, lane);
+    P::run<4, 2, mt::ANY>(acc, src, ln, none, still, slot0, slot1, wave, lane);
+    __builtin_amdgcn_s_waitcnt(0);
     const int c = c0 + wave * 64 + 4 * (lane >> 4);
     if (c0 + wave * 64 >= p.d) return;
 #pragma unroll

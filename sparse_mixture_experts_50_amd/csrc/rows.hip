@@ -59,16 +59,22 @@ __device__ __forceinline__ float lane_f(float v, int l) {
 }
 
 // Calls body(slot, weight, j) for the token's kept assignments, j ascending.
-// W: whether the weights are needed.
-template <bool W, typename F>
+// W: whether the weights are needed.  PAD: slots of the padded space, which
+// are also kept in pad_slot (by one wave of the token's: keep).
+template <bool W, bool PAD = false, typename F>
 __device__ __forceinline__ void each_kept(const RowsParams &p, int t, int lane,
-                                          F body) {
+                                          F body, bool keep = false) {
     const int32_t *so = p.slot_of + (size_t)t * p.k;
     const float *tw = W ? p.topk_w + (size_t)t * p.k : nullptr;
     for (int j0 = 0; j0 < p.k; j0 += 64) {
         const int j = j0 + lane;
-        const int s = j < p.k ? so[j] : -1;
+        int s = j < p.k ? so[j] : -1;
         const float w = W && j < p.k ? tw[j] : 0.0f;
+        if (PAD && j < p.k) {
+            const int e = p.topk_idx ? p.topk_idx[(size_t)t * p.k + j] : j;
+            if (s >= 0) s += p.pad[e] - p.offsets[e];
+            if (keep) p.pad_slot[(size_t)t * p.k + j] = s;
+        }
         unsigned long long m = __ballot(s >= 0);
         while (m) {
             const int l = __builtin_ctzll(m);
@@ -89,6 +95,7 @@ __device__ __forceinline__ bool wave_span(const RowsParams &p, int nv, int &t,
     return t < p.T;
 }
 
+// TWO: x and dy into the gradient's padded row space, with the row weights.
 template <typename T, int S, bool TWO>
 __global__ __launch_bounds__(WAVES * 64) void dispatch_rows(RowsParams p) {
     const int lane = threadIdx.x & 63;
@@ -117,12 +124,9 @@ __global__ __launch_bounds__(WAVES * 64) void dispatch_rows(RowsParams p) {
                 if (TWO) o2[v] = qb[i];
             }
         }
-        if (p.row_w && v0 == 0 && lane == 0) p.row_w[row] = w;
+        if (TWO && v0 == 0 && lane == 0) p.row_w[row] = w;
     };
-    if (p.row_w)
-        each_kept<true>(p, t, lane, [&](int s, float w, int) { write(s, w); });
-    else
-        each_kept<false>(p, t, lane, [&](int s, float w, int) { write(s, w); });
+    each_kept<TWO, TWO>(p, t, lane, [&](int s, float w, int) { write(s, w); }, v0 == 0);
     if (p.n_shared) write(p.shared_base + t, 1.0f);
 }
 
