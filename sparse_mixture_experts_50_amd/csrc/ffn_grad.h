@@ -38,4 +38,7 @@ inline long long ffn_row_tiles(const FfnGradParams &p, int bm) {
 hipError_t launch_act_grad_mfma(const FfnGradParams &p, hipStream_t s);
 hipError_t launch_row_grad_mfma(const FfnGradParams &p, hipStream_t s);
 hipError_t launch_weight_grad_mfma(const FfnGradParams &p, hipStream_t s);
-int mfma_dw_tiles(int d_ff, int act);
+// Whether the routed groups have few rows each (another choice of tiles).
+bool mfma_few_rows(long long routed, int E);
+int mfma_dw_tiles(int d_ff, int act, bool few);
+int mfma_splits(long long routed, int E, int shared_rows, int N, int K);

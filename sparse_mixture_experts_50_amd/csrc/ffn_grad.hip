@@ -315,8 +315,18 @@ hipError_t launch_pad_groups(const PadParams &p, int dtype, hipStream_t s) {
     return hipGetLastError();
 }
 
-int ffn_grad_dw_tiles(int dtype, int d_ff, int act) {
-    return dtype == 1 ? mfma_dw_tiles(d_ff, act) : d_ff / 32;
+int ffn_grad_q_splits(int dtype, long long routed, int E, int shared_rows, int d, int d_ff) {
+    return dtype == 1 ? mfma_splits(routed, E, shared_rows, d_ff, d) : 1;
+}
+int ffn_grad_dx_splits(int dtype, long long routed, int E, int shared_rows, int d, int d_ff,
+                       int act) {
+    return dtype == 1 ? mfma_splits(routed, E, shared_rows, d,
+                                    act == ACT_SWIGLU ? 2 * d_ff : d_ff)
+                      : 1;
+}
+
+int ffn_grad_dw_tiles(int dtype, int d_ff, int act, long long routed, int E) {
+    return dtype == 1 ? mfma_dw_tiles(d_ff, act, mfma_few_rows(routed, E)) : d_ff / 32;
 }
 
 hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype,

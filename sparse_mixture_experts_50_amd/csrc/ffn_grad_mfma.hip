@@ -82,6 +82,20 @@ __device__ __forceinline__ void store_rows(u32x4 *scr, int u0, const float (&v)[
     __builtin_amdgcn_wave_barrier();
 }
 
+// The same without LDS, in pieces of 32 bytes a row.
+template <int TN>
+__device__ __forceinline__ void store_pieces(const float (&v)[TN][4], bf16 *out, size_t ld,
+                                             int lo, int hi, int lane) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+        u32x2 o;
+        o.x = pack_bf16x2(v[j][0], v[j][1]);
+        o.y = pack_bf16x2(v[j][2], v[j][3]);
+        if (16 * j >= lo && 16 * j < hi)
+            *(u32x2 *)(out + (size_t)(lane & 15) * ld + 16 * j + 4 * (lane >> 4)) = o;
+    }
+}
+
 // The tile of round r: persistent blocks, each XCD (block index mod 8)
 // taking consecutive tiles.
 __device__ __forceinline__ int tile_of(int r) {
@@ -103,13 +117,14 @@ __device__ __forceinline__ int split_blocks(int rows) {
 struct RowTile {
     int g, row0, nrows, rb, n_tile;
 };
+template <bool SMALL>
 __device__ __forceinline__ RowTile row_tile(const TileTable &tt, int G, int L) {
     RowTile r;
     r.g = __builtin_amdgcn_readfirstlane(find_group(tt, G, L));
     const int local = L - __builtin_amdgcn_readfirstlane(tt.base[r.g]);
     const int mt = __builtin_amdgcn_readfirstlane(tt.mt[r.g]);
     const int rows = __builtin_amdgcn_readfirstlane(tt.rows[r.g]);
-    r.rb = split_blocks(rows);
+    r.rb = SMALL ? 2 : split_blocks(rows);
     r.n_tile = local / mt;
     const int m = local - r.n_tile * mt;
     r.row0 = __builtin_amdgcn_readfirstlane(tt.start[r.g]) + m * 32 * r.rb;
@@ -118,8 +133,9 @@ __device__ __forceinline__ RowTile row_tile(const TileTable &tt, int G, int L) {
 }
 
 // f(integral_constant<rb>)
-template <typename F> __device__ __forceinline__ void by_height(int rb, F f) {
-    if (rb == 8) f(std::integral_constant<int, 8>{});
+template <bool SMALL, typename F> __device__ __forceinline__ void by_height(int rb, F f) {
+    if (SMALL) f(std::integral_constant<int, 2>{});
+    else if (rb == 8) f(std::integral_constant<int, 8>{});
     else if (rb == 7) f(std::integral_constant<int, 7>{});
     else if (rb == 6) f(std::integral_constant<int, 6>{});
     else if (rb == 4) f(std::integral_constant<int, 4>{});
@@ -141,61 +157,92 @@ __device__ __forceinline__ int tile_start(int i, int size, int n) {
     return n >= size ? min(i * size, n - size) : 0;
 }
 
+// Tiles and slots of the kernels below.  SMALL: for groups of few rows, whose
+// products stream the weights once: small tiles, several blocks per CU, more
+// loads in flight.
+template <bool SMALL> struct Shape {
+    static constexpr int BM = SMALL ? 64 : 256, BN = SMALL ? 128 : 256;
+    static constexpr int SLOTS = SMALL ? 3 : 2, BLOCKS = SMALL ? 2 : 1;
+};
+
+// Keeps the slots' first stages coming: run() through two slots, run_ring()
+// through three.
+template <typename P, bool SMALL, int RB, mt::Stages KIND, int NC>
+__device__ __forceinline__ void run_tile(floatx4 (&acc)[RB][NC], const typename P::Source &src,
+                                         const typename P::Source &next,
+                                         const typename P::Lanes &ln, u32x4 *slot0,
+                                         u32x4 *slot1, u32x4 *slot2, int wave, int lane) {
+    if constexpr (SMALL) {
+        u32x4 *const slot[3] = {slot0, slot1, slot2};
+        P::template run_ring<RB, 3>(acc, src, ln, next, ln, slot, wave, lane);
+    } else {
+        P::template run<RB, RB, KIND>(acc, src, ln, next, ln, slot0, slot1, wave, lane);
+    }
+}
+
 // out[rows][N] (fp32) = the sum of one or two products A B of a group's rows
 // with its weights, stored along K.  Q: q = dy W2; else dx = dz W1 + du W3
-// (GATED).
-template <bool Q, bool GATED, mt::Stages KIND>
-__global__ __launch_bounds__(256, 1) void ffn_rows_by_weights(FfnGradParams p) {
-    typedef mt::Tiles<256, 256, 2, 2, 1, false, true, GATED> P;
+// (GATED).  SMALL: over one of `splits` ranges of K, each to a plane of its
+// own.
+template <bool Q, bool GATED, mt::Stages KIND, bool SMALL>
+__global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_rows_by_weights(FfnGradParams p) {
+    constexpr int BM = Shape<SMALL>::BM, BN = Shape<SMALL>::BN;
+    typedef mt::Tiles<BM, BN, 2, 2, 1, false, true, GATED> P;
     constexpr int TN = P::TN;
-    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], slot2[SMALL ? P::STAGE : 1];
     __shared__ TileTable tt;
     const int G = p.E + p.n_shared;
     const int N = Q ? p.d_ff : p.d, K = Q ? p.d : p.d_ff;
-    build_tile_table(tt, p.offsets, p.E, p.n_shared, 0, p.T, 256, (N + 255) / 256);
-    const int total = __builtin_amdgcn_readfirstlane(tt.base[G]);
+    build_tile_table(tt, p.offsets, p.E, p.n_shared, 0, p.T, BM, (N + BN - 1) / BN);
+    const int splits = !SMALL ? 1 : Q ? p.q_splits : p.dx_splits;
+    const int tiles = __builtin_amdgcn_readfirstlane(tt.base[G]), total = tiles * splits;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / 2, wn = wave % 2;
-    const int kt = (GATED ? 2 : 1) * K / mt::SK;
+    const int kt = (GATED ? 2 : 1) * K / mt::SK, per = (kt + splits - 1) / splits;
     const size_t mat = (size_t)p.d_ff * p.d;
-    auto source = [&](const RowTile &t) __attribute__((always_inline)) {
-        const int n0 = tile_start(t.n_tile, 256, N);
+    auto source = [&](const RowTile &t, int split) __attribute__((always_inline)) {
+        const int n0 = tile_start(t.n_tile, BN, N);
         const size_t at = (size_t)t.row0 * K;
         typename P::Source s;
         s.a = (uint64_t)((const bf16 *)(Q ? p.dys : p.dz) + at);
         s.b = (uint64_t)(of_group<bf16>(Q ? p.w2 : p.w1, Q ? p.ws2 : p.ws1, t.g, p.E, mat) + n0);
         s.a2 = GATED ? (uint64_t)((const bf16 *)p.du + at) : s.a;
         s.b2 = GATED ? (uint64_t)(of_group<bf16>(p.w3, p.ws3, t.g, p.E, mat) + n0) : s.b;
-        s.kt = kt;
+        s.s0 = SMALL ? split * per : 0;
+        s.kt = SMALL ? min(per, kt - s.s0) : kt;
         return s;
     };
     int L = tile_of(0);
     if (L >= total) return;
     typename P::Lanes ln;
-    ln.init(K * 2, 256, N * 2, min(N, 256), wave, threadIdx.x & 63);
+    ln.init(K * 2, BM, N * 2, min(N, BN), wave, threadIdx.x & 63);
     ln.split = K / mt::SK;
-    RowTile t = row_tile(tt, G, L);
-    typename P::Source src = source(t);
+    int split = SMALL ? L / tiles : 0;
+    RowTile t = row_tile<SMALL>(tt, G, L - split * tiles);
+    typename P::Source src = source(t, split);
     P::load_stage(src, ln, 0, slot0, wave);
     P::load_stage(src, ln, 1, slot1, wave);
+    if (SMALL) P::load_stage(src, ln, 2, slot2, wave);
     for (int r = 1;; ++r) {
         const int lane = tile_lane();
         L = tile_of(r);
         const bool more = L < total;
-        const RowTile tn = more ? row_tile(tt, G, L) : t;
-        const typename P::Source next = source(tn);
-        by_height(t.rb, [&](auto height) __attribute__((always_inline)) {
+        const int nsplit = SMALL && more ? L / tiles : split;
+        const RowTile tn = more ? row_tile<SMALL>(tt, G, L - nsplit * tiles) : t;
+        const typename P::Source next = source(tn, nsplit);
+        by_height<SMALL>(t.rb, [&](auto height) __attribute__((always_inline)) {
             constexpr int RB = decltype(height)::value;
             floatx4 acc[RB][TN];
             mt::clear(acc);
-            P::template run<RB, RB, KIND>(acc, src, ln, next, ln, slot0, slot1, wave, lane);
-            const int lo = t.n_tile * 256;
-            const int c0 = tile_start(t.n_tile, 256, N) + wn * TN * 16;
+            run_tile<P, SMALL, RB, KIND>(acc, src, next, ln, slot0, slot1, slot2, wave, lane);
+            const int lo = t.n_tile * BN;
+            const int c0 = tile_start(t.n_tile, BN, N) + wn * TN * 16;
+            float *plane = (Q ? p.q : p.dxs) + (size_t)split * p.rows * N;
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 const int m = (wm * RB + i) * 16;
                 if (m >= t.nrows) continue;
-                float *out = (Q ? p.q : p.dxs) + (size_t)(t.row0 + m + (lane & 15)) * N + c0 +
+                float *out = plane + (size_t)(t.row0 + m + (lane & 15)) * N + c0 +
                              4 * (lane >> 4);
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
@@ -206,21 +253,24 @@ __global__ __launch_bounds__(256, 1) void ffn_rows_by_weights(FfnGradParams p) {
         if (!more) break;
         t = tn;
         src = next;
+        split = nsplit;
     }
     __builtin_amdgcn_s_waitcnt(0);
 }
 
 // z (and u) of a tile, then with q: r h, dz, du and the parts of <q, h>.  A
-// gated tile is 128 columns of z and the same 128 of u.
-template <int ACT, mt::Stages KIND>
-__global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
-    constexpr int PANELS = ACT == ACT_SWIGLU ? 2 : 1, BN = 256 / PANELS;
-    typedef mt::Tiles<256, BN, 2, 2, PANELS, false, false> P;
+// gated tile has half the columns, of z and of u.
+template <int ACT, mt::Stages KIND, bool SMALL>
+__global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_act_grad(FfnGradParams p) {
+    constexpr int PANELS = ACT == ACT_SWIGLU ? 2 : 1;
+    constexpr int BM = Shape<SMALL>::BM, BN = Shape<SMALL>::BN / PANELS;
+    typedef mt::Tiles<BM, BN, 2, 2, PANELS, false, false> P;
     constexpr int TN = P::TN;
-    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], scr[4 * 32 * TN];
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], slot2[SMALL ? P::STAGE : 1];
+    __shared__ u32x4 scr[SMALL ? 1 : 4 * 32 * TN];
     __shared__ TileTable tt;
     const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
-    build_tile_table(tt, p.offsets, p.E, p.n_shared, 0, p.T, 256, (F + BN - 1) / BN);
+    build_tile_table(tt, p.offsets, p.E, p.n_shared, 0, p.T, BM, (F + BN - 1) / BN);
     const int total = __builtin_amdgcn_readfirstlane(tt.base[G]);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / 2, wn = wave % 2;
@@ -233,22 +283,24 @@ __global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
         s.b = (uint64_t)(of_group<bf16>(p.w1, p.ws1, t.g, p.E, mat) + at);
         s.b2 = PANELS > 1 ? (uint64_t)(of_group<bf16>(p.w3, p.ws3, t.g, p.E, mat) + at) : s.b;
         s.kt = kt;
+        s.s0 = 0;
         return s;
     };
     int L = tile_of(0);
     if (L >= total) return;
     typename P::Lanes ln;
-    ln.init(d * 2, 256, d * 2, min(F, BN), wave, threadIdx.x & 63);
+    ln.init(d * 2, BM, d * 2, min(F, BN), wave, threadIdx.x & 63);
     ln.split = kt;
-    RowTile t = row_tile(tt, G, L);
+    RowTile t = row_tile<SMALL>(tt, G, L);
     typename P::Source src = source(t);
     P::load_stage(src, ln, 0, slot0, wave);
     P::load_stage(src, ln, 1, slot1, wave);
+    if (SMALL) P::load_stage(src, ln, 2, slot2, wave);
     for (int r = 1;; ++r) {
         const int lane = tile_lane();
         L = tile_of(r);
         const bool more = L < total;
-        const RowTile tn = more ? row_tile(tt, G, L) : t;
+        const RowTile tn = more ? row_tile<SMALL>(tt, G, L) : t;
         const typename P::Source next = source(tn);
         const int l16 = lane & 15;
         const int c0 = tile_start(t.n_tile, BN, F) + wn * TN * 16;
@@ -257,7 +309,7 @@ __global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
         const int cq = c0 + 4 * (lane >> 4);
         const bf16 *bias[2] = {of_group<bf16>(p.b1, p.bs1, t.g, p.E, F),
                                PANELS > 1 ? of_group<bf16>(p.b3, p.bs3, t.g, p.E, F) : nullptr};
-        by_height(t.rb, [&](auto height) __attribute__((always_inline)) {
+        by_height<SMALL>(t.rb, [&](auto height) __attribute__((always_inline)) {
             constexpr int RB = decltype(height)::value;
             // the sums start from the biases
             floatx4 z[RB][TN * PANELS];
@@ -275,7 +327,7 @@ __global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
                         for (int i = 0; i < RB; ++i) z[i][k * TN + j] = f;
                     }
                 }
-            P::template run<RB, RB, KIND>(z, src, ln, next, ln, slot0, slot1, wave, lane);
+            run_tile<P, SMALL, RB, KIND>(z, src, next, ln, slot0, slot1, slot2, wave, lane);
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 const int m0 = (wm * RB + i) * 16;
@@ -288,6 +340,14 @@ __global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
                 for (int j = 0; j < TN; ++j)
                     q[j] = 16 * j >= lo && 16 * j < hi ? *(const floatx4 *)(qp + 16 * j)
                                                        : floatx4{0.f, 0.f, 0.f, 0.f};
+                if (SMALL) {
+                    for (int s = 1; s < p.q_splits; ++s) {
+                        const float *qs = qp + (size_t)s * p.rows * F;
+#pragma unroll
+                        for (int j = 0; j < TN; ++j)
+                            if (16 * j >= lo && 16 * j < hi) q[j] += *(const floatx4 *)(qs + 16 * j);
+                    }
+                }
                 float vh[TN][4], vz[TN][4], vu[TN][4], dot = 0.0f;
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
@@ -309,9 +369,13 @@ __global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
                 if (lane < 16) p.dw_part[(size_t)row * p.dw_tiles + t.n_tile * 2 + wn] = dot;
                 const size_t at = (size_t)(t.row0 + m0) * F + c0;
                 const int u0 = wave * 32 * TN;
-                store_rows<TN>(scr, u0, vh, (bf16 *)p.h + at, F, lo, hi, lane);
-                store_rows<TN>(scr, u0, vz, (bf16 *)p.dz + at, F, lo, hi, lane);
-                if (PANELS > 1) store_rows<TN>(scr, u0, vu, (bf16 *)p.du + at, F, lo, hi, lane);
+                auto store = [&](const float (&v)[TN][4], void *to) __attribute__((always_inline)) {
+                    if (SMALL) store_pieces<TN>(v, (bf16 *)to + at, F, lo, hi, lane);
+                    else store_rows<TN>(scr, u0, v, (bf16 *)to + at, F, lo, hi, lane);
+                };
+                store(vh, p.h);
+                store(vz, p.dz);
+                if (PANELS > 1) store(vu, p.du);
                 // one row block at a time: the accumulators are read as they
                 // are used, not all at once
                 __builtin_amdgcn_sched_barrier(0);
@@ -327,19 +391,23 @@ __global__ __launch_bounds__(256, 1) void ffn_act_grad(FfnGradParams p) {
 // Tiles of one matrix's gradient go in strips of 8 row tiles, so that the 32
 // consecutive tiles of an XCD's round are 8 x 4 and read 12 operand panels.
 // Groups are whole stages of rows, their last rows zero.
+// SMALL: 128 x 128 tiles, two blocks per CU, for groups of few rows, whose
+// time is the stores'.
 struct WeightTile {
     int g, which, mi, ni;                // which: 0 dW1, 1 dW2, 2 dW3
 };
 
-__global__ __launch_bounds__(256, 1) void ffn_weight_grad(FfnGradParams p) {
-    typedef mt::Tiles<256, 256, 2, 2, 1, true, true> P;
-    constexpr int TN = P::TN, RB = 8;
+template <bool SMALL>
+__global__ __launch_bounds__(256, SMALL ? 2 : 1) void ffn_weight_grad(FfnGradParams p) {
+    constexpr int B = SMALL ? 128 : 256;
+    typedef mt::Tiles<B, B, 2, 2, 1, true, true> P;
+    constexpr int TN = P::TN, RB = B / 32;
     __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], scr[4 * 32 * TN];
     const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / 2, wn = wave % 2;
     const int mats = p.act == ACT_SWIGLU ? 3 : 2;
-    const int tiles = (F + 255) / 256 * ((d + 255) / 256);      // of a matrix
+    const int tiles = (F + B - 1) / B * ((d + B - 1) / B);      // of a matrix
     const int total = G * tiles * mats;
     const size_t mat = (size_t)F * d;
     auto tile = [&](int L) __attribute__((always_inline)) {
@@ -350,7 +418,7 @@ __global__ __launch_bounds__(256, 1) void ffn_weight_grad(FfnGradParams p) {
         t.which = k == mats - 1 ? 1 : 2 * k;
         local -= k * tiles;
         const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
-        const int mtiles = (M + 255) / 256, ntiles = (N + 255) / 256;
+        const int mtiles = (M + B - 1) / B, ntiles = (N + B - 1) / B;
         const int strip = local / (8 * ntiles), in = local - strip * 8 * ntiles;
         const int sm = min(8, mtiles - strip * 8);
         t.mi = strip * 8 + in % sm;
@@ -376,29 +444,30 @@ __global__ __launch_bounds__(256, 1) void ffn_weight_grad(FfnGradParams p) {
     };
     auto source = [&](const WeightTile &t) __attribute__((always_inline)) {
         const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
-        const bf16 *A = (const bf16 *)(t.which == 0 ? p.dz : t.which == 1 ? p.dys : p.du);
-        const bf16 *B = (const bf16 *)(t.which == 1 ? p.h : p.xs);
+        const bf16 *a = (const bf16 *)(t.which == 0 ? p.dz : t.which == 1 ? p.dys : p.du);
+        const bf16 *b = (const bf16 *)(t.which == 1 ? p.h : p.xs);
         int start, rows;
         group_rows(p, t.g, start, rows);
         start = __builtin_amdgcn_readfirstlane(start);
-        P::Source s;
-        s.a = s.a2 = (uint64_t)(A + (size_t)start * M + tile_start(t.mi, 256, M));
-        s.b = s.b2 = (uint64_t)(B + (size_t)start * N + tile_start(t.ni, 256, N));
+        typename P::Source s;
+        s.a = s.a2 = (uint64_t)(a + (size_t)start * M + tile_start(t.mi, B, M));
+        s.b = s.b2 = (uint64_t)(b + (size_t)start * N + tile_start(t.ni, B, N));
         s.kt = __builtin_amdgcn_readfirstlane(rows) / mt::SK;
+        s.s0 = 0;
         return s;
     };
     auto lanes = [&](const WeightTile &t, int lane) __attribute__((always_inline)) {
         const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
-        P::Lanes ln;
-        ln.init(M * 2, min(M, 256), N * 2, min(N, 256), wave, lane);
+        typename P::Lanes ln;
+        ln.init(M * 2, min(M, B), N * 2, min(N, B), wave, lane);
         ln.split = 0;
         return ln;
     };
     int r = 0;
     WeightTile t;
     if (!find(r, t)) return;
-    P::Source src = source(t);
-    P::Lanes ln = lanes(t, threadIdx.x & 63);
+    typename P::Source src = source(t);
+    typename P::Lanes ln = lanes(t, threadIdx.x & 63);
     P::load_stage(src, ln, 0, slot0, wave);
     P::load_stage(src, ln, 1, slot1, wave);
     for (;;) {
@@ -406,26 +475,26 @@ __global__ __launch_bounds__(256, 1) void ffn_weight_grad(FfnGradParams p) {
         WeightTile tn = t;
         const bool more = find(r, tn);
         if (!more) tn = t;
-        const P::Source next = source(tn);
-        const P::Lanes lnext = lanes(tn, lane);
+        const typename P::Source next = source(tn);
+        const typename P::Lanes lnext = lanes(tn, lane);
         floatx4 acc[RB][TN];
         mt::clear(acc);
-        P::run<RB, 8, mt::ANY>(acc, src, ln, next, lnext, slot0, slot1, wave, lane);
+        P::template run<RB, RB, mt::ANY>(acc, src, ln, next, lnext, slot0, slot1, wave, lane);
         const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
         bf16 *out = result(t);
-        const int m0 = tile_start(t.mi, 256, M) + wm * RB * 16;
-        const int c0 = tile_start(t.ni, 256, N) + wn * TN * 16;
+        const int m0 = tile_start(t.mi, B, M) + wm * RB * 16;
+        const int c0 = tile_start(t.ni, B, N) + wn * TN * 16;
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
             const int mi = m0 + i * 16;
-            if (mi < t.mi * 256 || mi >= M) continue;
+            if (mi < t.mi * B || mi >= M) continue;
             float v[TN][4];
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[j][e] = acc[i][j][e];
             store_rows<TN>(scr, wave * 32 * TN, v, out + (size_t)mi * N + c0, N,
-                           t.ni * 256 - c0, N - c0, lane);
+                           t.ni * B - c0, N - c0, lane);
             __builtin_amdgcn_sched_barrier(0);
         }
         if (!more) break;
@@ -445,42 +514,69 @@ int cus() {
     return n / 8 * 8;
 }
 
-int grid_for(long long tiles) {
-    const int n = cus();
+int grid_for(long long tiles, int per_cu) {
+    const int n = cus() * per_cu;
     const long long g = (tiles + 7) / 8 * 8;
     return (int)(g < n ? (g < 8 ? 8 : g) : n);
 }
 
-// Row tiles of 256 rows by n columns in tiles of bn.
-int row_grid(const FfnGradParams &p, int n, int bn) {
-    return grid_for(ffn_row_tiles(p, 256) * ((n + bn - 1) / bn));
+// Groups of at most 64 rows on average: one 64-row tile holds most of them.
+bool few_rows(const FfnGradParams &p) { return mfma_few_rows(p.routed, p.E); }
+
+// Row tiles by n columns in tiles of bn.
+template <bool SMALL> int row_grid(const FfnGradParams &p, int n, int bn, int splits = 1) {
+    return grid_for(ffn_row_tiles(p, Shape<SMALL>::BM) * ((n + bn - 1) / bn) * splits,
+                    Shape<SMALL>::BLOCKS);
+}
+
+template <bool Q, bool GATED, bool SMALL> void rows_as(const FfnGradParams &p, hipStream_t s) {
+    const dim3 grid(row_grid<SMALL>(p, Q ? p.d_ff : p.d, Shape<SMALL>::BN,
+                                    Q ? p.q_splits : p.dx_splits));
+    if (!GATED && ((Q ? p.d : p.d_ff) / mt::SK & 1))
+        hipLaunchKernelGGL((ffn_rows_by_weights<Q, GATED, GATED ? mt::EVEN : mt::ODD, SMALL>),
+                           grid, dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((ffn_rows_by_weights<Q, GATED, mt::EVEN, SMALL>), grid, dim3(256), 0,
+                           s, p);
+}
+template <bool Q, bool GATED> void rows_by_weights(const FfnGradParams &p, hipStream_t s) {
+    if (few_rows(p)) rows_as<Q, GATED, true>(p, s);
+    else rows_as<Q, GATED, false>(p, s);
+}
+
+template <int ACT, bool SMALL> void act_as(const FfnGradParams &p, hipStream_t s) {
+    constexpr int BN = Shape<SMALL>::BN / (ACT == ACT_SWIGLU ? 2 : 1);
+    const dim3 grid(row_grid<SMALL>(p, p.d_ff, BN));
+    if (p.d / mt::SK & 1)
+        hipLaunchKernelGGL((ffn_act_grad<ACT, mt::ODD, SMALL>), grid, dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((ffn_act_grad<ACT, mt::EVEN, SMALL>), grid, dim3(256), 0, s, p);
+}
+template <int ACT> void act_grad_as(const FfnGradParams &p, hipStream_t s) {
+    if (few_rows(p)) act_as<ACT, true>(p, s);
+    else act_as<ACT, false>(p, s);
 }
 
 }  // namespace
 
-// Two waves side by side in each column tile: 128 columns gated, 256 else.
-int mfma_dw_tiles(int d_ff, int act) {
-    const int bn = act == ACT_SWIGLU ? 128 : 256;
+bool mfma_few_rows(long long routed, int E) { return routed <= 64ll * E; }
+
+// Ranges of K for N columns: as many as give two blocks per CU (of 256) a
+// tile, each of 8 stages or more.  A split product's planes are added by
+// the kernel that reads them.
+int mfma_splits(long long routed, int E, int shared_rows, int N, int K) {
+    if (!mfma_few_rows(routed, E)) return 1;
+    const long long tiles = ((routed < E ? routed : E) + (shared_rows + 63) / 64) *
+                            ((N + 127) / 128);
+    long long s = tiles > 0 ? 512 / tiles : 1;
+    if (s > K / (8 * mt::SK)) s = K / (8 * mt::SK);
+    return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
+}
+
+// Two waves side by side in each column tile of the activation gradient.
+int mfma_dw_tiles(int d_ff, int act, bool few) {
+    const int bn = (few ? 128 : 256) / (act == ACT_SWIGLU ? 2 : 1);
     return (d_ff + bn - 1) / bn * 2;
-}
-
-template <bool Q, bool GATED>
-static void rows_by_weights(const FfnGradParams &p, hipStream_t s) {
-    const int N = Q ? p.d_ff : p.d;
-    const dim3 grid(row_grid(p, N, 256));
-    if (!GATED && ((Q ? p.d : p.d_ff) / mt::SK & 1))
-        hipLaunchKernelGGL((ffn_rows_by_weights<Q, GATED, GATED ? mt::EVEN : mt::ODD>), grid,
-                           dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL((ffn_rows_by_weights<Q, GATED, mt::EVEN>), grid, dim3(256), 0, s, p);
-}
-
-template <int ACT> static void act_grad_as(const FfnGradParams &p, hipStream_t s) {
-    const dim3 grid(row_grid(p, p.d_ff, ACT == ACT_SWIGLU ? 128 : 256));
-    if (p.d / mt::SK & 1)
-        hipLaunchKernelGGL((ffn_act_grad<ACT, mt::ODD>), grid, dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL((ffn_act_grad<ACT, mt::EVEN>), grid, dim3(256), 0, s, p);
 }
 
 hipError_t launch_act_grad_mfma(const FfnGradParams &p, hipStream_t s) {
@@ -498,8 +594,12 @@ hipError_t launch_row_grad_mfma(const FfnGradParams &p, hipStream_t s) {
 }
 
 hipError_t launch_weight_grad_mfma(const FfnGradParams &p, hipStream_t s) {
-    const long long tiles = (long long)((p.d_ff + 255) / 256) * ((p.d + 255) / 256);
-    const int grid = grid_for(tiles * (p.E + p.n_shared) * (p.act == ACT_SWIGLU ? 3 : 2));
-    hipLaunchKernelGGL(ffn_weight_grad, dim3(grid), dim3(256), 0, s, p);
+    const bool few = few_rows(p);
+    const int b = few ? 128 : 256;
+    const long long tiles = (long long)((p.d_ff + b - 1) / b) * ((p.d + b - 1) / b);
+    const int grid = grid_for(tiles * (p.E + p.n_shared) * (p.act == ACT_SWIGLU ? 3 : 2),
+                              few ? 2 : 1);
+    if (few) hipLaunchKernelGGL(ffn_weight_grad<true>, dim3(grid), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL(ffn_weight_grad<false>, dim3(grid), dim3(256), 0, s, p);
     return hipGetLastError();
 }

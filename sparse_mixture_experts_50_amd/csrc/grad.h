@@ -53,17 +53,23 @@ struct FfnGradParams {
     // h times the row weight, and the gradients of the pre-activations,
     // [rows][d_ff] each (du: SwiGLU)
     void *h, *dz, *du;
-    float *q;                 // bf16: [rows][d_ff], dy W2
+    float *q;                 // bf16: [q_splits][rows][d_ff], dy W2
+    int q_splits, dx_splits;  // partial sums of q and dxs
     float *dw_part;           // [rows][dw_tiles]: <dy W2, h> by column tile
     int dw_tiles;
-    float *dxs;               // [rows][d] fp32
+    float *dxs;               // [dx_splits][rows][d] fp32
     void *g_w1, *g_w2, *g_w3, *g_ws1, *g_ws2, *g_ws3;
     void *g_b1, *g_b2, *g_b3, *g_bs1, *g_bs2, *g_bs3;
     int E, n_shared, d, d_ff, act;
     int T;                    // shared rows, padded: [0, T)
     int rows;                 // upper bound of all rows
+    int routed;           // routed rows (at most)
 };
 // Rows of the padded space for T tokens and R routed rows of E experts.
+// Partial sums of q (its depth d) and of dxs (depth d_ff, or 2 d_ff gated).
+int ffn_grad_q_splits(int dtype, long long routed, int E, int shared_rows, int d, int d_ff);
+int ffn_grad_dx_splits(int dtype, long long routed, int E, int shared_rows, int d, int d_ff,
+                       int act);
 size_t padded_rows(long long T, int n_shared, long long R, int E);
 // Group starts of the padded space, and its padding rows zeroed.
 struct PadParams {
@@ -75,7 +81,7 @@ struct PadParams {
 };
 hipError_t launch_pad_groups(const PadParams &p, int dtype, hipStream_t s);
 // Column tiles that launch_ffn_act_grad writes to dw_part.
-int ffn_grad_dw_tiles(int dtype, int d_ff, int act);
+int ffn_grad_dw_tiles(int dtype, int d_ff, int act, long long routed, int E);
 hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype, hipStream_t s);
 hipError_t launch_ffn_row_grad(const FfnGradParams &p, int dtype, hipStream_t s);
 hipError_t launch_ffn_weight_grad(const FfnGradParams &p, int dtype, hipStream_t s);
@@ -101,7 +107,9 @@ struct RouterGradParams {
     float *wr_part;           // [splits][E][d]
     int splits;
     const void *dx_add;       // [T][d] in the layer's type, or null
-    const float *dxs;         // [rows][d] expert row gradients, or null
+    const float *dxs;         // [dx_splits][rows][d] expert row gradients, or null
+    int dx_splits;
+    size_t dx_plane;          // elements of one of them
     void *dx, *dwr;           // [T][d], [E][d]; null = not wanted
     float *db;                // [E] or null
     float aux, z;             // d L / d (sum_t f p) and d L / d (sum lse^2)

@@ -13,7 +13,7 @@ struct GradLayout {
     size_t logits, dl, db_part, wr_part, router_total;
     size_t pad, pad_slot, row_w, xs, dys, h, dz, du, q, dw_part, dxs, total;
     size_t rows;
-    int ep, splits, dw_tiles;
+    int ep, splits, dw_tiles, q_splits, dx_splits;
     RouterPlan logit_plan;
 };
 
@@ -40,16 +40,20 @@ GradLayout layout(const moe_desc *d) {
     L.pad = take((size_t)(d->E + 1) * 4);
     L.pad_slot = take((size_t)d->T * d->k * 4);
     // column tiles of <dy W2, h>, and <dy, b2>
-    L.dw_tiles = ffn_grad_dw_tiles(d->dtype, d->d_ff, d->activation);
+    L.dw_tiles = ffn_grad_dw_tiles(d->dtype, d->d_ff, d->activation, routed_rows(d), d->E);
     L.row_w = take(L.rows * 4);
     L.xs = take(L.rows * d->d * es);
     L.dys = take(L.rows * d->d * es);
     L.h = take(L.rows * d->d_ff * es);
     L.dz = take(L.rows * d->d_ff * es);
     L.du = take(d->activation == MOE_ACT_SWIGLU ? L.rows * d->d_ff * es : 0);
-    L.q = take(d->dtype == MOE_BF16 ? L.rows * d->d_ff * 4 : 0);
+    const int shared = d->n_shared * d->T;
+    L.q_splits = ffn_grad_q_splits(d->dtype, routed_rows(d), d->E, shared, d->d, d->d_ff);
+    L.dx_splits = ffn_grad_dx_splits(d->dtype, routed_rows(d), d->E, shared, d->d, d->d_ff,
+                                     d->activation);
+    L.q = take(d->dtype == MOE_BF16 ? L.q_splits * L.rows * d->d_ff * 4 : 0);
     L.dw_part = take(L.rows * (L.dw_tiles + 1) * 4);
-    L.dxs = take(L.rows * d->d * 4);
+    L.dxs = take(L.dx_splits * L.rows * d->d * 4);
     // a row tile of 256 may reach past the last row of any operand
     take((size_t)256 * (d->d > d->d_ff ? d->d : d->d_ff) * es);
     L.total = off;
@@ -365,6 +369,9 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
     p.d_ff = desc->d_ff;
     p.act = desc->activation;
     p.rows = (int)L.rows;
+    p.q_splits = L.q_splits;
+    p.dx_splits = L.dx_splits;
+    p.routed = (int)routed_rows(desc);
 
     const bool weights = p.g_w1 || p.g_w2 || p.g_w3 || p.g_ws1 || p.g_ws2 || p.g_ws3;
     const bool biases = p.g_b1 || p.g_b2 || p.g_b3 || p.g_bs1 || p.g_bs2 || p.g_bs3;
@@ -384,6 +391,8 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
         q.dw_part = p.dw_part;
         q.dw_tiles = p.dw_tiles;
         q.dxs = p.dxs;
+        q.dx_splits = p.dx_splits;
+        q.dx_plane = (size_t)p.rows * p.d;
         q.slot_of = rp.pad_slot;
         q.shared_base = 0;
         if (launch_router_grad(q, dt, s) != hipSuccess) return MOE_ERR_HIP;

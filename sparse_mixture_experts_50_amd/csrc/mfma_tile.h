@@ -47,8 +47,18 @@ __device__ __forceinline__ void dma16_lanes(const char *src, u32x4 *lds) {
         (const void *)src, (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
 }
 
+// HAND: as volatile asm.  The compiler then keeps the issue order as written
+// and 256 accumulators in AGPRs (the builtin splits them between AGPRs and
+// VGPRs and copies them back and forth every step), but knows nothing of the
+// wait states around an MFMA: only for straight loops over a register file
+// full of accumulators, where it has no room and no reason to copy one.
+// Tiles of fewer accumulators use the builtin.
+template <bool HAND>
 __device__ __forceinline__ void mfma(floatx4 &acc, const bf16x8 &a, const bf16x8 &b) {
-    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    if (HAND)
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    else
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
 }
 
 // W rows (columns) of one operand in a slot from unit U0 on, PANELS of them:
@@ -161,13 +171,17 @@ struct Tiles {
     typedef Loader<BF, BN, PANELS, LA::UNITS> LB;
     static constexpr int STAGE = LA::UNITS + LB::UNITS;
 
+    // 256 x 256 tiles fill the AGPRs.
+    static constexpr bool HAND = BM * BN * PANELS == 256 * 256;
+
     // The operands of one tile: element (0, 0) of each (uniform).  SPLIT:
     // a2, b2 of the second product; PANELS 2: b2 of the second panel.  kt:
     // stages (maybe 0; a stage's worth of either operand can be read all the
     // same).
+    // s0: the first stage (of a range of K).
     struct Source {
         uint64_t a, b, a2, b2;
-        int kt;
+        int kt, s0;
     };
     // What the loads of every tile share.
     struct Lanes {
@@ -188,7 +202,7 @@ struct Tiles {
     struct Stage {
         uint64_t a, b, b2;
         __device__ __forceinline__ void set(const Source &src, const Lanes &ln, int s) {
-            s = max(min(s, src.kt - 1), 0);
+            s = max(min(s, src.kt - 1), 0) + src.s0;
             const bool second = SPLIT && s >= ln.split;
             const int n = second ? s - ln.split : s;
             a = (second ? src.a2 : src.a) + (uint64_t)n * ln.step_a;
@@ -212,8 +226,7 @@ struct Tiles {
                                                       int s, u32x4 *st, int wave) {
         Stage g;
         g.set(src, ln, s);
-#pragma unroll
-        for (int l = 0; l < LA::LOADS + LB::LOADS; ++l) load<LA::LOADS>(g, ln, l, st, wave);
+        load_all(g, ln, st, wave);
     }
 
     // item z of n in `span` slots goes to slot z * span / n; first(q) is the
@@ -221,6 +234,106 @@ struct Tiles {
     static constexpr int first(int q, int n, int span) {
         const int z = (q * n + span - 1) / span;
         return z < n ? z : n;
+    }
+
+    // A wave's work on a stage of a tile of RB 16-row blocks per wave.
+    template <int RB> struct Worker {
+        typedef Reader<AF, BM, 0, RB> RA;
+        typedef Reader<BF, BN, LA::UNITS, TN> RBd;
+        static constexpr int NM = RB * NC;               // MFMAs per sub-step
+        static constexpr int NA = RB * RA::READS, NR = NA + NC * RBd::READS;
+        // reads go between the first three quarters of the MFMAs, loads
+        // between all of them
+        static constexpr int RSPAN = NM * 3 / 4, MAXR = (NR + RSPAN - 1) / RSPAN;
+        RA a;
+        RBd b;
+        bf16x8 fa0[RB], fb0[NC], fa1[RB], fb1[NC];
+
+        __device__ __forceinline__ void read(bf16x8 (&fa)[RB], bf16x8 (&fb)[NC],
+                                             const u32x4 *st, int kk, int r) {
+            if (r < NA) {
+                const int q = r / RA::READS;
+                a.read(fa[q], st, kk, q, q * 16, r % RA::READS);
+            } else {
+                const int q = (r - NA) / RBd::READS;
+                b.read(fb[q], st, kk, q % TN, (q / TN) * BN + (q % TN) * 16,
+                       (r - NA) % RBd::READS);
+            }
+        }
+        // Waits for what has been asked for and reads the first fragments.
+        __device__ __forceinline__ void begin(const u32x4 *slot0, int wave, int lane) {
+            a.init((wave / WN) * RB * 16, lane);
+            b.init((wave % WN) * TN * 16, lane);
+            __builtin_amdgcn_s_waitcnt(0);
+            __builtin_amdgcn_s_barrier();
+#pragma unroll
+            for (int r = 0; r < NR; ++r) read(fa0, fb0, slot0, 0, r);
+        }
+        // Stage in cur: its sub-step 0 on fa0 while the other half is read
+        // into fa1, then sub-step 1 while nxt's first half is read into fa0
+        // (unless LAST) and stage g (PARTS 32-row parts of A) is loaded into
+        // cur.  AHEAD: loads that may still be in flight when the stage after
+        // this one has landed.
+        template <bool LAST, int PARTS, int AHEAD>
+        __device__ __forceinline__ void stage(floatx4 (&acc)[RB][NC], const Stage &g,
+                                              const Lanes &gl, u32x4 *cur, u32x4 *nxt,
+                                              int wave) {
+            constexpr int NL = PARTS + LB::LOADS;
+            constexpr int MAXL = (NL + NM - 1) / NM;
+            static_assert(AHEAD < 64, "vmcnt range");
+            __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
+#pragma unroll
+            for (int q = 0; q < NM; ++q) {
+                mfma<HAND>(acc[q / NC][q % NC], fb0[q % NC], fa0[q / NC]);
+#pragma unroll
+                for (int u = 0; u < MAXR; ++u)
+                    if (first(q, NR, RSPAN) + u < first(q + 1, NR, RSPAN))
+                        read(fa1, fb1, cur, 1, first(q, NR, RSPAN) + u);
+            }
+            // own reads done, the next stage landed, then every wave's part
+            __builtin_amdgcn_s_waitcnt((AHEAD & 0xF) | ((AHEAD >> 4) << 14) | (0x7 << 4));
+            __builtin_amdgcn_s_barrier();
+#pragma unroll
+            for (int q = 0; q < NM; ++q) {
+                mfma<HAND>(acc[q / NC][q % NC], fb1[q % NC], fa1[q / NC]);
+                if (!LAST) {
+#pragma unroll
+                    for (int u = 0; u < MAXR; ++u)
+                        if (first(q, NR, RSPAN) + u < first(q + 1, NR, RSPAN))
+                            read(fa0, fb0, nxt, 0, first(q, NR, RSPAN) + u);
+                }
+#pragma unroll
+                for (int u = 0; u < MAXL; ++u)
+                    if (first(q, NL, NM) + u < first(q + 1, NL, NM))
+                        load<PARTS>(g, gl, first(q, NL, NM) + u, cur, wave);
+            }
+        }
+    };
+    // Wait states that the compiler does not know the asm MFMAs need: before
+    // the first (a VALU write of its accumulator) and after the last (a read
+    // of its result).
+    static __device__ __forceinline__ void before() {
+        if (HAND) asm volatile("s_nop 4");
+    }
+    static __device__ __forceinline__ void after() {
+        if (HAND) asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7");
+    }
+    // Puts every write of the accumulators above this point and every later
+    // read below it (volatile asm keeps its order): above before(), or a
+    // constant may be written right ahead of its MFMA, below after().
+    template <int RB>
+    static __device__ __forceinline__ void pin(floatx4 (&acc)[RB][NC]) {
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+                if (HAND) asm volatile("" : "+a"(acc[i][j]));
+    }
+    // All loads of stage g.
+    static __device__ __forceinline__ void load_all(const Stage &g, const Lanes &ln,
+                                                    u32x4 *st, int wave) {
+#pragma unroll
+        for (int l = 0; l < LA::LOADS + LB::LOADS; ++l) load<LA::LOADS>(g, ln, l, st, wave);
     }
 
     // acc += A B of a tile of RB 16-row blocks per wave over its src.kt
@@ -233,106 +346,89 @@ struct Tiles {
                                                const Lanes &ln, const Source &next,
                                                const Lanes &lnext, u32x4 *slot0,
                                                u32x4 *slot1, int wave, int lane) {
-        typedef Reader<AF, BM, 0, RB> RA;
-        typedef Reader<BF, BN, LA::UNITS, TN> RBd;
-        constexpr int NM = RB * NC;                      // MFMAs per sub-step
-        constexpr int NA = RB * RA::READS, NR = NA + NC * RBd::READS;
-        // reads go between the first three quarters of the MFMAs, loads
-        // between all of them
-        constexpr int RSPAN = NM * 3 / 4, MAXR = (NR + RSPAN - 1) / RSPAN;
-        const int wm = wave / WN, wn = wave % WN;
-        RA a;
-        RBd b;
-        a.init(wm * RB * 16, lane);
-        b.init(wn * TN * 16, lane);
-        auto read = [&](bf16x8 (&fa)[RB], bf16x8 (&fb)[NC], const u32x4 *st, int kk,
-                        int r) __attribute__((always_inline)) {
-            if (r < NA) {
-                const int q = r / RA::READS;
-                a.read(fa[q], st, kk, q, q * 16, r % RA::READS);
-            } else {
-                const int q = (r - NA) / RBd::READS;
-                b.read(fb[q], st, kk, q % TN, (q / TN) * BN + (q % TN) * 16,
-                       (r - NA) % RBd::READS);
-            }
-        };
-        bf16x8 fa0[RB], fb0[NC], fa1[RB], fb1[NC];
-        __builtin_amdgcn_s_waitcnt(0);
-        __builtin_amdgcn_s_barrier();
-#pragma unroll
-        for (int r = 0; r < NR; ++r) read(fa0, fb0, slot0, 0, r);
-
-        // Stage in cur: its sub-step 0 on fa0 while the other half is read
-        // into fa1, then sub-step 1 while nxt's first half is read into fa0
-        // (unless LAST) and stage g is loaded into cur.
-        auto stage = [&](const Stage &g, const Lanes &gl, u32x4 *cur, u32x4 *nxt, auto last,
-                         auto parts) __attribute__((always_inline)) {
-            constexpr bool LAST = decltype(last)::value;
-            constexpr int NL = decltype(parts)::value + LB::LOADS;
-            constexpr int MAXL = (NL + NM - 1) / NM;
-            __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
-#pragma unroll
-            for (int q = 0; q < NM; ++q) {
-                mfma(acc[q / NC][q % NC], fb0[q % NC], fa0[q / NC]);
-#pragma unroll
-                for (int u = 0; u < MAXR; ++u)
-                    if (first(q, NR, RSPAN) + u < first(q + 1, NR, RSPAN))
-                        read(fa1, fb1, cur, 1, first(q, NR, RSPAN) + u);
-            }
-            // own reads done, the next stage landed, then every wave's part
-            __builtin_amdgcn_s_waitcnt(0x0 | (0x7 << 4));
-            __builtin_amdgcn_s_barrier();
-#pragma unroll
-            for (int q = 0; q < NM; ++q) {
-                mfma(acc[q / NC][q % NC], fb1[q % NC], fa1[q / NC]);
-                if (!LAST) {
-#pragma unroll
-                    for (int u = 0; u < MAXR; ++u)
-                        if (first(q, NR, RSPAN) + u < first(q + 1, NR, RSPAN))
-                            read(fa0, fb0, nxt, 0, first(q, NR, RSPAN) + u);
-                }
-#pragma unroll
-                for (int u = 0; u < MAXL; ++u)
-                    if (first(q, NL, NM) + u < first(q + 1, NL, NM))
-                        load<decltype(parts)::value>(g, gl, first(q, NL, NM) + u, cur, wave);
-            }
-        };
-        typedef std::integral_constant<int, RBA> Part;
-        typedef std::integral_constant<int, LA::LOADS> Whole;
+        Worker<RB> w;
+        pin(acc);
+        w.begin(slot0, wave, lane);
         Stage g, h;
-        // wait states that the compiler does not know the asm needs: before
-        // the first MFMA (a VALU write of its accumulator) and after the
-        // last (a read of its result)
         const int kt = src.kt;
         for (int s = 0; s + 2 < kt; s += 2) {
             g.set(src, ln, s + 2);
             h.set(src, ln, s + 3);
-            asm volatile("s_nop 4");
-            stage(g, ln, slot0, slot1, std::false_type{}, Part{});
-            stage(h, ln, slot1, slot0, std::false_type{}, Part{});
-            asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7");
+            before();
+            w.template stage<false, RBA, 0>(acc, g, ln, slot0, slot1, wave);
+            w.template stage<false, RBA, 0>(acc, h, ln, slot1, slot0, wave);
+            after();
         }
         g.set(next, lnext, 0);
         h.set(next, lnext, 1);
         if (KIND != ANY || kt > 0) {
-            asm volatile("s_nop 4");
-            stage(g, lnext, slot0, slot1, std::integral_constant<bool, KIND == ODD>{}, Whole{});
-            asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7");
+            before();
+            w.template stage<KIND == ODD, LA::LOADS, 0>(acc, g, lnext, slot0, slot1, wave);
+            after();
         } else {
-#pragma unroll
-            for (int l = 0; l < LA::LOADS + LB::LOADS; ++l)
-                load<LA::LOADS>(g, lnext, l, slot0, wave);
+            load_all(g, lnext, slot0, wave);
         }
         if (KIND == EVEN || (KIND == ANY && kt > 0 && (kt & 1) == 0)) {
-            asm volatile("s_nop 4");
-            stage(h, lnext, slot1, slot0, std::true_type{}, Whole{});
-            asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7");
+            before();
+            w.template stage<true, LA::LOADS, 0>(acc, h, lnext, slot1, slot0, wave);
+            after();
         } else {
-#pragma unroll
-            for (int l = 0; l < LA::LOADS + LB::LOADS; ++l)
-                load<LA::LOADS>(h, lnext, l, slot1, wave);
+            load_all(h, lnext, slot1, wave);
         }
-        // nothing that reads the results moves above the wait states
+        pin(acc);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // The same through NS slots, NS - 1 stages ahead (kt >= 1): for products
+    // that stream weights through small tiles, whose stages are worked on in
+    // far less time than a load takes.
+    template <int RB, int NS>
+    static __device__ __forceinline__ void run_ring(floatx4 (&acc)[RB][NC],
+                                                    const Source &src, const Lanes &ln,
+                                                    const Source &next, const Lanes &lnext,
+                                                    u32x4 *const (&slot)[NS], int wave,
+                                                    int lane) {
+        constexpr int NL = LA::LOADS + LB::LOADS, AHEAD = (NS - 2) * NL;
+        Worker<RB> w;
+        pin(acc);
+        w.begin(slot[0], wave, lane);
+        Stage g;
+        int left = src.kt;
+        for (int s = NS; left > NS; s += NS, left -= NS) {
+            before();
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                g.set(src, ln, s + i);
+                w.template stage<false, LA::LOADS, AHEAD>(acc, g, ln, slot[i],
+                                                          slot[(i + 1) % NS], wave);
+            }
+            after();
+        }
+        // the last LEFT stages, and the first NS of the next tile (one way
+        // for each LEFT: joining on the way would make the compiler wait for
+        // every load)
+        auto finish = [&](auto count) __attribute__((always_inline)) {
+            constexpr int LEFT = decltype(count)::value;
+            before();
+            auto one = [&](auto at) __attribute__((always_inline)) {
+                constexpr int i = decltype(at)::value;
+                g.set(next, lnext, i);
+                if constexpr (i < LEFT)
+                    w.template stage<i + 1 == LEFT, LA::LOADS, AHEAD>(
+                        acc, g, lnext, slot[i], slot[(i + 1) % NS], wave);
+                else
+                    load_all(g, lnext, slot[i], wave);
+            };
+            one(std::integral_constant<int, 0>{});
+            one(std::integral_constant<int, 1>{});
+            one(std::integral_constant<int, 2>{});
+            after();
+        };
+        static_assert(NS == 3, "the ways below");
+        if (left == 3) finish(std::integral_constant<int, 3>{});
+        else if (left == 2) finish(std::integral_constant<int, 2>{});
+        else finish(std::integral_constant<int, 1>{});
+        pin(acc);
         __builtin_amdgcn_sched_barrier(0);
     }
 };

@@ -226,19 +226,16 @@ __device__ __forceinline__ void expert_part(const RouterGradParams &p, int t, in
     for (int b = 0; b < NB; ++b) v[b] = floatx4{0.f, 0.f, 0.f, 0.f};
     if (p.dxs) {
         const int32_t *so = p.slot_of + (size_t)t * p.k;
+        auto add = [&](int row) __attribute__((always_inline)) {
+            const float *q = p.dxs + (size_t)row * p.d + c;
+            for (int i = 0; i < p.dx_splits; ++i, q += p.dx_plane)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) v[b] += load4(q + 16 * b);
+        };
 #pragma unroll 4
-        for (int j = 0; j < p.k; ++j) {
-            const int s = so[j];
-            if (s < 0) continue;
-            const float *q = p.dxs + (size_t)s * p.d + c;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) v[b] += load4(q + 16 * b);
-        }
-        if (p.n_shared) {
-            const float *q = p.dxs + (size_t)(p.shared_base + t) * p.d + c;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) v[b] += load4(q + 16 * b);
-        }
+        for (int j = 0; j < p.k; ++j)
+            if (so[j] >= 0) add(so[j]);
+        if (p.n_shared) add(p.shared_base + t);
     }
     if (p.dx_add) {
         const T *q = (const T *)p.dx_add + (size_t)t * p.d + c;
@@ -359,6 +356,7 @@ __global__ __launch_bounds__(256, 2) void router_grad_w_bf16(RouterGradParams p)
     src.a = src.a2 = (uint64_t)A + ((int64_t)head - mt::SK) * p.ep * 2;
     src.b = src.b2 = (uint64_t)B + ((int64_t)head - mt::SK) * p.d * 2;
     src.kt = (n + mt::SK - 1) / mt::SK;
+    src.s0 = 0;
     P::Lanes ln;
     ln.init(p.ep * 2, 64, p.d * 2, min(256, p.d - c0), wave, lane);
     ln.split = 0;
@@ -377,7 +375,7 @@ __global__ __launch_bounds__(256, 2) void router_grad_w_bf16(RouterGradParams p)
     // no stage after the last: every lane a zeroed line (x may end anywhere)
     P::Source none;
     none.a = none.a2 = none.b = none.b2 = (uint64_t)zero_line;
-    none.kt = 0;
+    none.kt = none.s0 = 0;
     P::Lanes still = {};
     if (src.kt > 1) P::load_stage(src, ln, 1, slot1, wave);
     else P::load_stage(none, still, 1, slot1, wave);
