@@ -117,7 +117,7 @@ struct RouterGradParams {
     int ep;                   // E rounded up to 64
 };
 // Tokens of one partial sum of the bias gradient.
-#define MOE_ROUTER_GRAD_TOKENS 32
+#define MOE_ROUTER_GRAD_TOKENS 16
 // Token ranges that the router weight gradient is split into.
 int router_grad_splits(int dtype, int T, int d, int E);
 // The forward's split bf16 router alone: partial logits of p.S ranges into

@@ -372,7 +372,7 @@ struct Tiles {
             before();
             w.template stage<true, LA::LOADS, 0>(acc, h, lnext, slot1, slot0, wave);
             after();
-        } else {
+        } else if (next.kt > 1) {
             load_all(h, lnext, slot1, wave);
         }
         pin(acc);

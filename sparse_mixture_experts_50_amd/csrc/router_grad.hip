@@ -47,8 +47,8 @@ __device__ __forceinline__ void store1(uint16_t *p, float v) {
 
 // A wave per token, experts lane + 64 i.  Each block also leaves the column
 // sums of its tokens for the bias gradient (before dl is rounded to the
-// layer's type, which feeds its two products).  Sixteen waves for 32 tokens:
-// the kernel waits for a few dependent loads and reductions a token.
+// layer's type, which feeds its two products).  A token per wave: the kernel
+// waits for a few dependent loads and reductions a token.
 template <typename T, bool CHOICE>
 __global__ __launch_bounds__(1024) void router_grad_dlogits(RouterGradParams p) {
     constexpr int NE = MOE_MAX_E / 64, WAVES = 16;
@@ -74,8 +74,15 @@ __global__ __launch_bounds__(1024) void router_grad_dlogits(RouterGradParams p) 
                 if (e < p.E) {
                     const float *q = p.logits + (size_t)t * p.E + e;
                     const size_t plane = (size_t)p.T * p.E;
-                    float a = q[0];
-                    for (int s = 1; s < p.logit_splits; ++s) a += q[s * plane];
+                    // every load issued before the in-order sum
+                    float part[MOE_ROUTER_MAX_SPLITS];
+#pragma unroll
+                    for (int s = 0; s < MOE_ROUTER_MAX_SPLITS; ++s)
+                        part[s] = s < p.logit_splits ? q[s * plane] : 0.0f;
+                    float a = part[0];
+#pragma unroll
+                    for (int s = 1; s < MOE_ROUTER_MAX_SPLITS; ++s)
+                        if (s < p.logit_splits) a += part[s];
                     if (p.add) a += p.add[e];
                     if (p.sub) a -= p.sub[e];
                     l[i] = a;
@@ -226,16 +233,40 @@ __device__ __forceinline__ void expert_part(const RouterGradParams &p, int t, in
     for (int b = 0; b < NB; ++b) v[b] = floatx4{0.f, 0.f, 0.f, 0.f};
     if (p.dxs) {
         const int32_t *so = p.slot_of + (size_t)t * p.k;
-        auto add = [&](int row) __attribute__((always_inline)) {
-            const float *q = p.dxs + (size_t)row * p.d + c;
-            for (int i = 0; i < p.dx_splits; ++i, q += p.dx_plane)
+        // four rows in flight: a slot that has none re-reads the first one
+        // that has, and drops it
+        auto add4 = [&](const int (&s)[4]) __attribute__((always_inline)) {
+            const int any = max(max(s[0], s[1]), max(s[2], s[3]));
+            if (any < 0) return;
+            const float *q[4];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) v[b] += load4(q + 16 * b);
+            for (int u = 0; u < 4; ++u)
+                q[u] = p.dxs + (size_t)(s[u] < 0 ? any : s[u]) * p.d + c;
+            for (int i = 0; i < p.dx_splits; ++i) {
+                floatx4 x[4][NB];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) x[u][b] = load4(q[u] + 16 * b);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    q[u] += p.dx_plane;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        if (s[u] >= 0) v[b] += x[u][b];
+                }
+            }
         };
-#pragma unroll 4
-        for (int j = 0; j < p.k; ++j)
-            if (so[j] >= 0) add(so[j]);
-        if (p.n_shared) add(p.shared_base + t);
+        for (int j = 0; j < p.k; j += 4) {
+            int s[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[u] = j + u < p.k ? so[j + u] : -1;
+            add4(s);
+        }
+        if (p.n_shared) {
+            const int s[4] = {p.shared_base + t, -1, -1, -1};
+            add4(s);
+        }
     }
     if (p.dx_add) {
         const T *q = (const T *)p.dx_add + (size_t)t * p.d + c;

@@ -402,79 +402,101 @@ def _routed(desc: MoeDesc) -> int:
     return desc.T * desc.k
 
 
+def _check(t, name, shape, dtype, device):
+    """_need, quick for what is right."""
+    if not (t.shape == shape and t.dtype is dtype and t.device == device
+            and t.is_contiguous()):
+        _need(t, name, shape, dtype, device)
+
+
 def _tokens(desc, t, name, device):
-    _need(t, name, (desc.T, desc.d), _TORCH[desc.dtype], device)
+    _check(t, name, (desc.T, desc.d), _TORCH[desc.dtype], device)
 
 
 def _rows(desc, t, name, device):
-    _need(t, name, (_routed(desc) + desc.n_shared * desc.T, desc.d),
-          _TORCH[desc.dtype], device)
+    _check(t, name, (_routed(desc) + desc.n_shared * desc.T, desc.d),
+           _TORCH[desc.dtype], device)
 
 
 def _routing(desc, r: Routing, device):
     """The routing buffers of this descriptor's calls."""
     if r.slot_of.device != device:
         raise ValueError(f"routing on {r.slot_of.device}, expected {device}")
-    if (tuple(r.slot_of.shape) != (desc.T, desc.k) or
+    if (r.slot_of.shape != (desc.T, desc.k) or
             r.slot_token.numel() != _routed(desc) or
             r.offsets.numel() != desc.E + 1):
         raise ValueError("routing buffers of another shape")
 
 
-def _run(name: str, t: torch.Tensor, *args) -> None:
-    """Call an entry point on the current stream of t's device, with that
-    device current (a stream handle of 0 means the current device's)."""
+def _slots(r: Routing) -> MoeRouting:
+    """The part of the routing that the row operators read."""
+    rs = MoeRouting()
+    rs.slot_of = r.slot_of.data_ptr()
+    rs.topk_w = r.topk_w.data_ptr()
+    return rs
+
+
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _run(name: str, device: torch.device, *args) -> None:
+    """Call an entry point on the device's current stream, with that device
+    current (a stream handle of 0 means the current device's)."""
     fn = getattr(_lib.lib(), name)
-    if t.device.index == torch.cuda.current_device():
-        check(name, fn(*args, _stream(t)))
-    else:
-        with torch.cuda.device(t.device):
-            check(name, fn(*args, _stream(t)))
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _run(name, device, *args)
+    stream = (_raw_stream(index) if _raw_stream is not None
+              else torch.cuda.current_stream(device).cuda_stream)
+    check(name, fn(*args, stream))
 
 
 def moe_dispatch_rows(desc, r: Routing, x, xs) -> None:
     """x [T][d] into expert-sorted rows xs; rows of dropped assignments are
     left as they were."""
-    _tokens(desc, x, "x", x.device)
-    _rows(desc, xs, "xs", x.device)
-    _routing(desc, r, x.device)
-    rs = r.struct()
-    _run("moe_dispatch_rows", x, ctypes.byref(desc), ctypes.byref(rs),
-         x.data_ptr(), xs.data_ptr())
+    dev = x.device
+    _tokens(desc, x, "x", dev)
+    _rows(desc, xs, "xs", dev)
+    _routing(desc, r, dev)
+    _run("moe_dispatch_rows", dev, ctypes.byref(desc),
+         ctypes.byref(_slots(r)), x.data_ptr(), xs.data_ptr())
 
 
 def moe_dispatch_rows_grad(desc, r: Routing, dxs, dx) -> None:
     """dx [T][d]: the gradient of moe_dispatch_rows for row gradients dxs."""
-    _tokens(desc, dx, "dx", dx.device)
-    _rows(desc, dxs, "dxs", dx.device)
-    _routing(desc, r, dx.device)
-    rs = r.struct()
-    _run("moe_dispatch_rows_grad", dx, ctypes.byref(desc), ctypes.byref(rs),
-         dxs.data_ptr(), dx.data_ptr())
+    dev = dx.device
+    _tokens(desc, dx, "dx", dev)
+    _rows(desc, dxs, "dxs", dev)
+    _routing(desc, r, dev)
+    _run("moe_dispatch_rows_grad", dev, ctypes.byref(desc),
+         ctypes.byref(_slots(r)), dxs.data_ptr(), dx.data_ptr())
 
 
 def moe_combine_rows(desc, r: Routing, ys, y) -> None:
     """Expert-sorted rows ys back into token order, weighted: y [T][d]."""
-    _tokens(desc, y, "y", y.device)
-    _rows(desc, ys, "ys", y.device)
-    _routing(desc, r, y.device)
-    rs = r.struct()
-    _run("moe_combine_rows", y, ctypes.byref(desc), ctypes.byref(rs),
-         ys.data_ptr(), y.data_ptr())
+    dev = y.device
+    _tokens(desc, y, "y", dev)
+    _rows(desc, ys, "ys", dev)
+    _routing(desc, r, dev)
+    _run("moe_combine_rows", dev, ctypes.byref(desc),
+         ctypes.byref(_slots(r)), ys.data_ptr(), y.data_ptr())
 
 
 def moe_combine_rows_grad(desc, r: Routing, dy, ys, dys, dw) -> None:
     """Gradients of moe_combine_rows for dy [T][d]: of the rows into dys
     (may be ys itself; rows of dropped assignments are left as they were),
     of the routing weights into dw [T][k] float32."""
-    _tokens(desc, dy, "dy", dy.device)
-    _rows(desc, ys, "ys", dy.device)
-    _rows(desc, dys, "dys", dy.device)
-    _need(dw, "dw", (desc.T, desc.k), torch.float32, dy.device)
-    _routing(desc, r, dy.device)
-    rs = r.struct()
-    _run("moe_combine_rows_grad", dy, ctypes.byref(desc), ctypes.byref(rs),
-         dy.data_ptr(), ys.data_ptr(), dys.data_ptr(), dw.data_ptr())
+    dev = dy.device
+    _tokens(desc, dy, "dy", dev)
+    _rows(desc, ys, "ys", dev)
+    _rows(desc, dys, "dys", dev)
+    _check(dw, "dw", (desc.T, desc.k), torch.float32, dev)
+    _routing(desc, r, dev)
+    _run("moe_combine_rows_grad", dev, ctypes.byref(desc),
+         ctypes.byref(_slots(r)), dy.data_ptr(), ys.data_ptr(),
+         dys.data_ptr(), dw.data_ptr())
 
 
 def moe_router_grad_workspace_size(desc: MoeDesc) -> int:
@@ -531,7 +553,7 @@ def moe_router_grad(desc, x, w, r: Routing, dw, g: Grads, ws,
     _check_grads(desc, g, w.device)
     p, n = _grad_ws(moe_router_grad_workspace_size(desc), ws, w.device)
     rs, wsct, gs = r.struct(), w.struct(), g.struct()
-    _run("moe_router_grad", x, ctypes.byref(desc), x.data_ptr(),
+    _run("moe_router_grad", x.device, ctypes.byref(desc), x.data_ptr(),
          ctypes.byref(wsct), ctypes.byref(rs), dw.data_ptr(), _ptr(dx_add),
          float(aux_scale), float(z_scale), ctypes.byref(gs), p, n)
 
@@ -549,7 +571,7 @@ def moe_backward(desc, x, w: Weights, r: Routing, dy, g: Grads, ws,
     _check_grads(desc, g, w.device)
     p, n = _grad_ws(moe_grad_workspace_size(desc), ws, w.device)
     rs, wsct, gs = r.struct(), w.struct(), g.struct()
-    _run("moe_backward", x, ctypes.byref(desc), x.data_ptr(),
+    _run("moe_backward", x.device, ctypes.byref(desc), x.data_ptr(),
          ctypes.byref(wsct), ctypes.byref(rs), dy.data_ptr(),
          float(aux_scale), float(z_scale), ctypes.byref(gs), p, n)
 
@@ -567,27 +589,35 @@ def moe_clip_grads(tensors, max_norm: float, norm, ws, out=None) -> None:
     device = norm.device
     _need(norm, "norm", (1,), torch.float32, device)
     out = tensors if out is None else out
-    if len(out) != len(tensors):
+    count = len(tensors)
+    if len(out) != count:
         raise ValueError("out: as many tensors as there are gradients")
-    arr = (_lib.MoeTensor * len(tensors))()
-    seen = set()
-    for item, t, o in zip(arr, tensors, out):
-        n = t.numel()
-        if t.dtype not in _DT:
+    same = out is tensors
+    flat, seen, filled = [], set(), 0
+    for t, o in zip(tensors, out):
+        n, dtype = t.numel(), _DT.get(t.dtype)
+        if dtype is None:
             raise ValueError(f"unsupported dtype {t.dtype}")
-        if (t.device != device or o.device != device or o.dtype != t.dtype
-                or o.numel() != n):
+        if t.device != device or not (same or (
+                o.device == device and o.dtype == t.dtype
+                and o.numel() == n)):
             raise ValueError("tensors of one device; out of the same sizes "
                              "and types")
-        if not (t.is_contiguous() and o.is_contiguous()):
+        if not (t.is_contiguous() and (same or o.is_contiguous())):
             raise ValueError("tensors must be contiguous")
-        item.src, item.dst = t.data_ptr(), o.data_ptr()
-        item.numel, item.dtype = n, _DT[t.dtype]
-        if n and item.dst in seen:
-            raise ValueError("a tensor is given twice")
-        seen.add(item.dst)
+        src = t.data_ptr()
+        dst = src if same else o.data_ptr()
+        if n:
+            filled += 1
+            seen.add(dst)
+        # MoeTensor: two pointers, the count, the type (and padding)
+        flat += (src, dst, n, dtype)
+    if len(seen) != filled:
+        raise ValueError("a tensor is given twice")
+    arr = (ctypes.c_int64 * (4 * count))(*flat)
     p, size = _grad_ws(moe_clip_workspace_size(tensors), ws, device)
-    _run("moe_clip_grads", norm, len(tensors), arr, float(max_norm),
+    _run("moe_clip_grads", device, count,
+         ctypes.cast(arr, ctypes.POINTER(_lib.MoeTensor)), float(max_norm),
          norm.data_ptr(), p, size)
 
 
