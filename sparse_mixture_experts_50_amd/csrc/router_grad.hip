@@ -295,7 +295,7 @@ __global__ __launch_bounds__(256) void router_grad_x_f32(RouterGradParams p) {
 // memory, the router rows of the 64 columns staged in LDS (zeros past E) and
 // transposed on the way to the MFMAs.  The rows of dx through the experts,
 // k fp32 rows a token, are what takes its time.
-template <int KS>                              // 64-deep stages: ep / 64
+template <int KS, bool ROWS>                   // KS 64-deep stages: ep / 64
 __global__ __launch_bounds__(256) void router_grad_x_bf16(RouterGradParams p) {
     typedef mt::Loader<true, 64, 1, 0> LB;
     __shared__ u32x4 slot[KS * LB::UNITS];
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(256) void router_grad_x_bf16(RouterGradParams p) {
     for (int k = 0; k < 2 * KS; ++k) fa[k] = as_bf16x8(*(const u32x4 *)(dl + 32 * k));
     const int c = c0 + 4 * (lane >> 4);
     floatx4 v[4];
-    expert_part<uint16_t, 4>(p, min(t, p.T - 1), c, v);
+    if (ROWS) expert_part<uint16_t, 4>(p, min(t, p.T - 1), c, v);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     floatx4 acc[4];
@@ -345,7 +345,7 @@ __global__ __launch_bounds__(256) void router_grad_x_bf16(RouterGradParams p) {
     if (t >= p.T) return;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        store4((uint16_t *)p.dx + (size_t)t * p.d + c + 16 * j, v[j] + acc[j]);
+        store4((uint16_t *)p.dx + (size_t)t * p.d + c + 16 * j, ROWS ? v[j] + acc[j] : acc[j]);
 }
 
 // dWr over one token range (of p.splits), in fp32 or, undivided, rounded.
@@ -369,13 +369,19 @@ __global__ __launch_bounds__(256) void router_grad_w_f32(RouterGradParams p) {
 
 static __device__ __align__(1024) const char zero_line[1024] = {};
 
-// 64 experts x 256 columns on the matrix cores, both operands along tokens.
-__global__ __launch_bounds__(256, 2) void router_grad_w_bf16(RouterGradParams p) {
-    typedef mt::Tiles<64, 256, 1, 4, 1, true, true> P;
+// BM experts x 256 columns on the matrix cores, both operands along tokens.
+// 64 experts, two blocks per CU, or 128: with E = 256 every column of x is
+// then read by two tiles instead of four, and a wave's fragments are read
+// from LDS for twice the MFMAs.
+template <int BM>
+__global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void router_grad_w_bf16(RouterGradParams p) {
+    constexpr int WM = BM / 64, WN = 4 / WM;
+    typedef mt::Tiles<BM, 256, WM, WN, 1, true, true> P;
+    constexpr int TN = P::TN, PARTS = BM / 32;
     __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int e0 = blockIdx.x * 64, c0 = blockIdx.y * 256;
+    const int e0 = blockIdx.x * BM, c0 = blockIdx.y * 256;
     const int per = (p.T + p.splits - 1) / p.splits;
     const int t0 = blockIdx.z * per;
     const int n = max(0, min(per, p.T - t0));       // may be 0: zeros
@@ -383,13 +389,13 @@ __global__ __launch_bounds__(256, 2) void router_grad_w_bf16(RouterGradParams p)
     const int over = n % mt::SK, head = over ? over : min(n, mt::SK);
     const uint16_t *A = (const uint16_t *)p.dl + (size_t)t0 * p.ep + e0;
     const uint16_t *B = (const uint16_t *)p.x + (size_t)t0 * p.d + c0;
-    P::Source src;
+    typename P::Source src;
     src.a = src.a2 = (uint64_t)A + ((int64_t)head - mt::SK) * p.ep * 2;
     src.b = src.b2 = (uint64_t)B + ((int64_t)head - mt::SK) * p.d * 2;
     src.kt = (n + mt::SK - 1) / mt::SK;
     src.s0 = 0;
-    P::Lanes ln;
-    ln.init(p.ep * 2, 64, p.d * 2, min(256, p.d - c0), wave, lane);
+    typename P::Lanes ln;
+    ln.init(p.ep * 2, min(BM, p.ep - e0), p.d * 2, min(256, p.d - c0), wave, lane);
     ln.split = 0;
     auto head_load = [&](const void *base, uint32_t off, int k, u32x4 *to) __attribute__((always_inline)) {
         const char *from = (const char *)base + off;
@@ -397,31 +403,33 @@ __global__ __launch_bounds__(256, 2) void router_grad_w_bf16(RouterGradParams p)
         mt::dma16_lanes(from, to);
     };
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-        head_load(A, ln.a.off[q], (wave * 64 + lane) / 8 + 32 * q, slot0 + (q * 4 + wave) * 64);
+    for (int q = 0; q < PARTS; ++q)
+        head_load(A, ln.a.off[q], (wave * 64 + lane) / (BM / 8) + 256 / (BM / 8) * q,
+                  slot0 + (q * 4 + wave) * 64);
 #pragma unroll
     for (int q = 0; q < 8; ++q)
         head_load(B, ln.b.off[q], (wave * 64 + lane) / 32 + 8 * q,
                   slot0 + (P::LA::UNITS + (q * 4 + wave) * 64));
     // no stage after the last: every lane a zeroed line (x may end anywhere)
-    P::Source none;
+    typename P::Source none;
     none.a = none.a2 = none.b = none.b2 = (uint64_t)zero_line;
     none.kt = none.s0 = 0;
-    P::Lanes still = {};
+    typename P::Lanes still = {};
     if (src.kt > 1) P::load_stage(src, ln, 1, slot1, wave);
     else P::load_stage(none, still, 1, slot1, wave);
-    floatx4 acc[4][4];
+    floatx4 acc[4][TN];
     mt::clear(acc);
-    P::run<4, 2, mt::ANY>(acc, src, ln, none, still, slot0, slot1, wave, lane);
+    P::template run<4, PARTS, mt::ANY>(acc, src, ln, none, still, slot0, slot1, wave, lane);
     __builtin_amdgcn_s_waitcnt(0);
-    const int c = c0 + wave * 64 + 4 * (lane >> 4);
-    if (c0 + wave * 64 >= p.d) return;
+    const int wm = wave / WN, wn = wave % WN;
+    const int c = c0 + wn * TN * 16 + 4 * (lane >> 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int e = e0 + 16 * i + (lane & 15);
+        const int e = e0 + (wm * 4 + i) * 16 + (lane & 15);
         if (e >= p.E) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < TN; ++j) {
+            if (c + 16 * j >= p.d) continue;
             const size_t at = (size_t)e * p.d + c + 16 * j;
             if (p.splits > 1)
                 store4(p.wr_part + blockIdx.z * (size_t)p.E * p.d + at, acc[i][j]);
@@ -485,6 +493,16 @@ void router_grad_f32(const RouterGradParams &p, hipStream_t s) {
     }
 }
 
+template <bool ROWS> void dx_rows(const RouterGradParams &p, hipStream_t s) {
+    const dim3 grid((p.T + 63) / 64, p.d / 64), block(256);
+    switch (p.ep / 64) {
+    case 1: hipLaunchKernelGGL((router_grad_x_bf16<1, ROWS>), grid, block, 0, s, p); break;
+    case 2: hipLaunchKernelGGL((router_grad_x_bf16<2, ROWS>), grid, block, 0, s, p); break;
+    case 3: hipLaunchKernelGGL((router_grad_x_bf16<3, ROWS>), grid, block, 0, s, p); break;
+    default: hipLaunchKernelGGL((router_grad_x_bf16<4, ROWS>), grid, block, 0, s, p); break;
+    }
+}
+
 hipError_t router_grad_bf16(const RouterGradParams &p, hipStream_t s) {
     if (need_logits(p)) {
         // the forward's partial logits
@@ -502,17 +520,16 @@ hipError_t router_grad_bf16(const RouterGradParams &p, hipStream_t s) {
     }
     dlogits<uint16_t>(p, s);
     if (p.dx) {
-        const dim3 grid((p.T + 63) / 64, p.d / 64);
-        switch (p.ep / 64) {
-        case 1: hipLaunchKernelGGL(router_grad_x_bf16<1>, grid, dim3(256), 0, s, p); break;
-        case 2: hipLaunchKernelGGL(router_grad_x_bf16<2>, grid, dim3(256), 0, s, p); break;
-        case 3: hipLaunchKernelGGL(router_grad_x_bf16<3>, grid, dim3(256), 0, s, p); break;
-        default: hipLaunchKernelGGL(router_grad_x_bf16<4>, grid, dim3(256), 0, s, p); break;
-        }
+        if (p.dxs || p.dx_add) dx_rows<true>(p, s);
+        else dx_rows<false>(p, s);
     }
     if (p.dwr) {
-        hipLaunchKernelGGL(router_grad_w_bf16,
-                           dim3(p.ep / 64, (p.d + 255) / 256, p.splits), dim3(256), 0, s, p);
+        const int ny = (p.d + 255) / 256;
+        if (p.E <= 64)
+            hipLaunchKernelGGL(router_grad_w_bf16<64>, dim3(1, ny, p.splits), dim3(256), 0, s, p);
+        else
+            hipLaunchKernelGGL(router_grad_w_bf16<128>, dim3((p.E + 127) / 128, ny, p.splits),
+                               dim3(256), 0, s, p);
         sum_splits<uint16_t>(p, s);
     }
     return hipSuccess;
@@ -520,11 +537,15 @@ hipError_t router_grad_bf16(const RouterGradParams &p, hipStream_t s) {
 
 }  // namespace
 
-// Enough ranges for two blocks per CU, of at least 128 tokens each.
+// Enough ranges for the blocks that the CUs hold at once (two per CU; one of
+// the 128-expert tiles), of at least 128 tokens each.
 int router_grad_splits(int dtype, int T, int d, int E) {
-    const int bn = dtype == 1 ? 256 : f32t::BN;
-    const long long tiles = (long long)((E + 63) / 64) * ((d + bn - 1) / bn);
-    long long n = (512 + tiles - 1) / tiles;
+    const bool bf16 = dtype == 1, wide = bf16 && E > 64;
+    const int bm = wide ? 128 : 64, bn = bf16 ? 256 : f32t::BN;
+    const long long tiles = (long long)((E + bm - 1) / bm) * ((d + bn - 1) / bn);
+    const long long want = wide ? 256 : 512;
+    // (rounded up to a block over, the wide tiles would need a second round)
+    long long n = wide ? want / tiles : (want + tiles - 1) / tiles;
     const long long most = (T + 127) / 128;
     if (n > most) n = most;
     return (int)(n < 1 ? 1 : n);
