@@ -17,12 +17,15 @@ __device__ __forceinline__ const T *of_group(const void *routed,
                  : (const T *)shared;
 }
 
-// Rows of group g: [start, start + rows).
+// Rows of group g: [start, start + rows).  By scalar loads (the kernels of a
+// gradient only read the offsets), which do not wait behind stores in flight.
 __device__ __forceinline__ void group_rows(const FfnGradParams &p, int g,
                                            int &start, int &rows) {
     if (g < p.E) {
-        start = p.offsets[g];
-        rows = p.offsets[g + 1] - start;
+        typedef const __attribute__((address_space(4))) int *cptr;
+        const cptr offsets = (cptr)(uint64_t)p.offsets;
+        start = offsets[g];
+        rows = offsets[g + 1] - start;
     } else {
         start = 0;
         rows = p.T;
@@ -38,7 +41,8 @@ inline long long ffn_row_tiles(const FfnGradParams &p, int bm) {
 hipError_t launch_act_grad_mfma(const FfnGradParams &p, hipStream_t s);
 hipError_t launch_row_grad_mfma(const FfnGradParams &p, hipStream_t s);
 hipError_t launch_weight_grad_mfma(const FfnGradParams &p, hipStream_t s);
-// Whether the routed groups have few rows each (another choice of tiles).
-bool mfma_few_rows(long long routed, int E);
+// Whether the products take the small tiles: routed groups of few rows each,
+// or a narrow layer.
+bool mfma_few_rows(long long routed, int E, int d, int d_ff);
 int mfma_dw_tiles(int d_ff, int act, bool few);
 int mfma_splits(long long routed, int E, int shared_rows, int N, int K);

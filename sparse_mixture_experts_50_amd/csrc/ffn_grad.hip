@@ -325,8 +325,8 @@ int ffn_grad_dx_splits(int dtype, long long routed, int E, int shared_rows, int 
                       : 1;
 }
 
-int ffn_grad_dw_tiles(int dtype, int d_ff, int act, long long routed, int E) {
-    return dtype == 1 ? mfma_dw_tiles(d_ff, act, mfma_few_rows(routed, E)) : d_ff / 32;
+int ffn_grad_dw_tiles(int dtype, int d, int d_ff, int act, long long routed, int E) {
+    return dtype == 1 ? mfma_dw_tiles(d_ff, act, mfma_few_rows(routed, E, d, d_ff)) : d_ff / 32;
 }
 
 hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype,

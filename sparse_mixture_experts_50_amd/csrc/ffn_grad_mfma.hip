@@ -48,51 +48,66 @@ __device__ __forceinline__ void act_grad(float z, float u, float &h, float &hz,
     }
 }
 
-// Writes 16 rows of a wave's TN column blocks, columns lo..hi of them, as
-// bf16, whole rows of 32 TN bytes at a time: the MFMA layout (lane: row l % 16, 4 columns from
-// 4 (l / 16)) goes through the wave's own 32 TN 16-byte units of LDS, from
-// unit u0.  (Opaque indexes for the same reason as in mfma_tile.h: the next
-// tile's loads are in flight.)
-template <int TN>
-__device__ __forceinline__ void store_rows(u32x4 *scr, int u0, const float (&v)[TN][4],
-                                           bf16 *out, size_t ld, int lo, int hi,
-                                           int lane) {
-    constexpr int CPR = TN * 2;                  // 16-byte chunks per row
-    const int l16 = lane & 15, hq = lane >> 4;
+// Stores 16 rows of a wave's TN column blocks as bf16, whole rows of 32 TN
+// bytes at a time, TN / 2 stores: the MFMA layout (lane: row l % 16, 4
+// columns from 4 (l / 16)) goes through the wave's own 32 TN 16-byte units of
+// LDS, from unit u0.  turn() writes and reads them, store() stores what was
+// read: a wave's LDS operations run in order, so the next turn() may come
+// first and hide the reads.  (Opaque indexes for the same reason as in
+// mfma_tile.h: the next tile's loads are in flight.  Straight from the
+// registers, in pieces of 64 bytes a row as below, the fine-grained weight
+// gradient took 0.78 ms instead of 0.74.)
+template <int TN> struct RowStore {
+    static constexpr int CPR = TN * 2;           // 16-byte chunks per row
+    u32x4 q[CPR / 4];
+    __device__ __forceinline__ void turn(u32x4 *scr, int u0, const float (&v)[TN][4], int lane) {
+        const int l16 = lane & 15, hq = lane >> 4;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-        u32x2 o;
-        o.x = pack_bf16x2(v[j][0], v[j][1]);
-        o.y = pack_bf16x2(v[j][2], v[j][3]);
-        int at = (u0 + l16 * CPR + ((j * 2 + (hq >> 1)) ^ (l16 & (CPR - 1)))) * 2 + (hq & 1);
-        asm("" : "+v"(at));
-        ((u32x2 *)scr)[at] = o;
-    }
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
+        for (int j = 0; j < TN; ++j) {
+            u32x2 o;
+            o.x = pack_bf16x2(v[j][0], v[j][1]);
+            o.y = pack_bf16x2(v[j][2], v[j][3]);
+            int at = (u0 + l16 * CPR + ((j * 2 + (hq >> 1)) ^ (l16 & (CPR - 1)))) * 2 + (hq & 1);
+            asm("" : "+v"(at));
+            ((u32x2 *)scr)[at] = o;
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < CPR / 4; ++i) {
-        const int r = i * (64 / CPR) + lane / CPR, c = lane % CPR;
-        int at = u0 + r * CPR + (c ^ (r & (CPR - 1)));
-        asm("" : "+v"(at));
-        const u32x4 q = scr[at];
-        if (c * 8 >= lo && c * 8 < hi) *(u32x4 *)(out + (size_t)r * ld + c * 8) = q;
+        for (int i = 0; i < CPR / 4; ++i) {
+            const int r = i * (64 / CPR) + lane / CPR, c = lane % CPR;
+            int at = u0 + r * CPR + (c ^ (r & (CPR - 1)));
+            asm("" : "+v"(at));
+            q[i] = scr[at];
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
     }
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
-}
+    __device__ __forceinline__ void store(bf16 *out, size_t ld, int lane) const {
+#pragma unroll
+        for (int i = 0; i < CPR / 4; ++i)
+            *(u32x4 *)(out + (size_t)(i * (64 / CPR) + lane / CPR) * ld + lane % CPR * 8) = q[i];
+    }
+};
 
-// The same without LDS, in pieces of 32 bytes a row.
+// The same without LDS, and of columns lo..hi only: exchanging every second
+// row of 16 lanes with the next column block gives a lane 8 columns.
 template <int TN>
 __device__ __forceinline__ void store_pieces(const float (&v)[TN][4], bf16 *out, size_t ld,
                                              int lo, int hi, int lane) {
+    static_assert(TN % 2 == 0, "pairs of column blocks");
+    const int hq = lane >> 4, c = (hq & 1) * 16 + (hq >> 1) * 8;
+    bf16 *to = out + (size_t)(lane & 15) * ld + c;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-        u32x2 o;
-        o.x = pack_bf16x2(v[j][0], v[j][1]);
-        o.y = pack_bf16x2(v[j][2], v[j][3]);
-        if (16 * j >= lo && 16 * j < hi)
-            *(u32x2 *)(out + (size_t)(lane & 15) * ld + 16 * j + 4 * (lane >> 4)) = o;
+    for (int j = 0; j < TN; j += 2) {
+        const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16x2(v[j][0], v[j][1]),
+                                                        pack_bf16x2(v[j + 1][0], v[j + 1][1]),
+                                                        false, false);
+        const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16x2(v[j][2], v[j][3]),
+                                                        pack_bf16x2(v[j + 1][2], v[j + 1][3]),
+                                                        false, false);
+        const u32x4 q = {x[0], y[0], x[1], y[1]};
+        if (16 * j + c >= lo && 16 * j + c < hi) *(u32x4 *)(to + 16 * j) = q;
     }
 }
 
@@ -107,7 +122,10 @@ __device__ __forceinline__ int tile_of(int r) {
 // A group's rows in ceil(rows / 256) tiles of one height, 32 rb rows: rb
 // (16-row blocks per wave) is what an even split needs, rounded up to 2, 4,
 // 6, 7 or 8.  (Full tiles and a remainder instead would run a group of 384
-// rows as 512 and one of 1030 as 1280, here 384 and 1120.)
+// rows as 512 and one of 1030 as 1280, here 384 and 1120.)  The last tile of
+// several ends with the group: rows that it shares with the one before are
+// computed, and written with the same bits, twice, so that every tile is
+// whole and no store is a branch.
 __device__ __forceinline__ int split_blocks(int rows) {
     const int m = (rows + 255) >> 8;
     const int rb = ((rows + m - 1) / m + 31) >> 5;
@@ -115,7 +133,7 @@ __device__ __forceinline__ int split_blocks(int rows) {
 }
 
 struct RowTile {
-    int g, row0, nrows, rb, n_tile;
+    int g, row0, rb, n_tile;
 };
 template <bool SMALL>
 __device__ __forceinline__ RowTile row_tile(const TileTable &tt, int G, int L) {
@@ -127,8 +145,8 @@ __device__ __forceinline__ RowTile row_tile(const TileTable &tt, int G, int L) {
     r.rb = SMALL ? 2 : split_blocks(rows);
     r.n_tile = local / mt;
     const int m = local - r.n_tile * mt;
-    r.row0 = __builtin_amdgcn_readfirstlane(tt.start[r.g]) + m * 32 * r.rb;
-    r.nrows = min(32 * r.rb, rows - m * 32 * r.rb);
+    r.row0 = __builtin_amdgcn_readfirstlane(tt.start[r.g]) +
+             min(m * 32 * r.rb, rows - 32 * r.rb);
     return r;
 }
 
@@ -142,17 +160,18 @@ template <bool SMALL, typename F> __device__ __forceinline__ void by_height(int 
     else f(std::integral_constant<int, 2>{});
 }
 
-// The lane index, opaque, so that per-lane addresses are not kept across
-// tiles.
+// The lane index, counted anew (opaque), so that neither it nor per-lane
+// addresses are kept in registers across tiles.
 __device__ __forceinline__ int tile_lane() {
-    int tid = threadIdx.x;
-    asm volatile("" : "+v"(tid));
-    return tid & 63;
+    uint32_t ones = ~0u;
+    asm volatile("" : "+s"(ones));
+    return __builtin_amdgcn_mbcnt_hi(ones, __builtin_amdgcn_mbcnt_lo(ones, 0));
 }
 
-// First column of a tile: the last of an axis of n >= size ends with it (and
-// computes the columns that it shares with the one before again, storing
-// only its own), so that no operand is read past its end.
+// First column of a tile: the last of an axis of n >= size ends with it, so
+// that no operand is read past its end.  (What it shares with the tile before
+// it is computed again, to the same bits; axes shorter than a tile have the
+// small tiles, which store only their own columns.)
 __device__ __forceinline__ int tile_start(int i, int size, int n) {
     return n >= size ? min(i * size, n - size) : 0;
 }
@@ -223,6 +242,7 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_rows_by_weights
     P::load_stage(src, ln, 0, slot0, wave);
     P::load_stage(src, ln, 1, slot1, wave);
     if (SMALL) P::load_stage(src, ln, 2, slot2, wave);
+    mt::wait_loads<0>();
     for (int r = 1;; ++r) {
         const int lane = tile_lane();
         L = tile_of(r);
@@ -240,15 +260,15 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_rows_by_weights
             float *plane = (Q ? p.q : p.dxs) + (size_t)split * p.rows * N;
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
-                const int m = (wm * RB + i) * 16;
-                if (m >= t.nrows) continue;
-                float *out = plane + (size_t)(t.row0 + m + (lane & 15)) * N + c0 +
-                             4 * (lane >> 4);
+                float *out = plane + (size_t)(t.row0 + (wm * RB + i) * 16 + (lane & 15)) * N +
+                             c0 + 4 * (lane >> 4);
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    if (c0 + 16 * j >= lo && c0 + 16 * j < N)
+                    if (!SMALL || (c0 + 16 * j >= lo && c0 + 16 * j < N))
                         *(floatx4 *)(out + 16 * j) = acc[i][j];
             }
+            // the next tile's loads, ahead of the stores, have landed
+            mt::wait_loads<SMALL ? 0 : RB * TN>();
         });
         if (!more) break;
         t = tn;
@@ -296,6 +316,7 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_act_grad(FfnGra
     P::load_stage(src, ln, 0, slot0, wave);
     P::load_stage(src, ln, 1, slot1, wave);
     if (SMALL) P::load_stage(src, ln, 2, slot2, wave);
+    mt::wait_loads<0>();
     for (int r = 1;; ++r) {
         const int lane = tile_lane();
         L = tile_of(r);
@@ -328,18 +349,16 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_act_grad(FfnGra
                     }
                 }
             run_tile<P, SMALL, RB, KIND>(z, src, next, ln, slot0, slot1, slot2, wave, lane);
-#pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                const int m0 = (wm * RB + i) * 16;
-                if (m0 >= t.nrows) continue;
-                const int row = t.row0 + m0 + l16;
-                const float w = p.row_w[row];
+            // q and the routing weight of row block i
+            auto fetch = [&](int i, floatx4 (&q)[TN], float &w) __attribute__((always_inline)) {
+                const int row = t.row0 + (wm * RB + i) * 16 + l16;
                 const float *qp = p.q + (size_t)row * F + cq;
-                floatx4 q[TN];
+                w = p.row_w[row];
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    q[j] = 16 * j >= lo && 16 * j < hi ? *(const floatx4 *)(qp + 16 * j)
-                                                       : floatx4{0.f, 0.f, 0.f, 0.f};
+                    q[j] = !SMALL || (16 * j >= lo && 16 * j < hi)
+                               ? *(const floatx4 *)(qp + 16 * j)
+                               : floatx4{0.f, 0.f, 0.f, 0.f};
                 if (SMALL) {
                     for (int s = 1; s < p.q_splits; ++s) {
                         const float *qs = qp + (size_t)s * p.rows * F;
@@ -348,38 +367,64 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_act_grad(FfnGra
                             if (16 * j >= lo && 16 * j < hi) q[j] += *(const floatx4 *)(qs + 16 * j);
                     }
                 }
+            };
+            // The next row block's q is on the way while one is worked on.
+            floatx4 q[2][TN];
+            float rw[2];
+            fetch(0, q[0], rw[0]);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                if (i + 1 < RB) fetch(i + 1, q[(i + 1) & 1], rw[(i + 1) & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                const int m0 = (wm * RB + i) * 16;
+                const int row = t.row0 + m0 + l16;
+                const float w = rw[i & 1];
                 float vh[TN][4], vz[TN][4], vu[TN][4], dot = 0.0f;
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
+                    float part = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float h, hz, hu;
                         act_grad<ACT>(z[i][j][e],
                                       PANELS > 1 ? z[i][j + TN * (PANELS - 1)][e] : 0.0f,
                                       h, hz, hu);
-                        const float qq = q[j][e];
-                        dot = fmaf(qq, h, dot);
+                        const float qq = q[i & 1][j][e];
+                        part = fmaf(qq, h, part);
                         vh[j][e] = w * h;
                         vz[j][e] = w * qq * hz;
                         if (PANELS > 1) vu[j][e] = w * qq * hu;
                     }
+                    // columns shared with the tile before count there
+                    dot += 16 * j >= lo ? part : 0.0f;
                 }
                 dot += __shfl_xor(dot, 16, 64);
                 dot += __shfl_xor(dot, 32, 64);
                 if (lane < 16) p.dw_part[(size_t)row * p.dw_tiles + t.n_tile * 2 + wn] = dot;
                 const size_t at = (size_t)(t.row0 + m0) * F + c0;
-                const int u0 = wave * 32 * TN;
-                auto store = [&](const float (&v)[TN][4], void *to) __attribute__((always_inline)) {
-                    if (SMALL) store_pieces<TN>(v, (bf16 *)to + at, F, lo, hi, lane);
-                    else store_rows<TN>(scr, u0, v, (bf16 *)to + at, F, lo, hi, lane);
-                };
-                store(vh, p.h);
-                store(vz, p.dz);
-                if (PANELS > 1) store(vu, p.du);
+                bf16 *h = (bf16 *)p.h + at, *dz = (bf16 *)p.dz + at;
+                bf16 *du = PANELS > 1 ? (bf16 *)p.du + at : nullptr;
+                if (SMALL) {
+                    store_pieces<TN>(vh, h, F, lo, hi, lane);
+                    store_pieces<TN>(vz, dz, F, lo, hi, lane);
+                    if (PANELS > 1) store_pieces<TN>(vu, du, F, lo, hi, lane);
+                } else {
+                    const int u0 = wave * 32 * TN;
+                    RowStore<TN> sh, sz, su;
+                    sh.turn(scr, u0, vh, lane);
+                    sz.turn(scr, u0, vz, lane);
+                    if (PANELS > 1) su.turn(scr, u0, vu, lane);
+                    sh.store(h, F, lane);
+                    sz.store(dz, F, lane);
+                    if (PANELS > 1) su.store(du, F, lane);
+                }
                 // one row block at a time: the accumulators are read as they
                 // are used, not all at once
                 __builtin_amdgcn_sched_barrier(0);
             }
+            // (the last q, waited for above, came behind the next tile's loads:
+            // these have landed; what is outstanding are the last stores)
+            mt::wait_loads<SMALL ? 0 : PANELS * TN>();
         });
         if (!more) break;
         t = tn;
@@ -402,27 +447,26 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void ffn_weight_grad(FfnGradPar
     constexpr int B = SMALL ? 128 : 256;
     typedef mt::Tiles<B, B, 2, 2, 1, true, true> P;
     constexpr int TN = P::TN, RB = B / 32;
-    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], scr[4 * 32 * TN];
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], scr[SMALL ? 1 : 4 * 32 * TN];
     const int G = p.E + p.n_shared, d = p.d, F = p.d_ff;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / 2, wn = wave % 2;
     const int mats = p.act == ACT_SWIGLU ? 3 : 2;
     const int tiles = (F + B - 1) / B * ((d + B - 1) / B);      // of a matrix
-    const int total = G * tiles * mats;
+    const int per_group = tiles * mats;
     const size_t mat = (size_t)F * d;
-    auto tile = [&](int L) __attribute__((always_inline)) {
+    auto tile = [&](int g, int local) __attribute__((always_inline)) {
         WeightTile t;
-        t.g = L / (tiles * mats);
-        int local = L - t.g * (tiles * mats);
-        const int k = local / tiles;         // dW1, dW3, dW2
+        t.g = g;
+        int k = 0;                           // dW1, dW3, dW2
+        for (; local >= tiles; local -= tiles) ++k;
         t.which = k == mats - 1 ? 1 : 2 * k;
-        local -= k * tiles;
         const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
-        const int mtiles = (M + B - 1) / B, ntiles = (N + B - 1) / B;
-        const int strip = local / (8 * ntiles), in = local - strip * 8 * ntiles;
-        const int sm = min(8, mtiles - strip * 8);
-        t.mi = strip * 8 + in % sm;
-        t.ni = in / sm;
+        const int mtiles = (M + B - 1) / B, strip_tiles = 8 * ((N + B - 1) / B);
+        const int strip = local / strip_tiles;
+        const int in = local - strip * strip_tiles, sm = mtiles - strip * 8;
+        t.ni = sm >= 8 ? in >> 3 : in / sm;
+        t.mi = strip * 8 + in - t.ni * (sm >= 8 ? 8 : sm);
         return t;
     };
     auto result = [&](const WeightTile &t) __attribute__((always_inline)) {
@@ -430,17 +474,22 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void ffn_weight_grad(FfnGradPar
                : t.which == 1 ? of_group<bf16>(p.g_w2, p.g_ws2, t.g, p.E, mat)
                               : of_group<bf16>(p.g_w3, p.g_ws3, t.g, p.E, mat);
     };
-    // the first wanted tile from round r on (r is left after it); false: none
-    auto find = [&](int &r, WeightTile &t) __attribute__((always_inline)) {
-        for (;; ++r) {
-            const int L = tile_of(r);
-            if (L >= total) return false;
-            t = tile(L);
-            if (result(t)) {
-                ++r;
-                return true;
+    // The rounds' tiles: tile `local` of group g.  (A step adds the grid's
+    // blocks, a few groups at most, without a division.)
+    int g = tile_of(0) / per_group, local = tile_of(0) - g * per_group;
+    // the first wanted tile from the one at hand on (left after it); false:
+    // none
+    auto find = [&](WeightTile &t) __attribute__((always_inline)) {
+        while (g < G) {
+            t = tile(g, local);
+            local += gridDim.x;
+            while (local >= per_group) {
+                local -= per_group;
+                ++g;
             }
+            if (result(t)) return true;
         }
+        return false;
     };
     auto source = [&](const WeightTile &t) __attribute__((always_inline)) {
         const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
@@ -448,11 +497,10 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void ffn_weight_grad(FfnGradPar
         const bf16 *b = (const bf16 *)(t.which == 1 ? p.h : p.xs);
         int start, rows;
         group_rows(p, t.g, start, rows);
-        start = __builtin_amdgcn_readfirstlane(start);
         typename P::Source s;
         s.a = s.a2 = (uint64_t)(a + (size_t)start * M + tile_start(t.mi, B, M));
         s.b = s.b2 = (uint64_t)(b + (size_t)start * N + tile_start(t.ni, B, N));
-        s.kt = __builtin_amdgcn_readfirstlane(rows) / mt::SK;
+        s.kt = rows / mt::SK;
         s.s0 = 0;
         return s;
     };
@@ -463,40 +511,52 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void ffn_weight_grad(FfnGradPar
         ln.split = 0;
         return ln;
     };
-    int r = 0;
     WeightTile t;
-    if (!find(r, t)) return;
+    if (!find(t)) return;
     typename P::Source src = source(t);
     typename P::Lanes ln = lanes(t, threadIdx.x & 63);
     P::load_stage(src, ln, 0, slot0, wave);
     P::load_stage(src, ln, 1, slot1, wave);
+    mt::wait_loads<0>();
     for (;;) {
         const int lane = tile_lane();
         WeightTile tn = t;
-        const bool more = find(r, tn);
+        const bool more = find(tn);
         if (!more) tn = t;
         const typename P::Source next = source(tn);
         const typename P::Lanes lnext = lanes(tn, lane);
-        floatx4 acc[RB][TN];
-        mt::clear(acc);
-        P::template run<RB, RB, mt::ANY>(acc, src, ln, next, lnext, slot0, slot1, wave, lane);
         const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
         bf16 *out = result(t);
         const int m0 = tile_start(t.mi, B, M) + wm * RB * 16;
         const int c0 = tile_start(t.ni, B, N) + wn * TN * 16;
+        P::by_stages(src.kt, [&](auto kind) __attribute__((always_inline)) {
+            floatx4 acc[RB][TN];
+            mt::clear(acc);
+            // its first stages, ahead of the last tile's stores, have landed
+            mt::wait_loads<SMALL ? 0 : RB * TN / 2>();
+            P::template run<RB, RB, decltype(kind)::value>(acc, src, ln, next, lnext, slot0, slot1,
+                                                           wave, lane);
+            RowStore<SMALL ? 2 : TN> rows[2];
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            const int mi = m0 + i * 16;
-            if (mi < t.mi * B || mi >= M) continue;
-            float v[TN][4];
+            for (int i = 0; i < RB; ++i) {
+                const int mi = m0 + i * 16;
+                if (SMALL && (mi < t.mi * B || mi >= M)) continue;
+                float v[TN][4];
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
+                for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[j][e] = acc[i][j][e];
-            store_rows<TN>(scr, wave * 32 * TN, v, out + (size_t)mi * N + c0, N,
-                           t.ni * B - c0, N - c0, lane);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+                    for (int e = 0; e < 4; ++e) v[j][e] = acc[i][j][e];
+                bf16 *row = out + (size_t)mi * N + c0;
+                if constexpr (SMALL) {
+                    store_pieces<TN>(v, row, N, t.ni * B - c0, N - c0, lane);
+                } else {
+                    rows[i & 1].turn(scr, wave * 32 * TN, v, lane);
+                    if (i > 0) rows[(i - 1) & 1].store(row - (size_t)16 * N, N, lane);
+                    if (i == RB - 1) rows[i & 1].store(row, N, lane);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        });
         if (!more) break;
         t = tn;
         src = next;
@@ -520,8 +580,7 @@ int grid_for(long long tiles, int per_cu) {
     return (int)(g < n ? (g < 8 ? 8 : g) : n);
 }
 
-// Groups of at most 64 rows on average: one 64-row tile holds most of them.
-bool few_rows(const FfnGradParams &p) { return mfma_few_rows(p.routed, p.E); }
+bool few_rows(const FfnGradParams &p) { return mfma_few_rows(p.routed, p.E, p.d, p.d_ff); }
 
 // Row tiles by n columns in tiles of bn.
 template <bool SMALL> int row_grid(const FfnGradParams &p, int n, int bn, int splits = 1) {
@@ -559,13 +618,17 @@ template <int ACT> void act_grad_as(const FfnGradParams &p, hipStream_t s) {
 
 }  // namespace
 
-bool mfma_few_rows(long long routed, int E) { return routed <= 64ll * E; }
+// Groups of at most 64 rows on average: one 64-row tile holds most of them.
+// And layers with an axis shorter than a large tile.
+bool mfma_few_rows(long long routed, int E, int d, int d_ff) {
+    return routed <= 64ll * E || d < Shape<false>::BN || d_ff < Shape<false>::BN;
+}
 
 // Ranges of K for N columns: as many as give two blocks per CU (of 256) a
 // tile, each of 8 stages or more.  A split product's planes are added by
 // the kernel that reads them.
 int mfma_splits(long long routed, int E, int shared_rows, int N, int K) {
-    if (!mfma_few_rows(routed, E)) return 1;
+    if (!mfma_few_rows(routed, E, N, K)) return 1;
     const long long tiles = ((routed < E ? routed : E) + (shared_rows + 63) / 64) *
                             ((N + 127) / 128);
     long long s = tiles > 0 ? 512 / tiles : 1;

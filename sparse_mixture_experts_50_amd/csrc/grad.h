@@ -81,7 +81,7 @@ struct PadParams {
 };
 hipError_t launch_pad_groups(const PadParams &p, int dtype, hipStream_t s);
 // Column tiles that launch_ffn_act_grad writes to dw_part.
-int ffn_grad_dw_tiles(int dtype, int d_ff, int act, long long routed, int E);
+int ffn_grad_dw_tiles(int dtype, int d, int d_ff, int act, long long routed, int E);
 hipError_t launch_ffn_act_grad(const FfnGradParams &p, int dtype, hipStream_t s);
 hipError_t launch_ffn_row_grad(const FfnGradParams &p, int dtype, hipStream_t s);
 hipError_t launch_ffn_weight_grad(const FfnGradParams &p, int dtype, hipStream_t s);

@@ -40,7 +40,7 @@ GradLayout layout(const moe_desc *d) {
     L.pad = take((size_t)(d->E + 1) * 4);
     L.pad_slot = take((size_t)d->T * d->k * 4);
     // column tiles of <dy W2, h>, and <dy, b2>
-    L.dw_tiles = ffn_grad_dw_tiles(d->dtype, d->d_ff, d->activation, routed_rows(d), d->E);
+    L.dw_tiles = ffn_grad_dw_tiles(d->dtype, d->d, d->d_ff, d->activation, routed_rows(d), d->E);
     L.row_w = take(L.rows * 4);
     L.xs = take(L.rows * d->d * es);
     L.dys = take(L.rows * d->d * es);

@@ -27,8 +27,8 @@ namespace mt {
 
 constexpr int SK = 64;                   // stage depth
 
-// What is known of a tile's number of stages (ANY: maybe none).
-enum Stages { EVEN, ODD, ANY };
+// A tile's number of stages.
+enum Stages { EVEN, ODD, NONE };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -45,6 +45,13 @@ __device__ __forceinline__ void dma16(uint64_t base, uint32_t off, u32x4 *lds) {
 __device__ __forceinline__ void dma16_lanes(const char *src, u32x4 *lds) {
     __builtin_amdgcn_global_load_lds(
         (const void *)src, (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+}
+
+// Waits until at most N memory operations (63: the counter's range) of the
+// wave are outstanding; they end in order.
+template <int N> __device__ __forceinline__ void wait_loads() {
+    constexpr int n = N < 63 ? N : 63;
+    __builtin_amdgcn_s_waitcnt((n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
 
 // HAND: as volatile asm.  The compiler then keeps the issue order as written
@@ -76,7 +83,13 @@ struct Loader {
     static_assert(!KF || ((W == 64 || W == 128 || W == 256) && PANELS == 1), "");
     static_assert(W % 32 == 0, "whole loads");
 
-    uint32_t off[PER];
+    // K_FIRST: the swizzle, and with it the lane's offset, repeats every 16
+    // rows of k: loads OFFS apart differ by a uniform hop only.
+    static constexpr int OFFS = !KF ? PER : W == 256 ? 2 : 1;
+    static constexpr int HOP = KSTEP * OFFS;
+
+    uint32_t off[OFFS];
+    uint32_t hop;                                    // K_FIRST: HOP rows of k
 
     // the swizzle of k row k, in 32-byte pieces
     static __device__ __forceinline__ int swz(int k) {
@@ -86,8 +99,9 @@ struct Loader {
     // ld: bytes between rows (of k: K_FIRST); valid < W: rows (K_FIRST:
     // columns, a multiple of 8) from valid on re-read the first
     __device__ __forceinline__ void init(uint32_t ld, int valid, int wave, int lane) {
+        hop = KF ? HOP * ld : 0;
 #pragma unroll
-        for (int q = 0; q < PER; ++q) {
+        for (int q = 0; q < OFFS; ++q) {
             if (KF) {
                 const int k = (wave * 64 + lane) / CPK + KSTEP * q;
                 const int cs = lane % CPK;
@@ -107,13 +121,18 @@ struct Loader {
     static __device__ __forceinline__ uint32_t step(uint32_t ld) {
         return KF ? SK * ld : SK * 2;
     }
+    // the lane's offset in load q
+    __device__ __forceinline__ uint32_t at(int q) const {
+        return off[q % OFFS] + (KF ? hop * (uint32_t)(q / OFFS) : 0u);
+    }
     // load q of the stage at base (and base2, the second panel's)
     __device__ __forceinline__ void load(uint64_t base, uint64_t base2, int q, u32x4 *st,
                                          int wave) const {
-        uint32_t o = off[q % PER];
+        uint32_t o = off[q % OFFS];
         // opaque: else the offsets, widened to 64 bits, are kept as well
         asm("" : "+v"(o));
-        dma16(PANELS > 1 && q >= PER ? base2 : base, o,
+        dma16((PANELS > 1 && q >= PER ? base2 : base) +
+                  (KF ? hop * (uint32_t)(q / OFFS) : 0u), o,
               st + (U0 + (KF ? q * 4 + wave : wave + 4 * q) * 64));
     }
 };
@@ -260,11 +279,13 @@ struct Tiles {
                        (r - NA) % RBd::READS);
             }
         }
-        // Waits for what has been asked for and reads the first fragments.
+        // Reads the first fragments, of a stage that has landed in every wave.
         __device__ __forceinline__ void begin(const u32x4 *slot0, int wave, int lane) {
+            // opaque: else the indexes of several kinds of tile are worked
+            // out, and kept, ahead of the branch between them
+            asm volatile("" : "+v"(lane));
             a.init((wave / WN) * RB * 16, lane);
             b.init((wave % WN) * TN * 16, lane);
-            __builtin_amdgcn_s_waitcnt(0);
             __builtin_amdgcn_s_barrier();
 #pragma unroll
             for (int r = 0; r < NR; ++r) read(fa0, fb0, slot0, 0, r);
@@ -320,7 +341,8 @@ struct Tiles {
     }
     // Puts every write of the accumulators above this point and every later
     // read below it (volatile asm keeps its order): above before(), or a
-    // constant may be written right ahead of its MFMA, below after().
+    // constant may be written right ahead of its MFMA, below after().  At the
+    // head of each of two ways that read them: below the branch.
     template <int RB>
     static __device__ __forceinline__ void pin(floatx4 (&acc)[RB][NC]) {
 #pragma unroll
@@ -337,19 +359,30 @@ struct Tiles {
     }
 
     // acc += A B of a tile of RB 16-row blocks per wave over its src.kt
-    // stages, the first two of which have been asked for into slot0 and slot1
-    // (by load_stage(), or by this function for the tile before): while the
-    // last two are worked on, the first two of `next` are loaded.
+    // stages, the first two of which have landed in slot0 and slot1 as far as
+    // this wave's part goes (asked for by load_stage(), or by this function
+    // for the tile before; the caller waits, so that it need not wait for its
+    // own stores): while the last two are worked on, the first two of `next`
+    // are loaded.
     // RBA: 32-row parts of A that the tile's rows need.  KIND: of src.kt.
     template <int RB, int RBA, Stages KIND>
     static __device__ __forceinline__ void run(floatx4 (&acc)[RB][NC], const Source &src,
                                                const Lanes &ln, const Source &next,
                                                const Lanes &lnext, u32x4 *slot0,
                                                u32x4 *slot1, int wave, int lane) {
+        Stage g, h;
+        if constexpr (KIND == NONE) {
+            __builtin_amdgcn_s_barrier();
+            g.set(next, lnext, 0);
+            h.set(next, lnext, 1);
+            load_all(g, lnext, slot0, wave);
+            if (next.kt > 1) load_all(h, lnext, slot1, wave);
+            pin(acc);
+            return;
+        }
         Worker<RB> w;
         pin(acc);
         w.begin(slot0, wave, lane);
-        Stage g, h;
         const int kt = src.kt;
         for (int s = 0; s + 2 < kt; s += 2) {
             g.set(src, ln, s + 2);
@@ -361,22 +394,25 @@ struct Tiles {
         }
         g.set(next, lnext, 0);
         h.set(next, lnext, 1);
-        if (KIND != ANY || kt > 0) {
-            before();
-            w.template stage<KIND == ODD, LA::LOADS, 0>(acc, g, lnext, slot0, slot1, wave);
-            after();
-        } else {
-            load_all(g, lnext, slot0, wave);
-        }
-        if (KIND == EVEN || (KIND == ANY && kt > 0 && (kt & 1) == 0)) {
+        before();
+        w.template stage<KIND == ODD, LA::LOADS, 0>(acc, g, lnext, slot0, slot1, wave);
+        after();
+        if (KIND == EVEN) {
             before();
             w.template stage<true, LA::LOADS, 0>(acc, h, lnext, slot1, slot0, wave);
             after();
-        } else if (next.kt > 1) {
+        } else if (HAND || next.kt > 1) {    // (no branch between the large tiles' AGPRs)
             load_all(h, lnext, slot1, wave);
         }
         pin(acc);
         __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // f(integral_constant<Stages, KIND>) for a tile of kt stages.
+    template <typename F> static __device__ __forceinline__ void by_stages(int kt, F f) {
+        if (kt == 0) f(std::integral_constant<Stages, NONE>{});
+        else if (!(kt & 1)) f(std::integral_constant<Stages, EVEN>{});
+        else f(std::integral_constant<Stages, ODD>{});
     }
 
     // The same through NS slots, NS - 1 stages ahead (kt >= 1): for products

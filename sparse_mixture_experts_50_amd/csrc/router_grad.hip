@@ -315,7 +315,7 @@ __global__ __launch_bounds__(256) void router_grad_x_bf16(RouterGradParams p) {
             for (int q = 0; q < LB::LOADS; ++q) {
                 const int e = s * 64 + (wave * 64 + lane) / 8 + 32 * q;
                 const uint32_t back = e < p.E ? 0 : (uint32_t)e * (uint32_t)p.d * 2;
-                mt::dma16(wr, lb.off[q] + (uint32_t)s * 128u * (uint32_t)p.d - back,
+                mt::dma16(wr, lb.at(q) + (uint32_t)s * 128u * (uint32_t)p.d - back,
                           slot + s * LB::UNITS + (q * 4 + wave) * 64);
             }
     }
@@ -404,11 +404,11 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void router_grad_w_bf16(Rout
     };
 #pragma unroll
     for (int q = 0; q < PARTS; ++q)
-        head_load(A, ln.a.off[q], (wave * 64 + lane) / (BM / 8) + 256 / (BM / 8) * q,
+        head_load(A, ln.a.at(q), (wave * 64 + lane) / (BM / 8) + 256 / (BM / 8) * q,
                   slot0 + (q * 4 + wave) * 64);
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-        head_load(B, ln.b.off[q], (wave * 64 + lane) / 32 + 8 * q,
+        head_load(B, ln.b.at(q), (wave * 64 + lane) / 32 + 8 * q,
                   slot0 + (P::LA::UNITS + (q * 4 + wave) * 64));
     // no stage after the last: every lane a zeroed line (x may end anywhere)
     typename P::Source none;
@@ -419,7 +419,11 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void router_grad_w_bf16(Rout
     else P::load_stage(none, still, 1, slot1, wave);
     floatx4 acc[4][TN];
     mt::clear(acc);
-    P::template run<4, PARTS, mt::ANY>(acc, src, ln, none, still, slot0, slot1, wave, lane);
+    mt::wait_loads<0>();
+    P::by_stages(src.kt, [&](auto kind) __attribute__((always_inline)) {
+        P::template run<4, PARTS, decltype(kind)::value>(acc, src, ln, none, still, slot0,
+                                                         slot1, wave, lane);
+    });
     __builtin_amdgcn_s_waitcnt(0);
     const int wm = wave / WN, wn = wave % WN;
     const int c = c0 + wn * TN * 16 + 4 * (lane >> 4);
