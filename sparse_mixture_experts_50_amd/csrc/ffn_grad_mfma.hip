@@ -48,49 +48,8 @@ __device__ __forceinline__ void act_grad(float z, float u, float &h, float &hz,
     }
 }
 
-// Stores 16 rows of a wave's TN column blocks as bf16, whole rows of 32 TN
-// bytes at a time, TN / 2 stores: the MFMA layout (lane: row l % 16, 4
-// columns from 4 (l / 16)) goes through the wave's own 32 TN 16-byte units of
-// LDS, from unit u0.  turn() writes and reads them, store() stores what was
-// read: a wave's LDS operations run in order, so the next turn() may come
-// first and hide the reads.  (Opaque indexes for the same reason as in
-// mfma_tile.h: the next tile's loads are in flight.  Straight from the
-// registers, in pieces of 64 bytes a row as below, the fine-grained weight
-// gradient took 0.78 ms instead of 0.74.)
-template <int TN> struct RowStore {
-    static constexpr int CPR = TN * 2;           // 16-byte chunks per row
-    u32x4 q[CPR / 4];
-    __device__ __forceinline__ void turn(u32x4 *scr, int u0, const float (&v)[TN][4], int lane) {
-        const int l16 = lane & 15, hq = lane >> 4;
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            u32x2 o;
-            o.x = pack_bf16x2(v[j][0], v[j][1]);
-            o.y = pack_bf16x2(v[j][2], v[j][3]);
-            int at = (u0 + l16 * CPR + ((j * 2 + (hq >> 1)) ^ (l16 & (CPR - 1)))) * 2 + (hq & 1);
-            asm("" : "+v"(at));
-            ((u32x2 *)scr)[at] = o;
-        }
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int i = 0; i < CPR / 4; ++i) {
-            const int r = i * (64 / CPR) + lane / CPR, c = lane % CPR;
-            int at = u0 + r * CPR + (c ^ (r & (CPR - 1)));
-            asm("" : "+v"(at));
-            q[i] = scr[at];
-        }
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_wave_barrier();
-    }
-    __device__ __forceinline__ void store(bf16 *out, size_t ld, int lane) const {
-#pragma unroll
-        for (int i = 0; i < CPR / 4; ++i)
-            *(u32x4 *)(out + (size_t)(i * (64 / CPR) + lane / CPR) * ld + lane % CPR * 8) = q[i];
-    }
-};
-
-// The same without LDS, and of columns lo..hi only: exchanging every second
+// Stores 16 rows of a wave's TN column blocks, columns lo..hi of them, as
+// bf16 and straight from the registers: exchanging every second
 // row of 16 lanes with the next column block gives a lane 8 columns.
 template <int TN>
 __device__ __forceinline__ void store_pieces(const float (&v)[TN][4], bf16 *out, size_t ld,
@@ -109,13 +68,6 @@ __device__ __forceinline__ void store_pieces(const float (&v)[TN][4], bf16 *out,
         const u32x4 q = {x[0], y[0], x[1], y[1]};
         if (16 * j + c >= lo && 16 * j + c < hi) *(u32x4 *)(to + 16 * j) = q;
     }
-}
-
-// The tile of round r: persistent blocks, each XCD (block index mod 8)
-// taking consecutive tiles.
-__device__ __forceinline__ int tile_of(int r) {
-    const int nb = gridDim.x, per = nb >> 3;
-    return r * nb + (blockIdx.x & 7) * per + (blockIdx.x >> 3);
 }
 
 // (Groups are padded to 64 rows, see pad_groups.)
@@ -158,22 +110,6 @@ template <bool SMALL, typename F> __device__ __forceinline__ void by_height(int 
     else if (rb == 6) f(std::integral_constant<int, 6>{});
     else if (rb == 4) f(std::integral_constant<int, 4>{});
     else f(std::integral_constant<int, 2>{});
-}
-
-// The lane index, counted anew (opaque), so that neither it nor per-lane
-// addresses are kept in registers across tiles.
-__device__ __forceinline__ int tile_lane() {
-    uint32_t ones = ~0u;
-    asm volatile("" : "+s"(ones));
-    return __builtin_amdgcn_mbcnt_hi(ones, __builtin_amdgcn_mbcnt_lo(ones, 0));
-}
-
-// First column of a tile: the last of an axis of n >= size ends with it, so
-// that no operand is read past its end.  (What it shares with the tile before
-// it is computed again, to the same bits; axes shorter than a tile have the
-// small tiles, which store only their own columns.)
-__device__ __forceinline__ int tile_start(int i, int size, int n) {
-    return n >= size ? min(i * size, n - size) : 0;
 }
 
 // Tiles and slots of the kernels below.  SMALL: for groups of few rows, whose
@@ -220,7 +156,7 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_rows_by_weights
     const int kt = (GATED ? 2 : 1) * K / mt::SK, per = (kt + splits - 1) / splits;
     const size_t mat = (size_t)p.d_ff * p.d;
     auto source = [&](const RowTile &t, int split) __attribute__((always_inline)) {
-        const int n0 = tile_start(t.n_tile, BN, N);
+        const int n0 = mt::tile_start(t.n_tile, BN, N);
         const size_t at = (size_t)t.row0 * K;
         typename P::Source s;
         s.a = (uint64_t)((const bf16 *)(Q ? p.dys : p.dz) + at);
@@ -231,7 +167,7 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_rows_by_weights
         s.kt = SMALL ? min(per, kt - s.s0) : kt;
         return s;
     };
-    int L = tile_of(0);
+    int L = mt::tile_of(0);
     if (L >= total) return;
     typename P::Lanes ln;
     ln.init(K * 2, BM, N * 2, min(N, BN), wave, threadIdx.x & 63);
@@ -244,8 +180,8 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_rows_by_weights
     if (SMALL) P::load_stage(src, ln, 2, slot2, wave);
     mt::wait_loads<0>();
     for (int r = 1;; ++r) {
-        const int lane = tile_lane();
-        L = tile_of(r);
+        const int lane = mt::tile_lane();
+        L = mt::tile_of(r);
         const bool more = L < total;
         const int nsplit = SMALL && more ? L / tiles : split;
         const RowTile tn = more ? row_tile<SMALL>(tt, G, L - nsplit * tiles) : t;
@@ -256,7 +192,7 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_rows_by_weights
             mt::clear(acc);
             run_tile<P, SMALL, RB, KIND>(acc, src, next, ln, slot0, slot1, slot2, wave, lane);
             const int lo = t.n_tile * BN;
-            const int c0 = tile_start(t.n_tile, BN, N) + wn * TN * 16;
+            const int c0 = mt::tile_start(t.n_tile, BN, N) + wn * TN * 16;
             float *plane = (Q ? p.q : p.dxs) + (size_t)split * p.rows * N;
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
@@ -297,7 +233,7 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_act_grad(FfnGra
     const int kt = d / mt::SK;
     const size_t mat = (size_t)F * d;
     auto source = [&](const RowTile &t) __attribute__((always_inline)) {
-        const size_t at = (size_t)tile_start(t.n_tile, BN, F) * d;
+        const size_t at = (size_t)mt::tile_start(t.n_tile, BN, F) * d;
         typename P::Source s;
         s.a = s.a2 = (uint64_t)((const bf16 *)p.xs + (size_t)t.row0 * d);
         s.b = (uint64_t)(of_group<bf16>(p.w1, p.ws1, t.g, p.E, mat) + at);
@@ -306,7 +242,7 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_act_grad(FfnGra
         s.s0 = 0;
         return s;
     };
-    int L = tile_of(0);
+    int L = mt::tile_of(0);
     if (L >= total) return;
     typename P::Lanes ln;
     ln.init(d * 2, BM, d * 2, min(F, BN), wave, threadIdx.x & 63);
@@ -318,13 +254,13 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_act_grad(FfnGra
     if (SMALL) P::load_stage(src, ln, 2, slot2, wave);
     mt::wait_loads<0>();
     for (int r = 1;; ++r) {
-        const int lane = tile_lane();
-        L = tile_of(r);
+        const int lane = mt::tile_lane();
+        L = mt::tile_of(r);
         const bool more = L < total;
         const RowTile tn = more ? row_tile<SMALL>(tt, G, L) : t;
         const typename P::Source next = source(tn);
         const int l16 = lane & 15;
-        const int c0 = tile_start(t.n_tile, BN, F) + wn * TN * 16;
+        const int c0 = mt::tile_start(t.n_tile, BN, F) + wn * TN * 16;
         // this wave's columns of the tile's own, from c0: lo..hi
         const int lo = t.n_tile * BN - c0, hi = F - c0;
         const int cq = c0 + 4 * (lane >> 4);
@@ -410,7 +346,7 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_act_grad(FfnGra
                     if (PANELS > 1) store_pieces<TN>(vu, du, F, lo, hi, lane);
                 } else {
                     const int u0 = wave * 32 * TN;
-                    RowStore<TN> sh, sz, su;
+                    mt::RowStore<TN> sh, sz, su;
                     sh.turn(scr, u0, vh, lane);
                     sz.turn(scr, u0, vz, lane);
                     if (PANELS > 1) su.turn(scr, u0, vu, lane);
@@ -476,7 +412,7 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void ffn_weight_grad(FfnGradPar
     };
     // The rounds' tiles: tile `local` of group g.  (A step adds the grid's
     // blocks, a few groups at most, without a division.)
-    int g = tile_of(0) / per_group, local = tile_of(0) - g * per_group;
+    int g = mt::tile_of(0) / per_group, local = mt::tile_of(0) - g * per_group;
     // the first wanted tile from the one at hand on (left after it); false:
     // none
     auto find = [&](WeightTile &t) __attribute__((always_inline)) {
@@ -498,8 +434,8 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void ffn_weight_grad(FfnGradPar
         int start, rows;
         group_rows(p, t.g, start, rows);
         typename P::Source s;
-        s.a = s.a2 = (uint64_t)(a + (size_t)start * M + tile_start(t.mi, B, M));
-        s.b = s.b2 = (uint64_t)(b + (size_t)start * N + tile_start(t.ni, B, N));
+        s.a = s.a2 = (uint64_t)(a + (size_t)start * M + mt::tile_start(t.mi, B, M));
+        s.b = s.b2 = (uint64_t)(b + (size_t)start * N + mt::tile_start(t.ni, B, N));
         s.kt = rows / mt::SK;
         s.s0 = 0;
         return s;
@@ -519,7 +455,7 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void ffn_weight_grad(FfnGradPar
     P::load_stage(src, ln, 1, slot1, wave);
     mt::wait_loads<0>();
     for (;;) {
-        const int lane = tile_lane();
+        const int lane = mt::tile_lane();
         WeightTile tn = t;
         const bool more = find(tn);
         if (!more) tn = t;
@@ -527,8 +463,8 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void ffn_weight_grad(FfnGradPar
         const typename P::Lanes lnext = lanes(tn, lane);
         const int M = t.which == 1 ? d : F, N = t.which == 1 ? F : d;
         bf16 *out = result(t);
-        const int m0 = tile_start(t.mi, B, M) + wm * RB * 16;
-        const int c0 = tile_start(t.ni, B, N) + wn * TN * 16;
+        const int m0 = mt::tile_start(t.mi, B, M) + wm * RB * 16;
+        const int c0 = mt::tile_start(t.ni, B, N) + wn * TN * 16;
         P::by_stages(src.kt, [&](auto kind) __attribute__((always_inline)) {
             floatx4 acc[RB][TN];
             mt::clear(acc);
@@ -536,7 +472,7 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void ffn_weight_grad(FfnGradPar
             mt::wait_loads<SMALL ? 0 : RB * TN / 2>();
             P::template run<RB, RB, decltype(kind)::value>(acc, src, ln, next, lnext, slot0, slot1,
                                                            wave, lane);
-            RowStore<SMALL ? 2 : TN> rows[2];
+            mt::RowStore<SMALL ? 2 : TN> rows[2];
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 const int mi = m0 + i * 16;
@@ -565,26 +501,11 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void ffn_weight_grad(FfnGradPar
     __builtin_amdgcn_s_waitcnt(0);
 }
 
-int cus() {
-    int dev = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess ||
-        hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-        n < 8)
-        return 256;
-    return n / 8 * 8;
-}
-
-int grid_for(long long tiles, int per_cu) {
-    const int n = cus() * per_cu;
-    const long long g = (tiles + 7) / 8 * 8;
-    return (int)(g < n ? (g < 8 ? 8 : g) : n);
-}
-
 bool few_rows(const FfnGradParams &p) { return mfma_few_rows(p.routed, p.E, p.d, p.d_ff); }
 
 // Row tiles by n columns in tiles of bn.
 template <bool SMALL> int row_grid(const FfnGradParams &p, int n, int bn, int splits = 1) {
-    return grid_for(ffn_row_tiles(p, Shape<SMALL>::BM) * ((n + bn - 1) / bn) * splits,
+    return mt::grid_for(ffn_row_tiles(p, Shape<SMALL>::BM) * ((n + bn - 1) / bn) * splits,
                     Shape<SMALL>::BLOCKS);
 }
 
@@ -660,7 +581,7 @@ hipError_t launch_weight_grad_mfma(const FfnGradParams &p, hipStream_t s) {
     const bool few = few_rows(p);
     const int b = few ? 128 : 256;
     const long long tiles = (long long)((p.d_ff + b - 1) / b) * ((p.d + b - 1) / b);
-    const int grid = grid_for(tiles * (p.E + p.n_shared) * (p.act == ACT_SWIGLU ? 3 : 2),
+    const int grid = mt::grid_for(tiles * (p.E + p.n_shared) * (p.act == ACT_SWIGLU ? 3 : 2),
                               few ? 2 : 1);
     if (few) hipLaunchKernelGGL(ffn_weight_grad<true>, dim3(grid), dim3(256), 0, s, p);
     else hipLaunchKernelGGL(ffn_weight_grad<false>, dim3(grid), dim3(256), 0, s, p);

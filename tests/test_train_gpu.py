@@ -195,6 +195,21 @@ ROUTER = [
                                    (1.0, 0.5)])
 @pytest.mark.parametrize("T,d,E,k,choice,cap", ROUTER)
 def test_router_grad(dtype, aux, z, T, d, E, k, choice, cap):
+    check_router_grad(dtype, aux, z, T, d, E, k, choice, cap, True)
+
+
+# alone, around the sizes from which its bf16 products have large tiles: token
+# and column tiles that end with their axes, 2, 3 and 4 stages of experts
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,E,k", [
+    (256, 256, 128, 4), (255, 320, 192, 3), (321, 448, 192, 3),
+    (700, 256, 256, 8), (513, 704, 128, 2), (300, 192, 256, 2),
+    (1, 256, 128, 2), (600, 576, 100, 4), (1300, 64, 64, 2)])
+def test_router_grad_alone(dtype, T, d, E, k):
+    check_router_grad(dtype, 1.0, 0.25, T, d, E, k, False, -1, False)
+
+
+def check_router_grad(dtype, aux, z, T, d, E, k, choice, cap, add):
     desc, r, rd, g, x, wr, br = make(dtype, T, d, E, k, cap=cap,
                                      choice=choice)
     dev, dt = device(), DT[dtype]
@@ -209,11 +224,15 @@ def test_router_grad(dtype, aux, z, T, d, E, k, choice, cap):
     base = normal(g, (T, d), 0.1, dt)
     w = moe.RouterWeights(wr.to(dev), br.to(dev), ebias.to(dev))
     gr = moe.Grads(desc, dev, ("x", "w_router", "b_router"))
-    gr.x.copy_(base)
+    if add:
+        gr.x.copy_(base)
+    else:
+        base.zero_()
     ws = torch.empty(moe.moe_router_grad_workspace_size(desc),
                      dtype=torch.uint8, device=dev).fill_(255)
     moe.moe_router_grad(desc, x.to(dev), w, rd, dw.to(dev), gr, ws,
-                        aux_scale=aux, z_scale=z, dx_add=gr.x)
+                        aux_scale=aux, z_scale=z,
+                        dx_add=gr.x if add else None)
 
     p = {"w_router": wr.double().requires_grad_(),
          "b_router": br.double().requires_grad_(),
