@@ -539,10 +539,13 @@ template <int ACT> void act_grad_as(const FfnGradParams &p, hipStream_t s) {
 
 }  // namespace
 
-// Groups of at most 64 rows on average: one 64-row tile holds most of them.
-// And layers with an axis shorter than a large tile.
+// Groups of at most 48 rows on average: one 64-row tile holds most of them.
+// The whole gradient with the small and with the large tiles, at 48 and 64
+// rows a group: 16 experts of 1024 x 2816 170 and 190 us, 187 and 203; 8 of
+// 4096 x 14336 1137 and 1213, 1348 and 1292; 64 gated of 2048 x 1408 853 and
+// 820, 945 and 877.  And layers with an axis shorter than a large tile.
 bool mfma_few_rows(long long routed, int E, int d, int d_ff) {
-    return routed <= 64ll * E || d < Shape<false>::BN || d_ff < Shape<false>::BN;
+    return routed <= 48ll * E || d < Shape<false>::BN || d_ff < Shape<false>::BN;
 }
 
 // Ranges of K for N columns: as many as give two blocks per CU (of 256) a

@@ -348,10 +348,9 @@ __global__ __launch_bounds__(256) void router_grad_x_bf16(RouterGradParams p) {
         store4((uint16_t *)p.dx + (size_t)t * p.d + c + 16 * j, ROWS ? v[j] + acc[j] : acc[j]);
 }
 
-// dx without the experts' part of at least 256 tokens and columns and whole
-// 64s of experts (more than 64): a matrix product of K = E in 256 x 256
-// tiles, whose time is the stores'.  8192 x 7168 with 256 experts: 52 us, the
-// kernel above 93.
+// dx without the experts' part: a matrix product of K = E in 256 x 256 tiles,
+// whose time is the stores'.  8192 x 7168 with 256 experts: 52 us, the kernel
+// above 93.
 template <mt::Stages KIND>
 __global__ __launch_bounds__(256) void router_grad_x_tiles(RouterGradParams p) {
     typedef mt::Tiles<256, 256, 2, 2, 1, false, true> P;
@@ -440,9 +439,9 @@ __global__ __launch_bounds__(256) void router_grad_w_f32(RouterGradParams p) {
 static __device__ __align__(1024) const char zero_line[1024] = {};
 
 // BM experts x 256 columns on the matrix cores, both operands along tokens.
-// 64 experts, two blocks per CU, or 128: with E = 256 every column of x is
-// then read by two tiles instead of four, and a wave's fragments are read
-// from LDS for twice the MFMAs.
+// 64 experts, two blocks per CU, or 128 (see dw_wide): with E = 256 every
+// column of x is then read by two tiles instead of four, and a wave's
+// fragments are read from LDS for twice the MFMAs.
 template <int BM>
 __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void router_grad_w_bf16(RouterGradParams p) {
     constexpr int WM = BM / 64, WN = 4 / WM;
@@ -577,6 +576,25 @@ template <bool ROWS> void dx_rows(const RouterGradParams &p, hipStream_t s) {
     }
 }
 
+// dx alone by large tiles: whole 64s of experts (a stage's depth) and a tile
+// for every CU.  The kernel and the one with a block per 64 x 64: 8192 x 7168,
+// 256 experts 52 and 93 us; the whole router gradient with both large (see
+// dw_wide) and both small: 8192 x 4096, 64 experts 91 and 101 us, 512 x 4096,
+// 64 experts 35 and 30.
+bool dx_tiles(int T, int d, int E) {
+    return E % 64 == 0 && T >= 256 && d >= 256 &&
+           (long long)((T + 255) / 256) * ((d + 255) / 256) >= 256;
+}
+
+// dWr by 128-expert tiles: more than 64 experts, and tokens for a block on
+// every CU.  With them and with 64-expert tiles: 8192 x 7168, 256 experts 55
+// and 98 us; the whole gradient with both large and both small: 512 x 4096,
+// 128 experts 44 and 38, 300 x 2048, 256 experts 47 and 38.
+bool dw_wide(int T, int d, int E) {
+    return E > 64 &&
+           (long long)((E + 127) / 128) * ((d + 255) / 256) * ((T + 127) / 128) >= 256;
+}
+
 hipError_t router_grad_bf16(const RouterGradParams &p, hipStream_t s) {
     if (need_logits(p)) {
         // the forward's partial logits
@@ -596,7 +614,7 @@ hipError_t router_grad_bf16(const RouterGradParams &p, hipStream_t s) {
     if (p.dx) {
         if (p.dxs || p.dx_add) {
             dx_rows<true>(p, s);
-        } else if (p.E > 64 && p.E % 64 == 0 && p.T >= 256 && p.d >= 256) {
+        } else if (dx_tiles(p.T, p.d, p.E)) {
             const int grid = mt::grid_for((long long)((p.T + 255) / 256) * ((p.d + 255) / 256), 1);
             if (p.E / 64 & 1)
                 hipLaunchKernelGGL(router_grad_x_tiles<mt::ODD>, dim3(grid), dim3(256), 0, s, p);
@@ -608,8 +626,9 @@ hipError_t router_grad_bf16(const RouterGradParams &p, hipStream_t s) {
     }
     if (p.dwr) {
         const int ny = (p.d + 255) / 256;
-        if (p.E <= 64)
-            hipLaunchKernelGGL(router_grad_w_bf16<64>, dim3(1, ny, p.splits), dim3(256), 0, s, p);
+        if (!dw_wide(p.T, p.d, p.E))
+            hipLaunchKernelGGL(router_grad_w_bf16<64>, dim3((p.E + 63) / 64, ny, p.splits),
+                               dim3(256), 0, s, p);
         else
             hipLaunchKernelGGL(router_grad_w_bf16<128>, dim3((p.E + 127) / 128, ny, p.splits),
                                dim3(256), 0, s, p);
@@ -623,7 +642,7 @@ hipError_t router_grad_bf16(const RouterGradParams &p, hipStream_t s) {
 // Enough ranges for the blocks that the CUs hold at once (two per CU; one of
 // the 128-expert tiles), of at least 128 tokens each.
 int router_grad_splits(int dtype, int T, int d, int E) {
-    const bool bf16 = dtype == 1, wide = bf16 && E > 64;
+    const bool bf16 = dtype == 1, wide = bf16 && dw_wide(T, d, E);
     const int bm = wide ? 128 : 64, bn = bf16 ? 256 : f32t::BN;
     const long long tiles = (long long)((E + bm - 1) / bm) * ((d + bn - 1) / bn);
     const long long want = wide ? 256 : 512;

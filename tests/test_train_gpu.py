@@ -198,13 +198,15 @@ def test_router_grad(dtype, aux, z, T, d, E, k, choice, cap):
     check_router_grad(dtype, aux, z, T, d, E, k, choice, cap, True)
 
 
-# alone, around the sizes from which its bf16 products have large tiles: token
-# and column tiles that end with their axes, 2, 3 and 4 stages of experts
+# alone; the last ones large enough for the large tiles of its bf16 products:
+# token and column tiles that end with their axes, 1 to 4 stages of experts
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,d,E,k", [
     (256, 256, 128, 4), (255, 320, 192, 3), (321, 448, 192, 3),
     (700, 256, 256, 8), (513, 704, 128, 2), (300, 192, 256, 2),
-    (1, 256, 128, 2), (600, 576, 100, 4), (1300, 64, 64, 2)])
+    (1, 256, 128, 2), (600, 576, 100, 4), (1300, 64, 64, 2),
+    (4090, 4096, 64, 4), (4090, 4096, 128, 2), (8100, 2112, 192, 3),
+    (8192, 2048, 256, 8)])
 def test_router_grad_alone(dtype, T, d, E, k):
     check_router_grad(dtype, 1.0, 0.25, T, d, E, k, False, -1, False)
 
