@@ -351,6 +351,8 @@ int moe_bias_update(int32_t E, const int32_t *counts, float target,
  * drops) belong to no token: they are neither read nor written.  A row
  * tensor may be NULL when it has no rows.  Tensors of x's, the weights' and
  * the gradients' kinds start at 16-byte boundaries (MOE_ERR_INVALID_ARG).
+ * An output overlaps neither an input nor another output, except where that
+ * is allowed below (one that starts where its input does is refused).
  * Everything here is written without atomics: the same inputs give the same
  * bits.
  * ------------------------------------------------------------------ */
@@ -397,8 +399,8 @@ typedef struct moe_grads {
 
 /* Host.  Bytes of workspace of moe_router_grad and moe_backward, functions
  * of the descriptor alone (0 if it is invalid or d or d_ff exceeds 2^20,
- * and for moe_backward if expert_fp8: FP8 experts have no gradient).  The workspace holds nothing
- * between calls; it is not the forward's. */
+ * and for moe_backward if expert_fp8: FP8 experts have no gradient).  The
+ * workspace holds nothing between calls; it is not the forward's. */
 size_t moe_router_grad_workspace_size(const moe_desc *desc);
 size_t moe_grad_workspace_size(const moe_desc *desc);
 

@@ -191,7 +191,8 @@ int moe_dispatch_rows(const moe_desc *desc, const moe_routing *r,
     int st = check_desc(desc);
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
-    if (!x || !r || !r->slot_of || (!xs && have_rows(desc)) || !aligned(x, xs))
+    if (!x || !r || !r->slot_of || (!xs && have_rows(desc)) || !aligned(x, xs) ||
+        x == xs)
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.tok = x;
@@ -204,7 +205,8 @@ int moe_dispatch_rows_grad(const moe_desc *desc, const moe_routing *r,
     int st = check_desc(desc);
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
-    if (!dx || !r || !r->slot_of || (!dxs && have_rows(desc)) || !aligned(dx, dxs))
+    if (!dx || !r || !r->slot_of || (!dxs && have_rows(desc)) ||
+        !aligned(dx, dxs) || dx == dxs)
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.rows_in = dxs;
@@ -218,7 +220,7 @@ int moe_combine_rows(const moe_desc *desc, const moe_routing *r,
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
     if (!y || !r || !r->slot_of || !r->topk_w || (!ys && have_rows(desc)) ||
-        !aligned(y, ys))
+        !aligned(y, ys) || y == ys)
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.rows_in = ys;
@@ -233,7 +235,7 @@ int moe_combine_rows_grad(const moe_desc *desc, const moe_routing *r,
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
     if (!dy || !dw || !r || !r->slot_of || !r->topk_w ||
-        ((!ys || !dys) && have_rows(desc)) || !aligned(dy, ys, dys))
+        ((!ys || !dys) && have_rows(desc)) || !aligned(dy, ys, dys) || dys == dy)
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.tok = dy;
@@ -271,6 +273,7 @@ int moe_router_grad(const moe_desc *desc, const void *x, const moe_weights *w,
     if (!aligned(x, dx_add, w->w_router, g->x, g->w_router)) return MOE_ERR_INVALID_ARG;
     const GradLayout L = layout(desc);
     if (!ws || ws_bytes < L.router_total || !aligned(ws)) return MOE_ERR_WORKSPACE;
+    if (g->x == x) return MOE_ERR_INVALID_ARG;      // read after g->x is written
     RouterGradParams p =
         router_params(desc, x, w, r, aux_scale, z_scale, g, ws, L);
     p.dw = dw;
@@ -295,6 +298,7 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
         return MOE_ERR_INVALID_ARG;
     const GradLayout L = layout(desc);
     if (!ws || ws_bytes < L.total || !aligned(ws)) return MOE_ERR_WORKSPACE;
+    if (g->x == x) return MOE_ERR_INVALID_ARG;
 
     RowsParams rp = rows_params(desc, r);
     rp.tok = x;

@@ -141,6 +141,45 @@ def test_router_grad_refuses_missing_arguments():
     assert router_grad(desc(T=0), g=_lib.MoeGrads()) == 0
 
 
+def test_misaligned_tensors_are_refused():
+    d, odd = desc(n_shared=1, activation=2), FAKE + 8
+    ws = dict(ws1=FAKE, ws2=FAKE, w3=FAKE, ws3=FAKE)
+    for name, n in ROWS.items():
+        fn = getattr(_lib.lib(), name)
+        for i in range(2 if n == 2 else 3):     # (dw is plain float)
+            args = [FAKE + 4096 * i for i in range(n)]
+            args[i] += 8
+            assert fn(ctypes.byref(d), ctypes.byref(routing()), *args,
+                      None) == -1
+    out = grads(x=FAKE + 4096)
+    for kw in (dict(x=odd), dict(dy=odd)):
+        assert backward(d, w=weights(**ws), g=out, **kw) == -1
+    for name in ("w_router", "w1", "b1", "w2", "b2", "w3", "ws1", "bs2"):
+        assert backward(d, w=weights(**{**ws, name: odd}), g=out) == -1
+    for name, _ in _lib.MoeGrads._fields_:
+        if name != "b_router":
+            assert backward(d, w=weights(**ws), g=grads(**{name: odd})) == -1
+    assert backward(d, w=weights(**ws), g=out,
+                    ws=odd) == _lib.MOE_ERR_WORKSPACE
+    assert router_grad(d, x=odd, g=out) == -1
+    assert router_grad(d, w=weights(w_router=odd), g=out) == -1
+    assert router_grad(d, g=grads(w_router=odd)) == -1
+    assert router_grad(d, g=out, ws=odd) == _lib.MOE_ERR_WORKSPACE
+
+
+def test_outputs_over_inputs_are_refused():
+    d, a, b, c = desc(), FAKE, FAKE + 4096, FAKE + 8192
+    L, r = _lib.lib(), routing()
+    for name, args in (("moe_dispatch_rows", (a, a)),
+                       ("moe_dispatch_rows_grad", (a, a)),
+                       ("moe_combine_rows", (a, a)),
+                       ("moe_combine_rows_grad", (a, b, a, c))):
+        assert getattr(L, name)(ctypes.byref(d), ctypes.byref(r), *args,
+                                None) == -1
+    assert backward(d, g=grads(x=FAKE)) == -1
+    assert router_grad(d, g=grads(x=FAKE)) == -1
+
+
 def clip(items, max_norm=1.0, norm=FAKE, ws=FAKE, ws_bytes=1 << 30, n=None):
     arr = (_lib.MoeTensor * max(1, len(items)))(*items)
     return _lib.lib().moe_clip_grads(len(items) if n is None else n, arr,

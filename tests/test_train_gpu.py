@@ -321,6 +321,13 @@ BACKWARD = [
     (64, 64, 4, 4, 64, "gelu", 0, False, 64, True),
     (64, 64, 4, 4, 64, "silu", 1, False, 0, True),       # no routed rows
     (1100, 384, 1, 1, 640, "gelu", 0, True, -1, False),  # one long group
+    # large tiles that end with their axes, by row and by column
+    (2070, 320, 2, 1, 448, "silu", 1, True, -1, False),
+    (620, 832, 3, 2, 384, "swiglu", 1, True, 300, False),
+    (97, 448, 2, 2, 320, "gelu", 0, False, -1, False),
+    # many rows of narrow layers, which have the small tiles
+    (900, 192, 2, 1, 1088, "silu", 1, True, -1, False),
+    (1000, 1024, 2, 2, 128, "swiglu", 0, False, -1, False),
 ]
 
 
