@@ -200,14 +200,18 @@ __global__ __launch_bounds__(1024) void router_grad_dlogits(RouterGradParams p) 
     p.db_part[(size_t)blockIdx.x * p.E + e] = sum;
 }
 
-// db[e]: the blocks' partial sums, 64 lanes in a fixed order.
-__global__ __launch_bounds__(64) void router_grad_bias(RouterGradParams p) {
-    const int e = blockIdx.x;
+// db[e]: the blocks' partial sums, the 64 lanes of a wave in a fixed order.
+__device__ __forceinline__ void bias_sum(const RouterGradParams &p, int e) {
+    if (e >= p.E) return;
+    const int lane = threadIdx.x & 63;
     const int n = (p.T + MOE_ROUTER_GRAD_TOKENS - 1) / MOE_ROUTER_GRAD_TOKENS;
     float sum = 0.0f;
-    for (int i = threadIdx.x; i < n; i += 64) sum += p.db_part[(size_t)i * p.E + e];
+    for (int i = lane; i < n; i += 64) sum += p.db_part[(size_t)i * p.E + e];
     sum = wave_sum(sum);
-    if (threadIdx.x == 0) p.db[e] = sum;
+    if (lane == 0) p.db[e] = sum;
+}
+__global__ __launch_bounds__(256) void router_grad_bias(RouterGradParams p) {
+    bias_sum(p, blockIdx.x * 4 + (threadIdx.x >> 6));
 }
 
 __device__ __forceinline__ floatx4 load4(const float *p) { return *(const floatx4 *)p; }
@@ -512,8 +516,13 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void router_grad_w_bf16(Rout
     }
 }
 
+// dWr of the token ranges added up in `blocks` blocks, db in the others.
 template <typename T>
-__global__ __launch_bounds__(256) void router_grad_w_sum(RouterGradParams p) {
+__global__ __launch_bounds__(256) void router_grad_w_sum(RouterGradParams p, int blocks) {
+    if ((int)blockIdx.x >= blocks) {
+        bias_sum(p, (blockIdx.x - blocks) * 4 + (threadIdx.x >> 6));
+        return;
+    }
     const size_t n = (size_t)p.E * p.d;
     const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= n) return;
@@ -529,21 +538,24 @@ __global__ __launch_bounds__(256) void zero_fill(uint16_t *p, size_t n) {
         p[i] = 0;
 }
 
+// Whether dWr's token ranges are added up by a kernel, which then does db too.
+bool sums_w(const RouterGradParams &p) { return p.dwr && p.splits > 1; }
+
 template <typename T> void dlogits(const RouterGradParams &p, hipStream_t s) {
     const int nb = (p.T + MOE_ROUTER_GRAD_TOKENS - 1) / MOE_ROUTER_GRAD_TOKENS;
     if (p.choice)
         hipLaunchKernelGGL((router_grad_dlogits<T, true>), dim3(nb), dim3(1024), 0, s, p);
     else
         hipLaunchKernelGGL((router_grad_dlogits<T, false>), dim3(nb), dim3(1024), 0, s, p);
-    if (p.db)
-        hipLaunchKernelGGL(router_grad_bias, dim3(p.E), dim3(64), 0, s, p);
+    if (p.db && !sums_w(p))
+        hipLaunchKernelGGL(router_grad_bias, dim3((p.E + 3) / 4), dim3(256), 0, s, p);
 }
 
 template <typename T> void sum_splits(const RouterGradParams &p, hipStream_t s) {
-    if (p.splits > 1)
-        hipLaunchKernelGGL((router_grad_w_sum<T>),
-                           dim3((unsigned)(((size_t)p.E * p.d / 4 + 255) / 256)),
-                           dim3(256), 0, s, p);
+    if (!sums_w(p)) return;
+    const int blocks = (int)(((size_t)p.E * p.d / 4 + 255) / 256);
+    hipLaunchKernelGGL((router_grad_w_sum<T>), dim3(blocks + (p.db ? (p.E + 3) / 4 : 0)),
+                       dim3(256), 0, s, p, blocks);
 }
 
 bool need_logits(const RouterGradParams &p) {
