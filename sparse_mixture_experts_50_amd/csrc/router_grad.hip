@@ -13,6 +13,11 @@
 //
 // Without losses top-k routing needs no logits: dl depends on the k weights
 // alone.
+//
+// Measured, 8192 tokens of 7168 columns, 256 experts, top-8, both losses (30
+// GFLOP in each of three products): logits 45 us, dl 18, dx 52, dWr 55 and its
+// sum 9.  With the experts' part dx is bound by HBM: 4096 tokens of 4096 with
+// two fp32 rows each 66 us (of 2048 with six, 79 us).
 #include "grad.h"
 #include "kernels.h"
 #include "f32_tile.h"
@@ -40,9 +45,19 @@ __device__ __forceinline__ float lane_f(float v, int l) {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), l));
 }
 
-__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store1(uint16_t *p, float v) {
-    *p = (uint16_t)f32_to_bf16_bits(v);
+// dl of token t and expert e: [T][ep / 64][parts][64], the second part what
+// the first one's rounding leaves.
+__device__ __forceinline__ void store_dl(float *dl, const RouterGradParams &p, int t, int e,
+                                         float v) {
+    dl[(size_t)t * p.ep + e] = v;
+}
+__device__ __forceinline__ void store_dl(uint16_t *dl, const RouterGradParams &p, int t, int e,
+                                         float v) {
+    const uint16_t hi = (uint16_t)f32_to_bf16_bits(v);
+    uint16_t *at = dl + (size_t)t * p.ep * p.parts + (e >> 6) * 64 * p.parts + (e & 63);
+    at[0] = hi;
+    const float left = v - bf16_lo(hi);         // (not a number if v is infinite)
+    if (p.parts == 2) at[64] = (uint16_t)f32_to_bf16_bits(left == left ? left : 0.0f);
 }
 
 // A wave per token, experts lane + 64 i.  Each block also leaves the column
@@ -185,7 +200,7 @@ __global__ __launch_bounds__(1024) void router_grad_dlogits(RouterGradParams p) 
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             const int e = lane + 64 * i;
-            if (e < p.ep) store1((T *)p.dl + (size_t)t * p.ep + e, dl[i]);
+            if (e < p.ep) store_dl((T *)p.dl, p, t, e, dl[i]);
             db[i] += dl[i];
         }
     }
@@ -299,7 +314,7 @@ __global__ __launch_bounds__(256) void router_grad_x_f32(RouterGradParams p) {
 // memory, the router rows of the 64 columns staged in LDS (zeros past E) and
 // transposed on the way to the MFMAs.  The rows of dx through the experts,
 // k fp32 rows a token, are what takes its time.
-template <int KS, bool ROWS>                   // KS 64-deep stages: ep / 64
+template <int KS, bool ROWS, int PARTS>        // KS 64-deep stages: ep / 64
 __global__ __launch_bounds__(256) void router_grad_x_bf16(RouterGradParams p) {
     typedef mt::Loader<true, 64, 1, 0> LB;
     __shared__ u32x4 slot[KS * LB::UNITS];
@@ -324,11 +339,15 @@ __global__ __launch_bounds__(256) void router_grad_x_bf16(RouterGradParams p) {
             }
     }
     const int t = t0 + (lane & 15);
-    const uint16_t *dl = (const uint16_t *)p.dl + (size_t)min(t, p.T - 1) * p.ep +
+    const uint16_t *dl = (const uint16_t *)p.dl + (size_t)min(t, p.T - 1) * p.ep * PARTS +
                          8 * (lane >> 4);
-    bf16x8 fa[2 * KS];
+    bf16x8 fa[PARTS][2 * KS];
 #pragma unroll
-    for (int k = 0; k < 2 * KS; ++k) fa[k] = as_bf16x8(*(const u32x4 *)(dl + 32 * k));
+    for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+        for (int k = 0; k < 2 * KS; ++k)
+            fa[h][k] = as_bf16x8(*(const u32x4 *)(dl + 64 * ((k >> 1) * PARTS + h) +
+                                                  32 * (k & 1)));
     const int c = c0 + 4 * (lane >> 4);
     floatx4 v[4];
     if (ROWS) expert_part<uint16_t, 4>(p, min(t, p.T - 1), c, v);
@@ -344,7 +363,9 @@ __global__ __launch_bounds__(256) void router_grad_x_bf16(RouterGradParams p) {
             bf16x8 fb = {};
             b.read(fb, slot + (k >> 1) * LB::UNITS, k & 1, j, 0, 0);
             b.read(fb, slot + (k >> 1) * LB::UNITS, k & 1, j, 0, 1);
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fa[k], acc[j], 0, 0, 0);
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h)
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fa[h][k], acc[j], 0, 0, 0);
         }
     if (t >= p.T) return;
 #pragma unroll
@@ -446,29 +467,31 @@ static __device__ __align__(1024) const char zero_line[1024] = {};
 // 64 experts, two blocks per CU, or 128 (see dw_wide): with E = 256 every
 // column of x is then read by two tiles instead of four, and a wave's
 // fragments are read from LDS for twice the MFMAs.
-template <int BM>
+// TWO: 64 experts, both parts of dl side by side.
+template <int BM, bool TWO>
 __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void router_grad_w_bf16(RouterGradParams p) {
-    constexpr int WM = BM / 64, WN = 4 / WM;
+    constexpr int WM = TWO ? 1 : BM / 64, WN = 4 / WM, RB = BM / 16 / WM, EXPERTS = TWO ? 64 : BM;
     typedef mt::Tiles<BM, 256, WM, WN, 1, true, true> P;
-    constexpr int TN = P::TN, PARTS = BM / 32;
+    constexpr int TN = P::TN, LOADS = BM / 32;
     __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int e0 = blockIdx.x * BM, c0 = blockIdx.y * 256;
+    const int e0 = blockIdx.x * EXPERTS, c0 = blockIdx.y * 256;
+    const int lda = p.ep * (TWO ? 2 : 1), a0 = e0 * (TWO ? 2 : 1);
     const int per = (p.T + p.splits - 1) / p.splits;
     const int t0 = blockIdx.z * per;
     const int n = max(0, min(per, p.T - t0));       // may be 0: zeros
     // stage 0 holds what the whole stages of 64 tokens leave over
     const int over = n % mt::SK, head = over ? over : min(n, mt::SK);
-    const uint16_t *A = (const uint16_t *)p.dl + (size_t)t0 * p.ep + e0;
+    const uint16_t *A = (const uint16_t *)p.dl + (size_t)t0 * lda + a0;
     const uint16_t *B = (const uint16_t *)p.x + (size_t)t0 * p.d + c0;
     typename P::Source src;
-    src.a = src.a2 = (uint64_t)A + ((int64_t)head - mt::SK) * p.ep * 2;
+    src.a = src.a2 = (uint64_t)A + ((int64_t)head - mt::SK) * lda * 2;
     src.b = src.b2 = (uint64_t)B + ((int64_t)head - mt::SK) * p.d * 2;
     src.kt = (n + mt::SK - 1) / mt::SK;
     src.s0 = 0;
     typename P::Lanes ln;
-    ln.init(p.ep * 2, min(BM, p.ep - e0), p.d * 2, min(256, p.d - c0), wave, lane);
+    ln.init(lda * 2, min(BM, lda - a0), p.d * 2, min(256, p.d - c0), wave, lane);
     ln.split = 0;
     auto head_load = [&](const void *base, uint32_t off, int k, u32x4 *to) __attribute__((always_inline)) {
         const char *from = (const char *)base + off;
@@ -476,7 +499,7 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void router_grad_w_bf16(Rout
         mt::dma16_lanes(from, to);
     };
 #pragma unroll
-    for (int q = 0; q < PARTS; ++q)
+    for (int q = 0; q < LOADS; ++q)
         head_load(A, ln.a.at(q), (wave * 64 + lane) / (BM / 8) + 256 / (BM / 8) * q,
                   slot0 + (q * 4 + wave) * 64);
 #pragma unroll
@@ -490,14 +513,20 @@ __global__ __launch_bounds__(256, BM == 64 ? 2 : 1) void router_grad_w_bf16(Rout
     typename P::Lanes still = {};
     if (src.kt > 1) P::load_stage(src, ln, 1, slot1, wave);
     else P::load_stage(none, still, 1, slot1, wave);
-    floatx4 acc[4][TN];
+    floatx4 acc[RB][TN];
     mt::clear(acc);
     mt::wait_loads<0>();
     P::by_stages(src.kt, [&](auto kind) __attribute__((always_inline)) {
-        P::template run<4, PARTS, decltype(kind)::value>(acc, src, ln, none, still, slot0,
+        P::template run<RB, LOADS, decltype(kind)::value>(acc, src, ln, none, still, slot0,
                                                          slot1, wave, lane);
     });
     __builtin_amdgcn_s_waitcnt(0);
+    if (TWO) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] += acc[RB - 4 + i][j];
+    }
     const int wm = wave / WN, wn = wave % WN;
     const int c = c0 + wn * TN * 16 + 4 * (lane >> 4);
 #pragma unroll
@@ -578,14 +607,18 @@ void router_grad_f32(const RouterGradParams &p, hipStream_t s) {
     }
 }
 
-template <bool ROWS> void dx_rows(const RouterGradParams &p, hipStream_t s) {
+template <bool ROWS, int PARTS> void dx_parts(const RouterGradParams &p, hipStream_t s) {
     const dim3 grid((p.T + 63) / 64, p.d / 64), block(256);
     switch (p.ep / 64) {
-    case 1: hipLaunchKernelGGL((router_grad_x_bf16<1, ROWS>), grid, block, 0, s, p); break;
-    case 2: hipLaunchKernelGGL((router_grad_x_bf16<2, ROWS>), grid, block, 0, s, p); break;
-    case 3: hipLaunchKernelGGL((router_grad_x_bf16<3, ROWS>), grid, block, 0, s, p); break;
-    default: hipLaunchKernelGGL((router_grad_x_bf16<4, ROWS>), grid, block, 0, s, p); break;
+    case 1: hipLaunchKernelGGL((router_grad_x_bf16<1, ROWS, PARTS>), grid, block, 0, s, p); break;
+    case 2: hipLaunchKernelGGL((router_grad_x_bf16<2, ROWS, PARTS>), grid, block, 0, s, p); break;
+    case 3: hipLaunchKernelGGL((router_grad_x_bf16<3, ROWS, PARTS>), grid, block, 0, s, p); break;
+    default: hipLaunchKernelGGL((router_grad_x_bf16<4, ROWS, PARTS>), grid, block, 0, s, p); break;
     }
+}
+template <bool ROWS> void dx_rows(const RouterGradParams &p, hipStream_t s) {
+    if (p.parts == 2) dx_parts<ROWS, 2>(p, s);
+    else dx_parts<ROWS, 1>(p, s);
 }
 
 // dx alone by large tiles: whole 64s of experts (a stage's depth) and a tile
@@ -594,7 +627,7 @@ template <bool ROWS> void dx_rows(const RouterGradParams &p, hipStream_t s) {
 // dw_wide) and both small: 8192 x 4096, 64 experts 91 and 101 us, 512 x 4096,
 // 64 experts 35 and 30.
 bool dx_tiles(int T, int d, int E) {
-    return E % 64 == 0 && T >= 256 && d >= 256 &&
+    return E % 64 == 0 && router_grad_parts(1, T) == 1 && d >= 256 &&
            (long long)((T + 255) / 256) * ((d + 255) / 256) >= 256;
 }
 
@@ -603,7 +636,7 @@ bool dx_tiles(int T, int d, int E) {
 // and 98 us; the whole gradient with both large and both small: 512 x 4096,
 // 128 experts 44 and 38, 300 x 2048, 256 experts 47 and 38.
 bool dw_wide(int T, int d, int E) {
-    return E > 64 &&
+    return E > 64 && router_grad_parts(1, T) == 1 &&
            (long long)((E + 127) / 128) * ((d + 255) / 256) * ((T + 127) / 128) >= 256;
 }
 
@@ -638,18 +671,28 @@ hipError_t router_grad_bf16(const RouterGradParams &p, hipStream_t s) {
     }
     if (p.dwr) {
         const int ny = (p.d + 255) / 256;
-        if (!dw_wide(p.T, p.d, p.E))
-            hipLaunchKernelGGL(router_grad_w_bf16<64>, dim3((p.E + 63) / 64, ny, p.splits),
-                               dim3(256), 0, s, p);
+        const dim3 narrow((p.E + 63) / 64, ny, p.splits);
+        if (p.parts == 2)
+            hipLaunchKernelGGL((router_grad_w_bf16<128, true>), narrow, dim3(256), 0, s, p);
+        else if (!dw_wide(p.T, p.d, p.E))
+            hipLaunchKernelGGL((router_grad_w_bf16<64, false>), narrow, dim3(256), 0, s, p);
         else
-            hipLaunchKernelGGL(router_grad_w_bf16<128>, dim3((p.E + 127) / 128, ny, p.splits),
-                               dim3(256), 0, s, p);
+            hipLaunchKernelGGL((router_grad_w_bf16<128, false>),
+                               dim3((p.E + 127) / 128, ny, p.splits), dim3(256), 0, s, p);
         sum_splits<uint16_t>(p, s);
     }
     return hipSuccess;
 }
 
 }  // namespace
+
+// dl enters the bf16 products rounded to bf16: an error of the same size as
+// the rounding of their results, independent in every token and expert, whose
+// norm over many tokens is 1.4 times that of the results' alone.  With few
+// tokens (and few experts a token) there is no such mean, and a single bad
+// rounding shows: dl is then the sum of two bf16 parts (2^-17), both
+// multiplied; such calls are bound by their launches.
+int router_grad_parts(int dtype, int T) { return dtype == 1 && T < 1024 ? 2 : 1; }
 
 // Enough ranges for the blocks that the CUs hold at once (two per CU; one of
 // the 128-expert tiles), of at least 128 tokens each.
