@@ -58,8 +58,8 @@ __device__ __forceinline__ void act_grad(float z, float u, float &h, float &hz,
 }
 
 // Stores 16 rows of a wave's TN column blocks, columns lo..hi of them, as
-// bf16 and straight from the registers: exchanging every second
-// row of 16 lanes with the next column block gives a lane 8 columns.
+// bf16 and straight from the registers: exchanging every second row of 16
+// lanes with the next column block gives a lane 8 columns.
 template <int TN>
 __device__ __forceinline__ void store_pieces(const float (&v)[TN][4], bf16 *out, size_t ld,
                                              int lo, int hi, int lane) {
@@ -82,9 +82,11 @@ __device__ __forceinline__ void store_pieces(const float (&v)[TN][4], bf16 *out,
 // (Groups are padded to 64 rows, see pad_groups.)
 // A group's rows in ceil(rows / 256) tiles of one height, 32 rb rows: rb
 // (16-row blocks per wave) is what an even split needs, rounded up to 2, 4,
-// 6, 7 or 8.  (Full tiles and a remainder instead would run a group of 384
-// rows as 512 and one of 1030 as 1280, here 384 and 1120.)  The last tile of
-// several ends with the group: rows that it shares with the one before are
+// 6, 7 or 8.  (Whole tiles of every group first and one of the 64 to 192 rows
+// left over after them: fine-grained act grad 0.53 ms instead of 0.44, dx 0.45
+// instead of 0.40, Mixtral-shaped q 0.96 instead of 0.91 and dx 0.97 instead
+// of 1.01; a stage of a low tile takes nearly as long as a whole one's.)  The
+// last tile of several ends with the group: rows that it shares with the one before are
 // computed, and written with the same bits, twice, so that every tile is
 // whole and no store is a branch.
 __device__ __forceinline__ int split_blocks(int rows) {

@@ -474,9 +474,9 @@ struct Tiles {
 // columns from 4 (l / 16)) goes through the wave's own 32 TN 16-byte units of
 // LDS, from unit u0.  turn() writes and reads them, store() stores what was
 // read: a wave's LDS operations run in order, so the next turn() may come
-// first and hide the reads.  (Opaque indexes for the same reason as above: the next tile's loads are in flight.  Straight from the
-// registers, in pieces of 64 bytes a row as below, the fine-grained weight
-// gradient took 0.78 ms instead of 0.74.)
+// first and hide the reads.  (Opaque indexes as in Reader: the next tile's
+// loads are in flight.  Straight from the registers, in pieces of 64 bytes a
+// row, the fine-grained weight gradient took 0.78 ms instead of 0.74.)
 template <int TN> struct RowStore {
     static constexpr int CPR = TN * 2;           // 16-byte chunks per row
     u32x4 q[CPR / 4];
@@ -533,7 +533,6 @@ __device__ __forceinline__ int tile_start(int i, int size, int n) {
     return n >= size ? min(i * size, n - size) : 0;
 }
 
-// Blocks of a persistent grid.
 inline int cus() {
     int dev = 0, n = 0;
     if (hipGetDevice(&dev) != hipSuccess ||
@@ -543,6 +542,7 @@ inline int cus() {
     return n / 8 * 8;
 }
 
+// Blocks of a persistent grid.
 inline int grid_for(long long tiles, int per_cu) {
     const int n = cus() * per_cu;
     const long long g = (tiles + 7) / 8 * 8;
