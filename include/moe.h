@@ -413,6 +413,8 @@ size_t moe_grad_workspace_size(const moe_desc *desc);
  * (logits, where the losses need them) and of r topk_idx, topk_w, slot_of
  * and, for aux_scale != 0, f.  Writes g->x = dx_add + the router's part
  * (dx_add [T][d] dtype, NULL = 0, may be g->x), g->w_router, g->b_router.
+ * The logits' gradient is fp32; into products of dtype bf16 it enters as the
+ * sum of two bf16 values (to 2^-16), so each result is rounded to dtype once.
  * T == 0: the weights' gradients are zeroed. */
 int moe_router_grad(const moe_desc *desc, const void *x,
                     const moe_weights *w, const moe_routing *r,

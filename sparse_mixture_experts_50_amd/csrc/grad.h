@@ -102,9 +102,8 @@ struct RouterGradParams {
     // partial sums [T][E] over depth ranges of logit_depth
     float *logits;
     int logit_splits, logit_depth;
-    void *dl;                 // [T][ep] (bf16: [T][ep / 64][parts][64]) in the
-                              // layer's type, columns E.. zero
-    int parts;
+    void *dl;                 // [T][ep] fp32 (bf16: [T][ep / 64][2][64], two
+                              // parts of each), columns E.. zero
     float *db_part;           // [ceil(T / MOE_ROUTER_GRAD_TOKENS)][E]
     float *wr_part;           // [splits][E][d]
     int splits;
@@ -122,8 +121,6 @@ struct RouterGradParams {
 #define MOE_ROUTER_GRAD_TOKENS 16
 // Token ranges that the router weight gradient is split into.
 int router_grad_splits(int dtype, int T, int d, int E);
-// bf16 parts of dl (f32: 1).
-int router_grad_parts(int dtype, int T);
 // The forward's split bf16 router alone: partial logits of p.S ranges into
 // p.part (router.hip).
 struct RouterParams;

@@ -31,7 +31,7 @@ GradLayout layout(const moe_desc *d) {
     L.logit_plan = router_plan(d->T, d->d, d->E, 256);
     if (d->dtype == MOE_F32) L.logit_plan.S = 1;
     L.logits = take((size_t)L.logit_plan.S * d->T * d->E * 4);
-    L.dl = take((size_t)d->T * L.ep * router_grad_parts(d->dtype, d->T) * es);
+    L.dl = take((size_t)d->T * L.ep * 4);      // (bf16: two parts)
     L.db_part = take((size_t)((d->T + MOE_ROUTER_GRAD_TOKENS - 1) /
                               MOE_ROUTER_GRAD_TOKENS) * d->E * 4);
     L.wr_part = take(L.splits > 1 ? (size_t)L.splits * d->E * d->d * 4 : 0);
@@ -124,7 +124,6 @@ RouterGradParams router_params(const moe_desc *d, const void *x,
     p.logit_splits = L.logit_plan.S;
     p.logit_depth = L.logit_plan.kc;
     p.dl = at(ws, L.dl);
-    p.parts = router_grad_parts(d->dtype, d->T);
     p.db_part = (float *)at(ws, L.db_part);
     p.wr_part = (float *)at(ws, L.wr_part);
     p.splits = L.splits;
