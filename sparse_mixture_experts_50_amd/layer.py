@@ -621,6 +621,14 @@ def moe_clip_grads(tensors, max_norm: float, norm, ws, out=None) -> None:
          norm.data_ptr(), p, size)
 
 
+def _capturing(device: torch.device) -> bool:
+    """Whether the device's current stream is being captured into a graph."""
+    if device.type != "cuda":
+        return False
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class MoeLayer:
     """One sparse MoE FFN layer on a GPU: weights plus reusable buffers.
 
@@ -654,7 +662,10 @@ class MoeLayer:
         self.aux_alpha = aux_alpha
         self.routing = routing
         self._bufs = {}
+        self._grads = None          # the weights' gradients
+        self._grad_mem = {}         # x's gradient and the workspace, flat
         self._grad_bufs = {}
+        self._captured = set()      # token counts that a graph works in
 
     def desc(self, T: int) -> MoeDesc:
         w = self.w
@@ -689,16 +700,43 @@ class MoeLayer:
         moe_forward(desc, x.contiguous(), self.w, r, y, ws)
         return y, r
 
+    def _grad_flat(self, name: str, n: int, dtype) -> torch.Tensor:
+        """At least n elements that calls of every T share.  Where they are
+        too few, a quarter more than before at least, so that token counts
+        that creep up do not reallocate each time."""
+        old = self._grad_mem.get(name)
+        if old is None or old.numel() < n:
+            if old is not None:
+                n = max(n, old.numel() + old.numel() // 4)
+                if old.is_cuda:
+                    old.record_stream(torch.cuda.current_stream(old.device))
+                # what a captured graph writes stays as it is
+                self._grad_bufs = {T: b for T, b in self._grad_bufs.items()
+                                   if T in self._captured}
+            self._grad_mem[name] = torch.empty(n, dtype=dtype,
+                                               device=self.w.device)
+        return self._grad_mem[name]
+
     def grad_buffers(self, T: int):
         """(descriptor, Grads of x and every weight of the layer, gradient
-        workspace) for calls of T tokens."""
+        workspace) for calls of T tokens.  The weights' gradients are the
+        same buffers for every T, and x's gradient and the workspace share
+        their memory; only a T that was captured into a graph keeps its
+        own."""
         if T not in self._grad_bufs:
             desc, w = self.desc(T), self.w
-            ws = torch.empty(moe_grad_workspace_size(desc),
-                             dtype=torch.uint8, device=w.device)
-            names = ["x"] + [n for n in _grad_shapes(desc)
-                             if getattr(w, n, None) is not None]
-            self._grad_bufs[T] = (desc, Grads(desc, w.device, names), ws)
+            need = moe_grad_workspace_size(desc)
+            if self._grads is None:
+                self._grads = Grads(desc, w.device, [
+                    n for n in _grad_shapes(desc)
+                    if getattr(w, n, None) is not None]).as_dict()
+            gx = self._grad_flat("x", T * w.d, w.dtype)
+            ws = self._grad_flat("ws", need, torch.uint8)
+            g = Grads(desc, w.device, x=gx[:T * w.d].view(T, w.d),
+                      **self._grads)
+            self._grad_bufs[T] = (desc, g, ws)
+        if _capturing(self.w.device):
+            self._captured.add(T)
         return self._grad_bufs[T]
 
     def backward(self, x: torch.Tensor, routing: Routing, dy: torch.Tensor,
@@ -706,8 +744,9 @@ class MoeLayer:
         """Gradients of sum(dy * y) + aux_scale * l_aux + z_scale * z-loss
         for the forward that had this x and left this routing: of x and of
         every weight (FP8 experts have none).  The buffers are reused by
-        the next backward with the same T; its x is (T, H) also for a
-        (B, S, H) input."""
+        the next backward, of any T: use or copy the gradients before it,
+        and run the calls of a layer one after the other.  x's gradient is
+        (T, H) also for a (B, S, H) input."""
         x = x.reshape(-1, x.shape[-1]).contiguous()
         dy = dy.reshape(-1, dy.shape[-1]).contiguous()
         desc, g, ws = self.grad_buffers(x.shape[0])
