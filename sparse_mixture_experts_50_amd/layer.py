@@ -16,6 +16,7 @@ for expert choice) in slot order, then the shared expert's, one per token.
 """
 from __future__ import annotations
 
+import copy
 import ctypes
 from typing import Optional
 
@@ -201,7 +202,12 @@ class Weights:
 
 class Routing:
     """Device buffers of the routing results and statistics (k = E for
-    expert choice)."""
+    expert choice).  One that MoeLayer.forward returned stands for that call:
+    once a later forward has filled the same buffers, the operators that take
+    it refuse it (``clone()`` it before)."""
+
+    _buffers = None      # the Routing whose buffers these are, and
+    _call = None         # the forward that filled them
 
     def __init__(self, T: int, E: int, k: int, device,
                  slots: Optional[int] = None):
@@ -222,6 +228,31 @@ class Routing:
         # z-loss, entropy (bits), load imbalance, utilization, drop rate,
         # max share
         self.monitor = z(6, dt=f32)
+
+    def clone(self) -> "Routing":
+        """A copy that later forwards leave alone."""
+        self.check_current()
+        out = copy.copy(self)
+        out._buffers = out._call = None
+        for n, _ in MoeRouting._fields_:
+            setattr(out, n, getattr(self, n).clone())
+        return out
+
+    def check_current(self) -> None:
+        """Raise ValueError if a later forward has filled the buffers."""
+        if self._buffers is not None and \
+                self._buffers._call is not self._call:
+            raise ValueError(
+                "routing of an earlier forward: its buffers hold a later "
+                "one's of as many tokens (clone() the routing before that)")
+
+    def _filled(self, captured: bool) -> "Routing":
+        """These buffers as one forward's results.  What a graph fills again
+        on every replay stands for no one call."""
+        self._call = object()
+        out = copy.copy(self)
+        out._buffers = None if captured else self
+        return out
 
     def struct(self) -> MoeRouting:
         return MoeRouting(*[_ptr(getattr(self, n)) for n, _ in
@@ -420,6 +451,7 @@ def _rows(desc, t, name, device):
 
 def _routing(desc, r: Routing, device):
     """The routing buffers of this descriptor's calls."""
+    r.check_current()
     if r.slot_of.device != device:
         raise ValueError(f"routing on {r.slot_of.device}, expected {device}")
     if (r.slot_of.shape != (desc.T, desc.k) or
@@ -625,6 +657,8 @@ def _capturing(device: torch.device) -> bool:
     """Whether the device's current stream is being captured into a graph."""
     if device.type != "cuda":
         return False
+    if device.index == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
     with torch.cuda.device(device):
         return torch.cuda.is_current_stream_capturing()
 
@@ -639,7 +673,10 @@ class MoeLayer:
     or "swiglu" (the default when the weights carry w3).
 
     ``forward(x)`` returns ``(y, routing)``; the routing buffers are reused
-    by the next call with the same T (copy them to keep them)."""
+    by the next call with the same T: ``routing.clone()`` keeps them, as a
+    second forward before the first one's backward needs.  ``backward`` and
+    the row operators refuse a routing that a later forward has overwritten;
+    they do not see the replays of a captured one."""
 
     def __init__(self, weights: Weights, k: int,
                  capacity_factor: Optional[float] = None,
@@ -698,7 +735,7 @@ class MoeLayer:
             return y.reshape(shape), r
         desc, r, ws, y = self.buffers(x.shape[0])
         moe_forward(desc, x.contiguous(), self.w, r, y, ws)
-        return y, r
+        return y, r._filled(_capturing(self.w.device))
 
     def _grad_flat(self, name: str, n: int, dtype) -> torch.Tensor:
         """At least n elements that calls of every T share.  Where they are
@@ -742,11 +779,12 @@ class MoeLayer:
     def backward(self, x: torch.Tensor, routing: Routing, dy: torch.Tensor,
                  aux_scale: float = 1.0, z_scale: float = 0.0) -> Grads:
         """Gradients of sum(dy * y) + aux_scale * l_aux + z_scale * z-loss
-        for the forward that had this x and left this routing: of x and of
-        every weight (FP8 experts have none).  The buffers are reused by
-        the next backward, of any T: use or copy the gradients before it,
-        and run the calls of a layer one after the other.  x's gradient is
-        (T, H) also for a (B, S, H) input."""
+        for the forward that had this x and left this routing (the last one
+        of as many tokens, or a clone() of its routing): of x and of every
+        weight (FP8 experts have none).  The buffers are reused by the next
+        backward, of any T: use or copy the gradients before it, and run the
+        calls of a layer one after the other.  x's gradient is (T, H) also
+        for a (B, S, H) input."""
         x = x.reshape(-1, x.shape[-1]).contiguous()
         dy = dy.reshape(-1, dy.shape[-1]).contiguous()
         desc, g, ws = self.grad_buffers(x.shape[0])

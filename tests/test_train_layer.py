@@ -52,3 +52,46 @@ def test_captured_token_counts_keep_their_buffers(monkeypatch):
     again = lay.grad_buffers(40)
     assert again[1] is g and again[2] is ws
     assert lay.grad_buffers(41)[2] is lay.grad_buffers(2000)[2]
+
+
+def test_overwritten_routing_is_refused(monkeypatch):
+    """Two forwards of as many tokens: the first one's routing is gone, and
+    every operator that takes it says so; a clone and other token counts are
+    left alone."""
+    monkeypatch.setattr(layer_module, "moe_forward", lambda *a: None)
+    monkeypatch.setattr(layer_module, "_run", lambda *a: None)
+    lay = layer()
+    x, ws = torch.zeros(6, 64), torch.zeros(1 << 20, dtype=torch.uint8)
+    rows, dw = torch.zeros(12, 64), torch.zeros(6, 2)
+    _, first = lay.forward(x)
+    first.topk_idx.fill_(1)
+    kept = first.clone()
+    lay.backward(x, first, x)
+    lay.forward(torch.zeros(7, 64))
+    lay.backward(x, first, x)
+    _, second = lay.forward(x)
+    second.topk_idx.fill_(2)
+    desc = lay.desc(6)
+    g = moe.Grads(desc, "cpu", ("x",))
+    for call in (
+            lambda r: lay.backward(x, r, x),
+            lambda r: moe.moe_dispatch_rows(desc, r, x, rows),
+            lambda r: moe.moe_dispatch_rows_grad(desc, r, rows, x),
+            lambda r: moe.moe_combine_rows(desc, r, rows, x),
+            lambda r: moe.moe_combine_rows_grad(desc, r, x, rows, rows, dw),
+            lambda r: moe.moe_router_grad(desc, x, lay.w, r, dw, g, ws),
+            lambda r: r.clone()):
+        with pytest.raises(ValueError, match="earlier forward"):
+            call(first)
+        call(second)
+        call(kept)
+    assert bool((kept.topk_idx == 1).all())
+    assert second.clone().topk_idx.data_ptr() != second.topk_idx.data_ptr()
+    # a captured forward's routing is filled anew by every replay
+    monkeypatch.setattr(layer_module, "_capturing", lambda device: True)
+    _, captured = lay.forward(x)
+    monkeypatch.setattr(layer_module, "_capturing", lambda device: False)
+    with pytest.raises(ValueError):
+        lay.backward(x, second, x)
+    lay.forward(x)
+    lay.backward(x, captured, x)

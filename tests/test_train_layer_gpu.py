@@ -70,3 +70,21 @@ def test_captured_step_outlives_larger_calls():
         for n, t in want.items():
             assert torch.equal(getattr(g, n), t), (more, n)
         assert bool((filled == 7.0).all())
+
+
+def test_two_forwards_before_their_backwards():
+    """As pipelining or a layer used twice runs them: with a clone of the
+    first routing both backwards give what a layer of their own gives;
+    without, the first one is refused."""
+    lay = make_layer()
+    (xa, da), (xb, db) = tokens(120, 1), tokens(120, 2)
+    _, ra = lay.forward(xa)
+    kept = ra.clone()
+    _, rb = lay.forward(xb)
+    with pytest.raises(ValueError, match="earlier forward"):
+        lay.backward(xa, ra, da)
+    for x, r, dy in ((xa, kept, da), (xb, rb, db)):
+        got = {n: t.clone() for n, t in lay.backward(
+            x, r, dy, z_scale=0.1).as_dict().items()}
+        for n, t in step(make_layer(), x, dy).as_dict().items():
+            assert torch.equal(got[n], t), n
