@@ -351,8 +351,9 @@ int moe_bias_update(int32_t E, const int32_t *counts, float target,
  * drops) belong to no token: they are neither read nor written.  A row
  * tensor may be NULL when it has no rows.  Tensors of x's, the weights' and
  * the gradients' kinds start at 16-byte boundaries (MOE_ERR_INVALID_ARG).
- * An output overlaps neither an input nor another output, except where that
- * is allowed below (one that starts where its input does is refused).
+ * An output overlaps neither an input, the workspace nor another output,
+ * except where that is allowed below; one that starts where one of them does
+ * is refused (MOE_ERR_INVALID_ARG; moe_clip_grads: *norm only).
  * Everything here is written without atomics: the same inputs give the same
  * bits.
  * ------------------------------------------------------------------ */

@@ -1,5 +1,7 @@
 // Host side of the training entry points of include/moe.h: argument checks,
 // workspace layout and launches, as for the forward in moe_api.hip.
+#include <initializer_list>
+
 #include "../../include/moe.h"
 #include "grad.h"
 #include "host.h"
@@ -89,6 +91,19 @@ bool aligned_weights(const moe_weights *w) {
 bool aligned_grads(const moe_grads *g) {
     return aligned(g->x, g->w_router, g->w1, g->w2, g->w3, g->ws1, g->ws2, g->ws3,
                    g->b1, g->b2, g->b3, g->bs1, g->bs2, g->bs3);
+}
+
+// Whether an output starts where an input or another output does.
+bool clash(std::initializer_list<const void *> outs,
+           std::initializer_list<const void *> ins) {
+    for (const void *const *o = outs.begin(); o != outs.end(); ++o) {
+        if (!*o) continue;
+        for (const void *i : ins)
+            if (*o == i) return true;
+        for (const void *const *q = outs.begin(); q != o; ++q)
+            if (*o == *q) return true;
+    }
+    return false;
 }
 
 // The gradient's kernels hold row offsets within a tile in 32 bits.
@@ -192,7 +207,7 @@ int moe_dispatch_rows(const moe_desc *desc, const moe_routing *r,
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
     if (!x || !r || !r->slot_of || (!xs && have_rows(desc)) || !aligned(x, xs) ||
-        x == xs)
+        clash({xs}, {x, r->slot_of}))
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.tok = x;
@@ -206,7 +221,7 @@ int moe_dispatch_rows_grad(const moe_desc *desc, const moe_routing *r,
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
     if (!dx || !r || !r->slot_of || (!dxs && have_rows(desc)) ||
-        !aligned(dx, dxs) || dx == dxs)
+        !aligned(dx, dxs) || clash({dx}, {dxs, r->slot_of}))
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.rows_in = dxs;
@@ -220,7 +235,7 @@ int moe_combine_rows(const moe_desc *desc, const moe_routing *r,
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
     if (!y || !r || !r->slot_of || !r->topk_w || (!ys && have_rows(desc)) ||
-        !aligned(y, ys) || y == ys)
+        !aligned(y, ys) || clash({y}, {ys, r->slot_of, r->topk_w}))
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.rows_in = ys;
@@ -235,7 +250,8 @@ int moe_combine_rows_grad(const moe_desc *desc, const moe_routing *r,
     if (st != MOE_OK) return st;
     if (desc->T == 0) return MOE_OK;
     if (!dy || !dw || !r || !r->slot_of || !r->topk_w ||
-        ((!ys || !dys) && have_rows(desc)) || !aligned(dy, ys, dys) || dys == dy)
+        ((!ys || !dys) && have_rows(desc)) || !aligned(dy, ys, dys) ||
+        clash({dys, dw}, {dy, r->slot_of, r->topk_w}) || dw == ys)
         return MOE_ERR_INVALID_ARG;
     RowsParams p = rows_params(desc, r);
     p.tok = dy;
@@ -273,7 +289,11 @@ int moe_router_grad(const moe_desc *desc, const void *x, const moe_weights *w,
     if (!aligned(x, dx_add, w->w_router, g->x, g->w_router)) return MOE_ERR_INVALID_ARG;
     const GradLayout L = layout(desc);
     if (!ws || ws_bytes < L.router_total || !aligned(ws)) return MOE_ERR_WORKSPACE;
-    if (g->x == x) return MOE_ERR_INVALID_ARG;      // read after g->x is written
+    if (clash({g->x, g->w_router, g->b_router},
+              {x, dw, ws, w->w_router, w->b_router, w->expert_bias, r->topk_idx,
+               r->topk_w, r->slot_of, r->f}) ||
+        clash({g->w_router, g->b_router}, {dx_add}))
+        return MOE_ERR_INVALID_ARG;
     RouterGradParams p =
         router_params(desc, x, w, r, aux_scale, z_scale, g, ws, L);
     p.dw = dw;
@@ -298,7 +318,12 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
         return MOE_ERR_INVALID_ARG;
     const GradLayout L = layout(desc);
     if (!ws || ws_bytes < L.total || !aligned(ws)) return MOE_ERR_WORKSPACE;
-    if (g->x == x) return MOE_ERR_INVALID_ARG;
+    if (clash({g->x, g->w_router, g->b_router, g->w1, g->b1, g->w2, g->b2, g->ws1,
+               g->bs1, g->ws2, g->bs2, g->w3, g->b3, g->ws3, g->bs3},
+              {x, dy, ws, w->w_router, w->b_router, w->expert_bias, w->w1, w->b1,
+               w->w2, w->b2, w->ws1, w->bs1, w->ws2, w->bs2, w->w3, w->b3, w->ws3,
+               w->bs3, r->topk_idx, r->topk_w, r->offsets, r->slot_of, r->f}))
+        return MOE_ERR_INVALID_ARG;
 
     RowsParams rp = rows_params(desc, r);
     rp.tok = x;
@@ -429,6 +454,10 @@ int moe_clip_grads(int32_t n, const moe_tensor *tensors, float max_norm,
         if (t.numel > (1ll << 40)) return MOE_ERR_UNSUPPORTED;
     }
     if (!ws || ws_bytes < moe_clip_workspace_size(n)) return MOE_ERR_WORKSPACE;
+    for (int i = 0; i < n; ++i)
+        if (tensors[i].src == norm || tensors[i].dst == norm)
+            return MOE_ERR_INVALID_ARG;
+    if (ws == norm) return MOE_ERR_INVALID_ARG;
     hipStream_t s = (hipStream_t)stream;
     const int tables = clip_tables(n), most = clip_blocks(tables);
     double *part = (double *)ws;
