@@ -92,7 +92,7 @@ typedef enum {
     MOE_OK = 0,
     MOE_ERR_INVALID_ARG = -1, /* null pointer, bad size, k out of range */
     MOE_ERR_UNSUPPORTED = -2, /* shape or dtype this library cannot run */
-    MOE_ERR_WORKSPACE = -3,   /* workspace missing or too small */
+    MOE_ERR_WORKSPACE = -3,   /* workspace missing, too small or misaligned */
     MOE_ERR_HIP = -4,         /* a HIP launch failed */
     MOE_ERR_SCRATCH = -5      /* moe_forward_noalloc: the shape needs more
                                  than MOE_NOALLOC_SCRATCH_BYTES of scratch */
@@ -350,7 +350,8 @@ int moe_bias_update(int32_t E, const int32_t *counts, float target,
  * per token (row R + t).  Routed rows at and beyond offsets[E] (capacity
  * drops) belong to no token: they are neither read nor written.  A row
  * tensor may be NULL when it has no rows.  Tensors of x's, the weights' and
- * the gradients' kinds start at 16-byte boundaries (MOE_ERR_INVALID_ARG).
+ * the gradients' kinds start at 16-byte boundaries (MOE_ERR_INVALID_ARG), and
+ * so do workspaces (MOE_ERR_WORKSPACE).
  * An output overlaps neither an input, the workspace nor another output,
  * except where that is allowed below; one that starts where one of them does
  * is refused (MOE_ERR_INVALID_ARG; moe_clip_grads: *norm only).

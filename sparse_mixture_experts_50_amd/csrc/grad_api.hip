@@ -453,7 +453,8 @@ int moe_clip_grads(int32_t n, const moe_tensor *tensors, float max_norm,
         // chunk numbers are 32-bit within a launch
         if (t.numel > (1ll << 40)) return MOE_ERR_UNSUPPORTED;
     }
-    if (!ws || ws_bytes < moe_clip_workspace_size(n)) return MOE_ERR_WORKSPACE;
+    if (!ws || ws_bytes < moe_clip_workspace_size(n) || !aligned(ws))
+        return MOE_ERR_WORKSPACE;
     for (int i = 0; i < n; ++i)
         if (tensors[i].src == norm || tensors[i].dst == norm)
             return MOE_ERR_INVALID_ARG;

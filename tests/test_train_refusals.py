@@ -1,5 +1,5 @@
-"""Outputs laid over inputs or over each other are refused before any HIP call
-(host without a GPU)."""
+"""Outputs laid over inputs or over each other, and a misaligned workspace, are
+refused before any HIP call (host without a GPU)."""
 import ctypes
 
 import pytest
@@ -93,3 +93,9 @@ def test_clip_norm_over_a_tensor():
     a, b = (STEP, STEP, 8, 0), (2 * STEP, 3 * STEP, 8, 1)
     for norm in (STEP, 2 * STEP, 3 * STEP, 4 * STEP):
         assert clip([a, b], norm, 4 * STEP) == -1
+
+
+def test_clip_misaligned_workspace():
+    for off in (1, 4, 8):
+        assert clip([(STEP, STEP, 8, 0)], 2 * STEP, 3 * STEP + off) == \
+            _lib.MOE_ERR_WORKSPACE
