@@ -389,7 +389,9 @@ int moe_combine_rows_grad(const moe_desc *desc, const moe_routing *r,
 /* Gradients of a layer: caller-owned device buffers, each of its weight's
  * shape and type (b_router fp32; x [T][d]), written whole, not added to.
  * NULL = not wanted.  There is no gradient of expert_bias (balancing state,
- * stepped by moe_bias_update).  Groups without rows get zeros. */
+ * stepped by moe_bias_update).  Groups without rows get zeros, and so do
+ * (from moe_backward) gradients of weights that the descriptor's layer does
+ * not have: w3, b3 without SwiGLU, the shared expert's without one. */
 typedef struct moe_grads {
     void *x;
     void *w_router;

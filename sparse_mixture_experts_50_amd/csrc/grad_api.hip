@@ -186,6 +186,27 @@ int zero_grads(const moe_desc *d, const moe_grads *g, hipStream_t s) {
     return MOE_OK;
 }
 
+// The wanted gradients of weights that take no part in the layer.
+moe_grads absent_grads(const moe_desc *d, const moe_grads *g) {
+    moe_grads a = {};
+    const bool gated = d->activation == MOE_ACT_SWIGLU;
+    if (!gated) {
+        a.w3 = g->w3;
+        a.b3 = g->b3;
+    }
+    if (!d->n_shared) {
+        a.ws1 = g->ws1;
+        a.bs1 = g->bs1;
+        a.ws2 = g->ws2;
+        a.bs2 = g->bs2;
+    }
+    if (!gated || !d->n_shared) {
+        a.ws3 = g->ws3;
+        a.bs3 = g->bs3;
+    }
+    return a;
+}
+
 constexpr int kClipBlocks = 2048;
 constexpr int kClipLeast = 64;
 
@@ -402,6 +423,8 @@ int moe_backward(const moe_desc *desc, const void *x, const moe_weights *w,
     p.dx_splits = L.dx_splits;
     p.routed = (int)routed_rows(desc);
 
+    const moe_grads absent = absent_grads(desc, g);
+    if ((st = zero_grads(desc, &absent, s)) != MOE_OK) return st;
     const bool weights = p.g_w1 || p.g_w2 || p.g_w3 || p.g_ws1 || p.g_ws2 || p.g_ws3;
     const bool biases = p.g_b1 || p.g_b2 || p.g_b3 || p.g_bs1 || p.g_bs2 || p.g_bs3;
     const bool router = g->x || g->w_router || g->b_router;

@@ -88,3 +88,42 @@ def test_two_forwards_before_their_backwards():
             x, r, dy, z_scale=0.1).as_dict().items()}
         for n, t in step(make_layer(), x, dy).as_dict().items():
             assert torch.equal(got[n], t), n
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("act,shared", [("gelu", 0), ("silu", 1),
+                                        ("swiglu", 0)])
+def test_gradients_of_weights_that_the_layer_lacks(act, shared, dtype):
+    """Wanted all the same they are zeros, also of calls that want nothing
+    else."""
+    dev, T, d, E, F = device(), 40, 128, 4, 128
+    desc = moe.make_desc(T, d, E, 2, F, dtype, n_shared=shared,
+                         activation=act)
+
+    def z(*s):
+        return torch.randn(s, device=dev).mul_(0.1).to(dtype)
+
+    w = moe.Weights(z(E, d), z(E, F, d), z(E, d, F),
+                    ws1=z(F, d) if shared else None,
+                    ws2=z(d, F) if shared else None,
+                    w3=z(E, F, d) if act == "swiglu" else None)
+    lay = moe.MoeLayer(w, 2, activation=act)
+    x, dy = z(T, d), z(T, d)
+    _, r = lay.forward(x)
+    want = {n: t.clone() for n, t in lay.backward(x, r, dy).as_dict().items()}
+    lacks = ([] if act == "swiglu" else ["w3", "b3"]) + \
+        ([] if shared else ["ws1", "bs1", "ws2", "bs2"]) + \
+        ([] if shared and act == "swiglu" else ["ws3", "bs3"])
+    ws = torch.empty(moe.moe_grad_workspace_size(desc), dtype=torch.uint8,
+                     device=dev)
+    for names in (lacks, [*lacks, *want], lacks[-1:]):
+        g = moe.Grads(desc, dev, names)
+        for t in g.as_dict().values():
+            t.fill_(7.0)
+        moe.moe_backward(desc, x, w, r, dy, g, ws, aux_scale=1.0)
+        for n in names:
+            got = getattr(g, n)
+            if n in lacks:
+                assert not got.any(), n
+            else:
+                assert torch.equal(got, want[n]), n
