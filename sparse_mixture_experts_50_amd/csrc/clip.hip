@@ -5,12 +5,14 @@
 // Bound by HBM: one read for the norm, one read and one write for the
 // clipping.  Both passes walk 32 KB chunks of all tensors, dealt round-robin
 // to the blocks, so tensors of any mix of sizes keep every CU busy; the
-// second pass walks them backwards and finds the first pass's last 256 MB
-// in the last-level cache.  Squares are summed in double: HBM leaves the
-// double rate idle, large values cannot overflow and the sum of 1e9 squares
-// keeps its digits.  Every block of the second pass adds the at most 2048
-// partial sums by itself (16 KB out of L2) instead of waiting for a launch
-// that does only that.  The order of every sum is fixed.
+// second pass walks them (and the tables of 96 tensors, one a launch)
+// backwards and finds the first pass's last 256 MB in the last-level cache.
+// Squares are summed in double: HBM leaves the double rate idle, large values
+// cannot overflow and the sum of 1e9 squares keeps its digits.  Every block of
+// the second pass adds the partial sums by itself instead of waiting for a
+// launch that does only that: at most 2048 of them up to 32 tables (16 KB out
+// of L2), 64 for each table of a longer list.  The order of every sum is
+// fixed.
 //
 // Measured: 24 tensors of both types, 8.5 GB read and written, 2.35 ms, 5.4
 // TB/s of the 12.7 GB that two passes move; 40 tensors of 0.7 MB together 45

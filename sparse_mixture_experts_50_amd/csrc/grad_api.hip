@@ -515,7 +515,8 @@ int moe_clip_grads(int32_t n, const moe_tensor *tensors, float max_norm,
         parts += grid;
     }
     float *out = norm;
-    for (int k = 0; k < tables && write; ++k) {
+    // backwards, as within a table: the last tensors are still cached
+    for (int k = tables - 1; k >= 0 && write; --k) {
         const long long chunks = fill(k, tab);
         if (chunks == 0) continue;
         const int grid = (int)(chunks < kClipBlocks ? chunks : kClipBlocks);
