@@ -16,7 +16,7 @@ for expert choice) in slot order, then the shared expert's, one per token.
 """
 from __future__ import annotations
 
-import copy
+import collections
 import ctypes
 from typing import Optional
 
@@ -232,7 +232,7 @@ class Routing:
     def clone(self) -> "Routing":
         """A copy that later forwards leave alone."""
         self.check_current()
-        out = copy.copy(self)
+        out = self._copy()
         out._buffers = out._call = None
         for n, _ in MoeRouting._fields_:
             setattr(out, n, getattr(self, n).clone())
@@ -250,8 +250,13 @@ class Routing:
         """These buffers as one forward's results.  What a graph fills again
         on every replay stands for no one call."""
         self._call = object()
-        out = copy.copy(self)
+        out = self._copy()
         out._buffers = None if captured else self
+        return out
+
+    def _copy(self) -> "Routing":
+        out = Routing.__new__(Routing)
+        out.__dict__.update(self.__dict__)
         return out
 
     def struct(self) -> MoeRouting:
@@ -616,8 +621,9 @@ def moe_clip_workspace_size(tensors) -> int:
 def moe_clip_grads(tensors, max_norm: float, norm, ws, out=None) -> None:
     """Global norm of contiguous float32 / bfloat16 tensors into norm [1]
     (float32), and the tensors scaled by min(1, max_norm / (norm + 1e-6)),
-    in place or into ``out`` (tensors of the same sizes and types).  ``ws``
-    of moe_clip_workspace_size(tensors) bytes."""
+    in place or into ``out`` (tensors of the same sizes and types, each its
+    own gradient or apart from all of them).  ``ws`` of
+    moe_clip_workspace_size(tensors) bytes."""
     device = norm.device
     _need(norm, "norm", (1,), torch.float32, device)
     out = tensors if out is None else out
@@ -625,7 +631,7 @@ def moe_clip_grads(tensors, max_norm: float, norm, ws, out=None) -> None:
     if len(out) != count:
         raise ValueError("out: as many tensors as there are gradients")
     same = out is tensors
-    flat, seen, filled = [], set(), 0
+    flat, seen, pairs = [], set(), []
     for t, o in zip(tensors, out):
         n, dtype = t.numel(), _DT.get(t.dtype)
         if dtype is None:
@@ -640,12 +646,16 @@ def moe_clip_grads(tensors, max_norm: float, norm, ws, out=None) -> None:
         src = t.data_ptr()
         dst = src if same else o.data_ptr()
         if n:
-            filled += 1
             seen.add(dst)
+            pairs.append((src, dst))
         # MoeTensor: two pointers, the count, the type (and padding)
         flat += (src, dst, n, dtype)
-    if len(seen) != filled:
+    if len(seen) != len(pairs):
         raise ValueError("a tensor is given twice")
+    if not same and not seen.isdisjoint(s for s, _ in pairs):
+        times = collections.Counter(s for s, _ in pairs)
+        if any(times[d] > (s == d) for s, d in pairs):
+            raise ValueError("out: a tensor is another's gradient")
     arr = (ctypes.c_int64 * (4 * count))(*flat)
     p, size = _grad_ws(moe_clip_workspace_size(tensors), ws, device)
     _run("moe_clip_grads", device, count,
@@ -758,8 +768,8 @@ class MoeLayer:
         """(descriptor, Grads of x and every weight of the layer, gradient
         workspace) for calls of T tokens.  The weights' gradients are the
         same buffers for every T, and x's gradient and the workspace share
-        their memory; only a T that was captured into a graph keeps its
-        own."""
+        their memory, which is replaced when a larger call needs more; a T
+        that was captured into a graph keeps the buffers of its capture."""
         if T not in self._grad_bufs:
             desc, w = self.desc(T), self.w
             need = moe_grad_workspace_size(desc)

@@ -3,7 +3,10 @@ refused before any HIP call (host without a GPU)."""
 import ctypes
 
 import pytest
+import torch
 
+import sparse_mixture_experts_50_amd as moe
+import sparse_mixture_experts_50_amd.layer as layer_module
 from sparse_mixture_experts_50_amd import _lib
 from test_train_abi import desc
 
@@ -99,3 +102,20 @@ def test_clip_misaligned_workspace():
     for off in (1, 4, 8):
         assert clip([(STEP, STEP, 8, 0)], 2 * STEP, 3 * STEP + off) == \
             _lib.MOE_ERR_WORKSPACE
+
+
+def test_clip_out_over_another_tensor(monkeypatch):
+    """Each result goes to its own tensor or apart from all of them."""
+    a, b, n = torch.ones(8), torch.ones(8), torch.zeros(1)
+    ws = torch.zeros(moe.moe_clip_workspace_size([a, b]), dtype=torch.uint8)
+    new = torch.empty(8)
+    for src, out in (([a, b], [b, a]), ([a, b], [new, a]), ([a, b], [a, a]),
+                     ([a, b], [b, new]), ([a, a], [a, new])):
+        with pytest.raises(ValueError, match="twice|another"):
+            moe.moe_clip_grads(src, 1.0, n, ws, out=out)
+    sent = []
+    monkeypatch.setattr(layer_module, "_run", lambda *args: sent.append(1))
+    for src, out in (([a, b], [a, new]), ([a, b], [a, b]), ([a, a], [b, new]),
+                     ([a, torch.empty(0)], [new, torch.empty(0)])):
+        moe.moe_clip_grads(src, 1.0, n, ws, out=out)
+    assert len(sent) == 4
