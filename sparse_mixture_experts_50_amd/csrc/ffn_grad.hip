@@ -20,7 +20,8 @@
 // bf16 layer's groups.  f32, 4000 tokens, 4 experts of 1024 x 1024, top-2:
 // 1.1 ms for the whole gradient, 76 TFLOP/s of fp32 MFMAs; the smallest layer
 // (256 tokens, 8 experts of 64 x 256) is bound by the latency of its 12
-// launches, 3 to 14 us each.
+// launches, 2 to 14 us each, one after the other (what depends on what is six
+// or seven deep).
 #include "ffn_grad.h"
 #include "f32_tile.h"
 
