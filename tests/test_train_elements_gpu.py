@@ -170,7 +170,10 @@ def router(dtype, T, d, E, k, choice, cap, aux, z, alpha, dw_size):
     (1500, 576, 100, 4, False, -1), (2050, 192, 65, 2, False, -1),
     (4090, 4096, 64, 4, False, -1), (8100, 2112, 192, 3, False, -1),
     (4097, 4096, 128, 2, False, -1), (8192, 2048, 256, 8, False, -1),
-    (1030, 256, 60, 60, True, 40)])
+    (1030, 256, 60, 60, True, 40),
+    # wide rows: the large tiles with few tokens
+    (513, 11008, 64, 2, False, -1), (300, 16448, 128, 2, False, -1),
+    (500, 8192, 200, 3, False, -1), (1100, 8192, 100, 2, False, -1)])
 def test_router_elements(dtype, T, d, E, k, choice, cap):
     router(dtype, T, d, E, k, choice, cap, 1.0, 0.25, 0.01, 1.0)
 
