@@ -203,8 +203,8 @@ class Weights:
 class Routing:
     """Device buffers of the routing results and statistics (k = E for
     expert choice).  One that MoeLayer.forward returned stands for that call:
-    once a later forward has filled the same buffers, the operators that take
-    it refuse it (``clone()`` it before)."""
+    once a later forward has filled the same buffers, the training operators
+    refuse it (``clone()`` it before)."""
 
     _buffers = None      # the Routing whose buffers these are, and
     _call = None         # the forward that filled them
