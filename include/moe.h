@@ -464,6 +464,66 @@ size_t moe_clip_workspace_size(int32_t n);
 int moe_clip_grads(int32_t n, const moe_tensor *tensors, float max_norm,
                    float *norm, void *ws, size_t ws_bytes, void *stream);
 
+/* One tensor of an AdamW step: numel elements, param (param_dtype) and
+ * master updated in place, grad read.
+ *   master         fp32 copy of a MOE_BF16 param, or NULL: the step is then
+ *                  taken on it, and param is its value rounded to nearest
+ *   m, v           the moments: fp32 [numel], or (state_bits 8) OCP E4M3
+ *                  bytes [numel] in blocks of 32 elements, the second moment
+ *                  as its square root
+ *   m_scale,       (state_bits 8) uint8 [ceil(numel / 32)]: a block's values
+ *   v_scale        are e4m3(byte) * 2^(scale - 127)
+ * Fresh states and scales are zero bytes.  param and grad are aligned to
+ * their elements, the others to 16 bytes (scales: 1).  numel == 0: skipped. */
+typedef struct moe_adamw_tensor {
+    void *param;
+    const void *grad;
+    float *master;
+    void *m, *v;
+    uint8_t *m_scale, *v_scale;
+    int64_t numel;
+    double weight_decay;
+    int32_t param_dtype, grad_dtype;
+} moe_adamw_tensor;
+
+/* What the tensors of a step share.  Host struct; steps, lr_scale and norm
+ * are device pointers, or NULL:
+ *   step        number t of this step, from 1 (steps == NULL)
+ *   steps       steps done so far; t is one more, and the call adds 1 at its
+ *               end (for a step captured into a graph)
+ *   lr_scale    [1], multiplies lr (a schedule that a graph replays)
+ *   norm        [1] of moe_clip_grads: gradients enter as
+ *               grad * min(1, max_norm / (norm + 1e-6))
+ *   state_bits  32 or 8
+ *   stochastic  1: a MOE_BF16 param without master is rounded at random, up
+ *               with the probability of the part that is lost; 0: to nearest.
+ *               8-bit states always are
+ *   seed        the random bits are a function of seed, t, the tensor's place
+ *               in the list and the element alone */
+typedef struct moe_adamw {
+    double lr, beta1, beta2, eps;
+    int64_t step;
+    int64_t *steps;
+    const float *lr_scale;
+    const float *norm;
+    float max_norm;
+    int32_t state_bits;
+    int32_t stochastic;
+    uint32_t seed;
+} moe_adamw;
+
+/* One AdamW step over n tensors, with g the (clipped) gradient:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   x = x - (lr weight_decay x
+ *            + lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps))
+ * in fp32, from m and v before they are rounded to 8 bits.  A block of 8-bit
+ * states with a value that is not finite becomes not-a-number throughout.
+ * Needs 0 <= beta1, beta2 < 1, eps > 0, lr and weight_decay finite and >= 0.
+ * `tensors` is a HOST array, read during the call.  No buffer of one tensor
+ * may be one of another's (only a tensor's own are compared). */
+int moe_adamw_step(const moe_adamw *h, int32_t n,
+                   const moe_adamw_tensor *tensors, void *stream);
+
 /* Host.  Static English text of a moe_status value. */
 const char *moe_status_string(int status);
 

@@ -15,10 +15,12 @@ from .layer import (Grads, MoeLayer, RouterWeights, Routing,  # noqa: F401
                     moe_dispatch_rows_grad,
                     moe_ffn_down, moe_ffn_up, moe_forward, moe_forward_noalloc,
                     moe_gemm_tail_split,
-                    moe_gemm_variant, moe_grad_workspace_size,
+                    moe_gemm_variant, moe_grad_norm, moe_grad_workspace_size,
                     moe_grouped_ffn, moe_permute, moe_route_dispatch,
                     moe_router_grad, moe_router_grad_workspace_size,
                     moe_router_topk,
                     moe_workspace_size)
+
+from .optim import AdamW  # noqa: F401
 
 __version__ = "0.1.0"

@@ -69,6 +69,23 @@ class MoeTensor(ctypes.Structure):
                 ("dtype", c_i32)]
 
 
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [("param", c_vp), ("grad", c_vp), ("master", c_vp),
+                ("m", c_vp), ("v", c_vp), ("m_scale", c_vp),
+                ("v_scale", c_vp), ("numel", ctypes.c_int64),
+                ("weight_decay", ctypes.c_double), ("param_dtype", c_i32),
+                ("grad_dtype", c_i32)]
+
+
+class MoeAdamw(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double),
+                ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("step", ctypes.c_int64), ("steps", c_vp),
+                ("lr_scale", c_vp), ("norm", c_vp),
+                ("max_norm", ctypes.c_float), ("state_bits", c_i32),
+                ("stochastic", c_i32), ("seed", ctypes.c_uint32)]
+
+
 # (name, restype, argtypes) of every entry point of include/moe.h
 SIGNATURES = {
     "moe_capacity": (c_i32, [c_i32, c_i32, ctypes.c_double]),
@@ -143,6 +160,8 @@ SIGNATURES = {
     "moe_clip_grads": (ctypes.c_int, [c_i32, ctypes.POINTER(MoeTensor),
                                       ctypes.c_float, c_vp, c_vp,
                                       ctypes.c_size_t, c_vp]),
+    "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(MoeAdamw), c_i32,
+                                      ctypes.POINTER(MoeAdamwTensor), c_vp]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_version": (ctypes.c_char_p, []),
 }

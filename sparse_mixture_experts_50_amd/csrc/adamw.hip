@@ -1,0 +1,295 @@
+// One AdamW step over many tensors.  With g the gradient (times the clipping
+// factor min(1, max_norm / (norm + 1e-6)) where a norm is given) and t the
+// number of the step:
+//   m = b1 m + (1 - b1) g          v = b2 v + (1 - b2) g^2
+//   x = x - (lr decay x + lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps))
+// The clipping factor enters here instead of in a pass of its own over the
+// gradients, and is not rounded to their type.
+//
+// 8-bit states.  Blocks of 32 elements share a power of two, the least one
+// under which the block's largest magnitude is at most 448, and hold e4m3
+// codes: a power of two costs no rounding of its own.  v is held as its root,
+// which has m's range: v itself would need twice the exponents.  Codes are
+// rounded at random, with probabilities that make the mean right: a step of
+// e4m3 is 2^-3 of the value, and rounding to nearest would throw away every
+// change of less than half of it, as (1 - b2) g^2 nearly always is.  A root
+// that is not 0 never becomes 0 (m / eps would be what follows).  The update
+// itself uses m and v before they are rounded.  The random bits are a hash of
+// seed, step, tensor and element, so the same call gives the same bits.
+// bf16 parameters without a master copy can be rounded in the same way: lr
+// is far below 2^-9 of a parameter, and nearest rounding keeps small updates
+// out.
+//
+// m and v are computed without contraction, in the order written above, and
+// the root is correctly rounded: the codes are then a function of the inputs
+// that plain elementary operations reproduce bit for bit.
+//
+// Bound by HBM: every operand is read and written once, by 32 KB and more of
+// loads in flight per CU; chunks of 16384 elements of all tensors are dealt
+// round-robin to the blocks, as the clipping's are.
+#include "adamw.h"
+
+namespace {
+
+constexpr int THREADS = 256;
+
+__device__ __forceinline__ uint32_t hash32(uint32_t x) {
+    x ^= x >> 16;
+    x *= 0x7FEB352Du;
+    x ^= x >> 15;
+    x *= 0x846CA68Bu;
+    return x ^ (x >> 16);
+}
+
+// V elements from e0 on, as fp32 (zero from n on).  whole: all of them, at an
+// address of a vector's alignment.
+template <int V>
+__device__ __forceinline__ void load(float (&x)[V], const void *p, bool f32, long long e0,
+                                     long long n, bool whole) {
+    if (whole) {
+        if (f32) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const floatx4 q = *(const floatx4 *)((const float *)p + e0 + i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i + e] = q[e];
+            }
+        } else {
+            const uint16_t *h = (const uint16_t *)p + e0;
+            uint32_t w[V / 2];
+            if (V == 8) *(u32x4 *)w = *(const u32x4 *)h;
+            else *(u32x2 *)w = *(const u32x2 *)h;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                x[2 * i] = bf16_lo(w[i]);
+                x[2 * i + 1] = bf16_hi(w[i]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = 0.0f;
+            if (e0 + i < n)
+                x[i] = f32 ? ((const float *)p)[e0 + i]
+                           : bf16_to_f32(((const uint16_t *)p)[e0 + i]);
+        }
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void store(const float (&x)[V], void *p, bool f32, long long e0,
+                                      long long n, bool whole) {
+    if (whole) {
+        if (f32) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                *(floatx4 *)((float *)p + e0 + i) =
+                    floatx4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+        } else {
+            uint16_t *h = (uint16_t *)p + e0;
+            uint32_t w[V / 2];
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+            if (V == 8) *(u32x4 *)h = *(u32x4 *)w;
+            else *(u32x2 *)h = *(u32x2 *)w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e0 + i < n) {
+                if (f32) ((float *)p)[e0 + i] = x[i];
+                else ((uint16_t *)p)[e0 + i] = (uint16_t)f32_to_bf16_bits(x[i]);
+            }
+    }
+}
+
+// The largest of 4 neighbouring lanes' values, in each of them.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));
+    return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));
+}
+
+// The lane's 8 codes of 32 as fp32.
+__device__ __forceinline__ void decode(float (&x)[8], u32x2 code, uint32_t scale) {
+    const float s = __uint_as_float(scale << 23);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(code[w], false);
+        const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(code[w], true);
+        x[4 * w] = a[0] * s;
+        x[4 * w + 1] = a[1] * s;
+        x[4 * w + 2] = b[0] * s;
+        x[4 * w + 3] = b[1] * s;
+    }
+}
+
+// The 8 codes of a lane's values, in a block of 4 lanes; scale: exponent + 127
+// of the block's power of two.  rnd: 16 random bits of each.  A block with a
+// value that is not finite is not-a-number throughout.
+template <bool ROOT>
+__device__ __forceinline__ u32x2 encode(const float (&x)[8], const uint32_t (&rnd)[8],
+                                        uint32_t &scale) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    top = quad_max(top);
+    // one more where the mantissa is over 1.75: 448 = 1.75 * 2^8
+    int e = (int)((top + 0x1FFFFFu) >> 23) - 8;
+    e = top == 0 ? 127 : max(e, 1);
+    const bool finite = top < 0x7F800000u;
+    if (!finite) e = 127;
+    scale = (uint32_t)e;
+    u32x2 out;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        uint32_t word = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const float v = x[4 * w + b];
+            // e4m3's smallest normal number to fp32's, 2^20 units a step
+            const float y = __builtin_amdgcn_ldexpf(fabsf(v), 7 - e);
+            uint32_t c = (__float_as_uint(y) + (rnd[4 * w + b] << 4)) >> 20;
+            c = min(c, 0x7Eu);
+            if (ROOT) c = v > 0.0f ? max(c, 1u) : c;
+            else c |= (__float_as_uint(v) >> 24) & (v != 0.0f ? 0x80u : 0u);
+            word |= c << (8 * b);
+        }
+        out[w] = finite ? word : 0x7F7F7F7Fu;
+    }
+    return out;
+}
+
+template <bool Q8>
+__global__ __launch_bounds__(THREADS) void adamw(AdamwTable tab, AdamwParams p) {
+#pragma clang fp contract(off)
+    constexpr int V = Q8 ? 8 : 4;
+    double lr = p.lr, bias1 = p.bias1, bias2 = p.bias2;
+    uint32_t step = (uint32_t)p.step;
+    if (p.steps) {
+        const int64_t t = *p.steps + 1;
+        step = (uint32_t)t;
+        bias1 = -expm1((double)t * p.log_b1);
+        bias2 = -expm1((double)t * p.log_b2);
+    }
+    if (p.lr_scale) lr *= (double)*p.lr_scale;
+    const float size = (float)(lr / bias1), unbias = (float)(1.0 / sqrt(bias2));
+    float f = 1.0f;
+    if (p.norm) {
+        // not fmin: a norm that is not a number has to reach the parameters
+        const double c = (double)p.max_norm / ((double)*p.norm + 1e-6);
+        f = c >= 1.0 ? 1.0f : (float)c;
+    }
+    for (int c = blockIdx.x; c < tab.first[tab.count]; c += gridDim.x) {
+        int lo = 0, hi = tab.count;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tab.first[mid] <= c) lo = mid; else hi = mid;
+        }
+        const AdamwTensor &t = tab.t[lo];
+        const bool pf32 = t.flags & ADAMW_PARAM_F32, gf32 = t.flags & ADAMW_GRAD_F32;
+        const bool aligned = t.flags & ADAMW_ALIGNED;
+        const long long n = t.n;
+        const float decay = (float)(lr * t.decay);
+        const uint32_t key = p.seed * 0x9E3779B1u + step * 0x85EBCA77u +
+                             (uint32_t)(p.index0 + lo) * 0xC2B2AE3Du;
+        const bool any = p.stochastic && !pf32 && !t.master;
+        const long long start = (long long)(c - tab.first[lo]) * MOE_ADAMW_CHUNK;
+        const long long end = min(start + MOE_ADAMW_CHUNK, n);
+        // (whole blocks of 4 lanes go round together)
+        for (long long b0 = start; b0 < end; b0 += THREADS * V) {
+            const long long e0 = b0 + (long long)threadIdx.x * V;
+            const bool live = e0 < n;
+            const bool whole = e0 + V <= n, vec = whole && aligned;
+            float x[V], g[V], m[V], v[V];
+            u32x2 mc = {0, 0}, vc = {0, 0};
+            uint32_t ms = 127, vs = 127;
+            load(g, t.grad, gf32, e0, n, vec);
+            if (t.master) load(x, t.master, true, e0, n, whole);
+            else load(x, t.param, pf32, e0, n, vec);
+            if constexpr (Q8) {
+                if (whole) {
+                    mc = *(const u32x2 *)((const uint8_t *)t.m + e0);
+                    vc = *(const u32x2 *)((const uint8_t *)t.v + e0);
+                } else if (live) {
+                    for (int i = 0; i < n - e0; ++i) {
+                        mc[i >> 2] |= (uint32_t)((const uint8_t *)t.m)[e0 + i] << (8 * (i & 3));
+                        vc[i >> 2] |= (uint32_t)((const uint8_t *)t.v)[e0 + i] << (8 * (i & 3));
+                    }
+                }
+                if (live) {
+                    ms = t.m_scale[e0 / MOE_ADAMW_BLOCK];
+                    vs = t.v_scale[e0 / MOE_ADAMW_BLOCK];
+                }
+                decode(m, mc, ms);
+                decode(v, vc, vs);
+            } else {
+                load(m, t.m, true, e0, n, whole);
+                load(v, t.v, true, e0, n, whole);
+            }
+            float root[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float gi = g[i] * f;
+                if (Q8) v[i] = v[i] * v[i];
+                m[i] = m[i] * p.b1 + gi * p.c1;
+                v[i] = v[i] * p.b2 + gi * gi * p.c2;
+                root[i] = sqrtf(v[i]);
+                const float upd = size * m[i] * __builtin_amdgcn_rcpf(root[i] * unbias + p.eps);
+                x[i] = x[i] - (x[i] * decay + upd);
+            }
+            uint32_t rm[V], rv[V];
+            if (Q8 || any) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const uint32_t r = hash32((uint32_t)(e0 + i) ^ key);
+                    rm[i] = r & 0xFFFFu;
+                    rv[i] = r >> 16;
+                    // (kept apart from the states' bits; a NaN stays one)
+                    if (any && x[i] == x[i])
+                        x[i] = __uint_as_float((__float_as_uint(x[i]) +
+                                                (hash32(r ^ 0x5BD1E995u) >> 16)) & 0xFFFF0000u);
+                }
+            }
+            if (t.master) store(x, t.master, true, e0, n, whole);
+            store(x, t.param, pf32, e0, n, vec);
+            if constexpr (Q8) {
+                mc = encode<false>(m, rm, ms);
+                vc = encode<true>(root, rv, vs);
+                if (whole) {
+                    *(u32x2 *)((uint8_t *)t.m + e0) = mc;
+                    *(u32x2 *)((uint8_t *)t.v + e0) = vc;
+                } else if (live) {
+                    for (int i = 0; i < n - e0; ++i) {
+                        ((uint8_t *)t.m)[e0 + i] = (uint8_t)(mc[i >> 2] >> (8 * (i & 3)));
+                        ((uint8_t *)t.v)[e0 + i] = (uint8_t)(vc[i >> 2] >> (8 * (i & 3)));
+                    }
+                }
+                if (live && (e0 & (MOE_ADAMW_BLOCK - 1)) == 0) {
+                    t.m_scale[e0 / MOE_ADAMW_BLOCK] = (uint8_t)ms;
+                    t.v_scale[e0 / MOE_ADAMW_BLOCK] = (uint8_t)vs;
+                }
+            } else {
+                store(m, t.m, true, e0, n, whole);
+                store(v, t.v, true, e0, n, whole);
+            }
+        }
+    }
+}
+
+__global__ void adamw_tick(int64_t *steps) { *steps += 1; }
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamwTable &tab, const AdamwParams &p, int bits,
+                        int grid, hipStream_t s) {
+    if (bits == 8)
+        hipLaunchKernelGGL(adamw<true>, dim3(grid), dim3(THREADS), 0, s, tab, p);
+    else
+        hipLaunchKernelGGL(adamw<false>, dim3(grid), dim3(THREADS), 0, s, tab, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_adamw_tick(int64_t *steps, hipStream_t s) {
+    hipLaunchKernelGGL(adamw_tick, dim3(1), dim3(1), 0, s, steps);
+    return hipGetLastError();
+}

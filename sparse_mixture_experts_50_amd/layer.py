@@ -663,6 +663,28 @@ def moe_clip_grads(tensors, max_norm: float, norm, ws, out=None) -> None:
          norm.data_ptr(), p, size)
 
 
+def moe_grad_norm(tensors, norm, ws) -> None:
+    """The norm of moe_clip_grads alone, into norm [1]; the tensors stay as
+    they are (moe_clip_grads without outputs)."""
+    device = norm.device
+    _need(norm, "norm", (1,), torch.float32, device)
+    flat = []
+    for t in tensors:
+        dtype = _DT.get(t.dtype)
+        if dtype is None:
+            raise ValueError(f"unsupported dtype {t.dtype}")
+        if t.device != device:
+            raise ValueError("tensors of one device")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        flat += (t.data_ptr(), 0, t.numel(), dtype)
+    arr = (ctypes.c_int64 * len(flat))(*flat)
+    p, size = _grad_ws(moe_clip_workspace_size(tensors), ws, device)
+    _run("moe_clip_grads", device, len(tensors),
+         ctypes.cast(arr, ctypes.POINTER(_lib.MoeTensor)), 0.0,
+         norm.data_ptr(), p, size)
+
+
 def _capturing(device: torch.device) -> bool:
     """Whether the device's current stream is being captured into a graph."""
     if device.type != "cuda":
