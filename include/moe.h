@@ -108,7 +108,10 @@ typedef enum {
 typedef enum {
     MOE_ACT_GELU = 0,    /* h = GELU(W1 x + b1), exact erf form */
     MOE_ACT_SILU = 1,    /* h = SiLU(W1 x + b1), SiLU(z) = z / (1 + e^-z) */
-    MOE_ACT_SWIGLU = 2   /* h = SiLU(W1 x + b1) * (W3 x + b3) */
+    MOE_ACT_SWIGLU = 2,  /* h = SiLU(W1 x + b1) * (W3 x + b3) */
+    MOE_ACT_NONE = 3,    /* h = W1 x + b1 (moe_linear) */
+    MOE_ACT_GEGLU = 4    /* h = GELU(W1 x + b1) * (W3 x + b3) (moe_linear,
+                            moe_dense_*) */
 } moe_activation;
 
 /* Layer shape, host struct passed by pointer.
@@ -134,7 +137,7 @@ typedef enum {
  *             Mixtral layer ("MoE inference with vLLM"; "AI-Research-
  *             SKILLs MoE training guide", sec. 9); its target is the
  *             weight-streaming decode shape, whose bytes it halves.
- *   activation a moe_activation (applies to routed and shared experts);
+ *   activation MOE_ACT_GELU, _SILU or _SWIGLU (routed and shared experts);
  *             MOE_ACT_SWIGLU needs d_ff a multiple of 128 for bf16 */
 typedef struct moe_desc {
     int32_t T, d, E, k, d_ff;
@@ -463,6 +466,93 @@ size_t moe_clip_workspace_size(int32_t n);
  * and types, n == 0 included (norm 0). */
 int moe_clip_grads(int32_t n, const moe_tensor *tensors, float max_norm,
                    float *norm, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------
+ * Dense layers beside the sparse one: linear layers with an epilogue, the
+ * feed-forward block of a model's layers that are not sparse, and their
+ * gradients.  Row-major and contiguous as above; x, weights, outputs and
+ * gradients are all of the descriptor's dtype and start at 16-byte
+ * boundaries, workspaces too.  Outputs overlap neither inputs, the
+ * workspace nor each other (refused where one starts where another does).
+ * Written without atomics: the same inputs give the same bits.  Sums are
+ * fp32, and a result is rounded to dtype once.
+ * ------------------------------------------------------------------ */
+
+/* M rows (0 <= M <= 2^22) of K features to N features; N and K multiples of
+ * 64, at most 2^20; any moe_activation, gated for MOE_ACT_SWIGLU and _GEGLU. */
+typedef struct moe_linear_desc {
+    int32_t M, N, K;
+    int32_t dtype;
+    int32_t activation;
+} moe_linear_desc;
+
+/* w [N][K] (required), b [N]; gated: w3 [N][K] (required then), b3 [N]. */
+typedef struct moe_linear_weights {
+    const void *w, *b, *w3, *b3;
+} moe_linear_weights;
+
+/* Of x's and the weights' shapes, written whole; NULL = not wanted.  w3, b3
+ * of a layer that is not gated get zeros. */
+typedef struct moe_linear_grads {
+    void *x, *w, *b, *w3, *b3;
+} moe_linear_grads;
+
+/* Host.  Workspace bytes, functions of the descriptor alone (0 if it is
+ * invalid); nothing is held between calls. */
+size_t moe_linear_workspace_size(const moe_linear_desc *desc);
+size_t moe_linear_grad_workspace_size(const moe_linear_desc *desc);
+
+/* y = residual + act(x w^T + b), gated: residual + a(x w^T + b) *
+ * (x w3^T + b3) with a SiLU or GELU, in one kernel.  x [M][K], y and residual
+ * (NULL = 0) [M][N]. */
+int moe_linear(const moe_linear_desc *desc, const void *x,
+               const moe_linear_weights *w, const void *residual, void *y,
+               void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients of sum(dy * y) for dy [M][N], from the forward's x and weights
+ * alone: the pre-activations are computed again.  g->x gets dx_add (NULL = 0)
+ * as well.  (The residual's gradient is dy.)  Pre-activations' gradients are
+ * rounded to dtype before the products.  M == 0: the weights' are zeroed. */
+int moe_linear_grad(const moe_linear_desc *desc, const void *x,
+                    const moe_linear_weights *w, const void *dy,
+                    const void *dx_add, const moe_linear_grads *g, void *ws,
+                    size_t ws_bytes, void *stream);
+
+/* The feed-forward block: T tokens (0 <= T <= 2^22), width d, hidden width
+ * d_ff, both multiples of 64 and at most 2^20; an activation that is not
+ * MOE_ACT_NONE. */
+typedef struct moe_dense_desc {
+    int32_t T, d, d_ff;
+    int32_t dtype;
+    int32_t activation;
+} moe_dense_desc;
+
+/* w1 [d_ff][d], b1 [d_ff], w2 [d][d_ff], b2 [d]; gated: w3, b3 like w1, b1
+ * (biases may be NULL). */
+typedef struct moe_dense_weights {
+    const void *w1, *b1, *w2, *b2, *w3, *b3;
+} moe_dense_weights;
+typedef struct moe_dense_grads {
+    void *x, *w1, *b1, *w2, *b2, *w3, *b3;
+} moe_dense_grads;
+
+size_t moe_dense_workspace_size(const moe_dense_desc *desc);
+size_t moe_dense_grad_workspace_size(const moe_dense_desc *desc);
+
+/* y = residual + W2 h + b2 with h = act(W1 x + b1), gated: a(W1 x + b1) *
+ * (W3 x + b3); h is rounded to dtype.  x, y, residual (NULL = 0) [T][d]. */
+int moe_dense_forward(const moe_dense_desc *desc, const void *x,
+                      const moe_dense_weights *w, const void *residual,
+                      void *y, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients of sum(dy * y); nothing of the forward is kept but x and the
+ * weights.  g->x gets dx_add (NULL = 0) as well: dy itself where x is the
+ * residual too.  h and the pre-activations' gradients are rounded to dtype
+ * between products, dy W2 is not.  T == 0: the weights' are zeroed. */
+int moe_dense_backward(const moe_dense_desc *desc, const void *x,
+                       const moe_dense_weights *w, const void *dy,
+                       const void *dx_add, const moe_dense_grads *g, void *ws,
+                       size_t ws_bytes, void *stream);
 
 /* One tensor of an AdamW step: numel elements, param (param_dtype) and
  * master updated in place, grad read.

@@ -5,8 +5,14 @@ The layer runs in hand-written HIP kernels behind the C ABI of
 include/moe.h (libmoe.so, built in-tree).  This package is the thin torch
 binding: torch supplies device memory and streams only.
 """
-from ._lib import (MoeError, MoeDesc, MoeGrads, MoeRouting,  # noqa: F401
-                   MoeTensor, MoeWeights, lib)
+from ._lib import (MoeDenseDesc, MoeDesc, MoeError, MoeGrads,  # noqa: F401
+                   MoeLinearDesc, MoeRouting, MoeTensor, MoeWeights, lib)
+from .dense import (DenseGrads, DenseLayer, DenseWeights,  # noqa: F401
+                    LinearGrads, LinearWeights, make_dense_desc,
+                    make_linear_desc, moe_dense_backward, moe_dense_forward,
+                    moe_dense_grad_workspace_size, moe_dense_workspace_size,
+                    moe_linear, moe_linear_grad,
+                    moe_linear_grad_workspace_size, moe_linear_workspace_size)
 from .layer import (Grads, MoeLayer, RouterWeights, Routing,  # noqa: F401
                     Weights, make_desc, moe_backward,
                     moe_bias_update, moe_capacity, moe_clip_grads,

@@ -30,6 +30,8 @@ MOE_ROUTE_EXPERT_CHOICE = 1
 MOE_ACT_GELU = 0
 MOE_ACT_SILU = 1
 MOE_ACT_SWIGLU = 2
+MOE_ACT_NONE = 3
+MOE_ACT_GEGLU = 4
 
 
 class MoeDesc(ctypes.Structure):
@@ -67,6 +69,35 @@ class MoeGrads(ctypes.Structure):
 class MoeTensor(ctypes.Structure):
     _fields_ = [("src", c_vp), ("dst", c_vp), ("numel", ctypes.c_int64),
                 ("dtype", c_i32)]
+
+
+class MoeLinearDesc(ctypes.Structure):
+    _fields_ = [("M", c_i32), ("N", c_i32), ("K", c_i32), ("dtype", c_i32),
+                ("activation", c_i32)]
+
+
+class MoeLinearWeights(ctypes.Structure):
+    _fields_ = [("w", c_vp), ("b", c_vp), ("w3", c_vp), ("b3", c_vp)]
+
+
+class MoeLinearGrads(ctypes.Structure):
+    _fields_ = [("x", c_vp), ("w", c_vp), ("b", c_vp), ("w3", c_vp),
+                ("b3", c_vp)]
+
+
+class MoeDenseDesc(ctypes.Structure):
+    _fields_ = [("T", c_i32), ("d", c_i32), ("d_ff", c_i32),
+                ("dtype", c_i32), ("activation", c_i32)]
+
+
+class MoeDenseWeights(ctypes.Structure):
+    _fields_ = [("w1", c_vp), ("b1", c_vp), ("w2", c_vp), ("b2", c_vp),
+                ("w3", c_vp), ("b3", c_vp)]
+
+
+class MoeDenseGrads(ctypes.Structure):
+    _fields_ = [("x", c_vp), ("w1", c_vp), ("b1", c_vp), ("w2", c_vp),
+                ("b2", c_vp), ("w3", c_vp), ("b3", c_vp)]
 
 
 class MoeAdamwTensor(ctypes.Structure):
@@ -160,6 +191,30 @@ SIGNATURES = {
     "moe_clip_grads": (ctypes.c_int, [c_i32, ctypes.POINTER(MoeTensor),
                                       ctypes.c_float, c_vp, c_vp,
                                       ctypes.c_size_t, c_vp]),
+    "moe_linear_workspace_size": (ctypes.c_size_t,
+                                  [ctypes.POINTER(MoeLinearDesc)]),
+    "moe_linear_grad_workspace_size": (ctypes.c_size_t,
+                                       [ctypes.POINTER(MoeLinearDesc)]),
+    "moe_linear": (ctypes.c_int, [ctypes.POINTER(MoeLinearDesc), c_vp,
+                                  ctypes.POINTER(MoeLinearWeights), c_vp,
+                                  c_vp, c_vp, ctypes.c_size_t, c_vp]),
+    "moe_linear_grad": (ctypes.c_int, [ctypes.POINTER(MoeLinearDesc), c_vp,
+                                       ctypes.POINTER(MoeLinearWeights), c_vp,
+                                       c_vp, ctypes.POINTER(MoeLinearGrads),
+                                       c_vp, ctypes.c_size_t, c_vp]),
+    "moe_dense_workspace_size": (ctypes.c_size_t,
+                                 [ctypes.POINTER(MoeDenseDesc)]),
+    "moe_dense_grad_workspace_size": (ctypes.c_size_t,
+                                      [ctypes.POINTER(MoeDenseDesc)]),
+    "moe_dense_forward": (ctypes.c_int, [ctypes.POINTER(MoeDenseDesc), c_vp,
+                                         ctypes.POINTER(MoeDenseWeights),
+                                         c_vp, c_vp, c_vp, ctypes.c_size_t,
+                                         c_vp]),
+    "moe_dense_backward": (ctypes.c_int, [ctypes.POINTER(MoeDenseDesc), c_vp,
+                                          ctypes.POINTER(MoeDenseWeights),
+                                          c_vp, c_vp,
+                                          ctypes.POINTER(MoeDenseGrads), c_vp,
+                                          ctypes.c_size_t, c_vp]),
     "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(MoeAdamw), c_i32,
                                       ctypes.POINTER(MoeAdamwTensor), c_vp]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -7,7 +7,6 @@ using namespace moe_host;
 
 namespace {
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
 int check_tensor(const moe_adamw *h, const moe_adamw_tensor &t) {
     if (t.numel < 0 || !(t.weight_decay >= 0.0) || t.weight_decay > 1e30)
@@ -23,8 +22,8 @@ int check_tensor(const moe_adamw *h, const moe_adamw_tensor &t) {
         (t.master && t.param_dtype != MOE_BF16))
         return MOE_ERR_INVALID_ARG;
     if ((uintptr_t)t.param % elem_bytes(t.param_dtype) ||
-        (uintptr_t)t.grad % elem_bytes(t.grad_dtype) || !aligned16(t.master) ||
-        !aligned16(t.m) || !aligned16(t.v))
+        (uintptr_t)t.grad % elem_bytes(t.grad_dtype) || !aligned(t.master) ||
+        !aligned(t.m) || !aligned(t.v))
         return MOE_ERR_INVALID_ARG;
     const void *own[] = {t.param, t.grad, t.m, t.v, t.master,
                          q8 ? t.m_scale : nullptr, q8 ? t.v_scale : nullptr,
@@ -88,7 +87,7 @@ extern "C" int moe_adamw_step(const moe_adamw *h, int32_t n,
             const moe_adamw_tensor &t = tensors[i];
             const long long own = (t.numel + MOE_ADAMW_CHUNK - 1) / MOE_ADAMW_CHUNK;
             if (chunks + own > 0x7fffffffll - most) break;
-            const bool ok = aligned16(t.param) && aligned16(t.grad);
+            const bool ok = aligned(t.param) && aligned(t.grad);
             const int flags = (t.param_dtype == MOE_F32 ? ADAMW_PARAM_F32 : 0) |
                               (t.grad_dtype == MOE_F32 ? ADAMW_GRAD_F32 : 0) |
                               (ok ? ADAMW_ALIGNED : 0);

@@ -197,7 +197,7 @@ struct GemmParams {
     int tail_split;
 };
 
-enum { ACT_GELU = 0, ACT_SILU = 1, ACT_SWIGLU = 2 };
+enum { ACT_GELU = 0, ACT_SILU = 1, ACT_SWIGLU = 2, ACT_NONE = 3, ACT_GEGLU = 4 };
 
 // SiLU(z) = z / (1 + e^-z) with the hardware exponential and reciprocal
 // (relative error a few 1e-7).

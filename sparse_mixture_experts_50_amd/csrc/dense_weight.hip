@@ -1,0 +1,147 @@
+// Weight gradients of the dense layer, bf16: out[R][C] = A^T B over M rows
+// (A [M][R], B [M][C]), up to three matrices in one launch, on the matrix
+// cores (tile product in mfma_tile.h; both operands are transposed on their
+// way from LDS).  The rows after the last whole stage of 64 come from a
+// buffer of 64 rows that is zero from M on, as a second product.
+// Few tiles: the rows go in ranges, each to an fp32 plane of its own.
+#include "dense_tile.h"
+
+namespace {
+
+using dn::bf16;
+
+struct WeightTile {
+    int k, mi, ni, split;
+};
+
+template <bool SMALL, bool PLANE>
+__global__ __launch_bounds__(256, SMALL ? 2 : 1) void dense_weight(DenseWeights p) {
+    constexpr int B = SMALL ? 128 : 256;
+    typedef mt::Tiles<B, B, 2, 2, 1, true, true, true> P;
+    constexpr int TN = P::TN, RB = B / 32;
+    constexpr bool TURN = !SMALL && !PLANE;
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], scr[TURN ? 4 * 32 * TN : 1];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / 2, wn = wave % 2;
+    const int stages = (p.M + mt::SK - 1) / mt::SK;
+    auto tiles = [&](int k) __attribute__((always_inline)) {
+        return (p.m[k].R + B - 1) / B * ((p.m[k].C + B - 1) / B);
+    };
+    int total = 0;
+    for (int k = 0; k < p.count; ++k) total += tiles(k) * p.splits;
+    auto tile_at = [&](int L) __attribute__((always_inline)) {
+        WeightTile t;
+        t.k = 0;
+        for (; t.k + 1 < p.count && L >= tiles(t.k) * p.splits; ++t.k) L -= tiles(t.k) * p.splits;
+        const dn::Tile at = dn::tile_at(L, (p.m[t.k].R + B - 1) / B, (p.m[t.k].C + B - 1) / B);
+        t.mi = at.mi;
+        t.ni = at.ni;
+        t.split = at.split;
+        return t;
+    };
+    auto source = [&](const WeightTile &t) __attribute__((always_inline)) {
+        const DenseMat &m = p.m[t.k];
+        const int m0 = mt::tile_start(t.mi, B, m.R), n0 = mt::tile_start(t.ni, B, m.C);
+        typename P::Source s;
+        s.a = (uint64_t)((const bf16 *)m.a + m0);
+        s.b = (uint64_t)((const bf16 *)m.b + n0);
+        s.a2 = (uint64_t)((const bf16 *)m.a2 + m0);
+        s.b2 = (uint64_t)((const bf16 *)m.b2 + n0);
+        s.s0 = t.split * p.per;
+        s.kt = min(p.per, stages - s.s0);
+        return s;
+    };
+    auto lanes = [&](const WeightTile &t, int lane) __attribute__((always_inline)) {
+        const int R = p.m[t.k].R, C = p.m[t.k].C;
+        typename P::Lanes ln;
+        ln.init(R * 2, min(R, B), C * 2, min(C, B), wave, lane);
+        ln.split = p.M / mt::SK;
+        return ln;
+    };
+    int L = mt::tile_of(0);
+    if (L >= total) return;
+    WeightTile t = tile_at(L);
+    typename P::Source src = source(t);
+    typename P::Lanes ln = lanes(t, threadIdx.x & 63);
+    P::load_stage(src, ln, 0, slot0, wave);
+    P::load_stage(src, ln, 1, slot1, wave);
+    mt::wait_loads<0>();
+    for (int r = 1;; ++r) {
+        const int lane = mt::tile_lane();
+        L = mt::tile_of(r);
+        const bool more = L < total;
+        const WeightTile tn = more ? tile_at(L) : t;
+        const typename P::Source next = source(tn);
+        const typename P::Lanes lnext = lanes(tn, lane);
+        const int R = p.m[t.k].R, C = p.m[t.k].C;
+        const int m0 = mt::tile_start(t.mi, B, R) + wm * RB * 16;
+        const int c0 = mt::tile_start(t.ni, B, C) + wn * TN * 16;
+        auto work = [&](auto kind) __attribute__((always_inline)) {
+            floatx4 acc[RB][TN];
+            mt::clear(acc);
+            // its first stages, ahead of the last tile's stores, have landed
+            mt::wait_loads<SMALL ? 0 : PLANE ? RB * TN : RB * TN / 2>();
+            P::template run<RB, RB, decltype(kind)::value>(acc, src, ln, next, lnext, slot0, slot1,
+                                                           wave, lane);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                const int mi = m0 + i * 16;
+                if (SMALL && (mi < t.mi * B || mi >= R)) continue;
+                if constexpr (PLANE) {
+                    float *out = p.plane + p.offset[t.k] + (size_t)t.split * R * C +
+                                 (size_t)(mi + (lane & 15)) * C + c0 + 4 * (lane >> 4);
+                    const int lo = t.ni * B - c0, hi = C - c0;
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+                        if (!SMALL || (16 * j >= lo && 16 * j < hi))
+                            *(floatx4 *)(out + 16 * j) = acc[i][j];
+                } else {
+                    float v[TN][4];
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[j][e] = acc[i][j][e];
+                    bf16 *row = (bf16 *)p.m[t.k].out + (size_t)mi * C + c0;
+                    if constexpr (SMALL) {
+                        dn::store_pieces<TN>(v, row + (size_t)(lane & 15) * C, t.ni * B - c0,
+                                             C - c0, lane);
+                    } else {
+                        mt::RowStore<TN> rows;
+                        rows.turn(scr, wave * 32 * TN, v, lane);
+                        rows.store(row, C, lane);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        if (src.kt & 1) work(std::integral_constant<mt::Stages, mt::ODD>{});
+        else work(std::integral_constant<mt::Stages, mt::EVEN>{});
+        if (!more) break;
+        t = tn;
+        src = next;
+        ln = lnext;
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+}
+
+template <bool SMALL, bool PLANE> void launch(const DenseWeights &p, hipStream_t s) {
+    constexpr int B = SMALL ? 128 : 256;
+    long long tiles = 0;
+    for (int k = 0; k < p.count; ++k)
+        tiles += (long long)((p.m[k].R + B - 1) / B) * ((p.m[k].C + B - 1) / B) * p.splits;
+    hipLaunchKernelGGL((dense_weight<SMALL, PLANE>), dim3(mt::grid_for(tiles, SMALL ? 2 : 1)),
+                       dim3(256), 0, s, p);
+}
+
+}  // namespace
+
+hipError_t launch_dense_weights_mfma(const DenseWeights &p, hipStream_t s) {
+    if (p.small) {
+        if (p.splits > 1) launch<true, true>(p, s);
+        else launch<true, false>(p, s);
+    } else {
+        if (p.splits > 1) launch<false, true>(p, s);
+        else launch<false, false>(p, s);
+    }
+    return hipGetLastError();
+}

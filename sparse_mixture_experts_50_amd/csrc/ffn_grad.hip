@@ -22,36 +22,11 @@
 // (256 tokens, 8 experts of 64 x 256) is bound by the latency of its 12
 // launches, 2 to 14 us each, one after the other (what depends on what is six
 // or seven deep).
+#include "act.h"
 #include "ffn_grad.h"
 #include "f32_tile.h"
 
 namespace {
-
-// h, dh/dz and dh/du at z, u, with the accurate library functions.
-template <int ACT>
-__device__ __forceinline__ void act_grad(float z, float u, float &h, float &hz,
-                                         float &hu) {
-    if (ACT == ACT_GELU) {
-        // z Phi(z), Phi + z phi
-        const float cdf = 0.5f * erfcf(z * -0.70710678f);
-        h = z * cdf;
-        hz = fmaf(z * 0.39894228f, expf(-0.5f * z * z), cdf);
-        hu = 0.0f;
-    } else {
-        const float sg = 1.0f / (1.0f + expf(-z));
-        const float a = z * sg;
-        const float da = fmaf(a, 1.0f - sg, sg);
-        if (ACT == ACT_SILU) {
-            h = a;
-            hz = da;
-            hu = 0.0f;
-        } else {
-            h = a * u;
-            hz = da * u;
-            hu = a;
-        }
-    }
-}
 
 // Block (g, c): the padding rows of group g, a c-th of their columns.  Every
 // block adds up the group sizes before its own by itself.
@@ -161,7 +136,7 @@ __global__ __launch_bounds__(256) void ffn_act_grad_f32(FfnGradParams p) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float h, hz, hu;
-                    act_grad<ACT>(z[i][j][e] + (b1 ? b1[c + e] : 0.0f),
+                    act_grad<ACT, false>(z[i][j][e] + (b1 ? b1[c + e] : 0.0f),
                                   u[i][j][e] + (b3 ? b3[c + e] : 0.0f), h, hz, hu);
                     dot = fmaf(q[i][j][e], h, dot);
                     const float wq = w * q[i][j][e];

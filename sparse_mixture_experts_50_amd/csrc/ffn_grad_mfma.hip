@@ -25,41 +25,13 @@
 // All three are persistent: one block per CU, whose tiles of a round lie
 // side by side in each XCD (consecutive tile numbers), where they share
 // operand panels through that XCD's L2.
+#include "act.h"
 #include "ffn_grad.h"
 #include "mfma_tile.h"
 
 namespace {
 
 typedef uint16_t bf16;
-
-// h, dh/dz and dh/du, with the fast forms of common.h: gelu_erf's erfc and
-// silu_f's exponential (relative errors of a few 1e-7).
-template <int ACT>
-__device__ __forceinline__ void act_grad(float z, float u, float &h, float &hz,
-                                         float &hu) {
-    hu = 0.0f;
-    if (ACT == ACT_GELU) {
-        h = gelu_erf(z);
-        // Phi + z phi; Phi = h / z loses nothing but its value at 0
-        const float pdf = 0.39894228f * __builtin_amdgcn_exp2f(z * z * -0.72134752f);
-        const float az = fabsf(z);
-        const float cdf = az > 1e-3f ? h * __builtin_amdgcn_rcpf(z)
-                                     : fmaf(0.39894228f, z, 0.5f);
-        hz = fmaf(z, pdf, cdf);
-    } else {
-        const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-z));
-        const float a = z * sg;
-        const float da = fmaf(a, 1.0f - sg, sg);
-        if (ACT == ACT_SILU) {
-            h = a;
-            hz = da;
-        } else {
-            h = a * u;
-            hz = da * u;
-            hu = a;
-        }
-    }
-}
 
 // Stores 16 rows of a wave's TN column blocks, columns lo..hi of them, as
 // bf16 and straight from the registers: exchanging every second row of 16
@@ -337,7 +309,7 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void ffn_act_grad(FfnGra
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float h, hz, hu;
-                        act_grad<ACT>(z[i][j][e],
+                        act_grad<ACT, true>(z[i][j][e],
                                       PANELS > 1 ? z[i][j + TN * (PANELS - 1)][e] : 0.0f,
                                       h, hz, hu);
                         const float qq = q[i & 1][j][e];

@@ -1,7 +1,5 @@
 // Host side of the training entry points of include/moe.h: argument checks,
 // workspace layout and launches, as for the forward in moe_api.hip.
-#include <initializer_list>
-
 #include "../../include/moe.h"
 #include "grad.h"
 #include "host.h"
@@ -80,10 +78,6 @@ bool have_rows(const moe_desc *d) {
     return routed_rows(d) + (long long)d->n_shared * d->T > 0;
 }
 
-// Vectors of 16 bytes are moved: operands are aligned to them.
-template <typename... P> bool aligned(const P *...p) {
-    return ((((uintptr_t)p & 15) == 0) && ...);
-}
 bool aligned_weights(const moe_weights *w) {
     return aligned(w->w_router, w->w1, w->w2, w->w3, w->ws1, w->ws2, w->ws3, w->b1,
                    w->b2, w->b3, w->bs1, w->bs2, w->bs3);
@@ -91,19 +85,6 @@ bool aligned_weights(const moe_weights *w) {
 bool aligned_grads(const moe_grads *g) {
     return aligned(g->x, g->w_router, g->w1, g->w2, g->w3, g->ws1, g->ws2, g->ws3,
                    g->b1, g->b2, g->b3, g->bs1, g->bs2, g->bs3);
-}
-
-// Whether an output starts where an input or another output does.
-bool clash(std::initializer_list<const void *> outs,
-           std::initializer_list<const void *> ins) {
-    for (const void *const *o = outs.begin(); o != outs.end(); ++o) {
-        if (!*o) continue;
-        for (const void *i : ins)
-            if (*o == i) return true;
-        for (const void *const *q = outs.begin(); q != o; ++q)
-            if (*o == *q) return true;
-    }
-    return false;
 }
 
 // The gradient's kernels hold row offsets within a tile in 32 bits.

@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <initializer_list>
 
 #include "../../include/moe.h"
 #include "kernels.h"
@@ -84,6 +85,24 @@ inline int device_cus() {
         cached[dev].store(n, std::memory_order_relaxed);
     }
     return n;
+}
+
+// Vectors of 16 bytes are moved: operands are aligned to them.
+template <typename... P> inline bool aligned(const P *...p) {
+    return ((((uintptr_t)p & 15) == 0) && ...);
+}
+
+// Whether an output starts where an input or another output does.
+inline bool clash(std::initializer_list<const void *> outs,
+                  std::initializer_list<const void *> ins) {
+    for (const void *const *o = outs.begin(); o != outs.end(); ++o) {
+        if (!*o) continue;
+        for (const void *i : ins)
+            if (*o == i) return true;
+        for (const void *const *q = outs.begin(); q != o; ++q)
+            if (*o == *q) return true;
+    }
+    return false;
 }
 
 }  // namespace moe_host
