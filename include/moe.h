@@ -596,7 +596,7 @@ typedef struct moe_adamw {
     int64_t *steps;
     const float *lr_scale;
     const float *norm;
-    float max_norm;
+    double max_norm;
     int32_t state_bits;
     int32_t stochastic;
     uint32_t seed;

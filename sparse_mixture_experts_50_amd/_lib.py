@@ -113,7 +113,7 @@ class MoeAdamw(ctypes.Structure):
                 ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
                 ("step", ctypes.c_int64), ("steps", c_vp),
                 ("lr_scale", c_vp), ("norm", c_vp),
-                ("max_norm", ctypes.c_float), ("state_bits", c_i32),
+                ("max_norm", ctypes.c_double), ("state_bits", c_i32),
                 ("stochastic", c_i32), ("seed", ctypes.c_uint32)]
 
 

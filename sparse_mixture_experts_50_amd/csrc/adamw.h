@@ -37,7 +37,7 @@ struct AdamwParams {
     int64_t step;             // number of this step (without `steps`)
     const float *lr_scale;    // or null
     const float *norm;        // or null
-    float max_norm;
+    double max_norm;
     float b1, c1, b2, c2, eps;
     uint32_t seed;
     int32_t index0;           // index of the table's first tensor

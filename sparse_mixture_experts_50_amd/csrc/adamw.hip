@@ -176,7 +176,7 @@ __global__ __launch_bounds__(THREADS) void adamw(AdamwTable tab, AdamwParams p) 
     float f = 1.0f;
     if (p.norm) {
         // not fmin: a norm that is not a number has to reach the parameters
-        const double c = (double)p.max_norm / ((double)*p.norm + 1e-6);
+        const double c = p.max_norm / ((double)*p.norm + 1e-6);
         f = c >= 1.0 ? 1.0f : (float)c;
     }
     for (int c = blockIdx.x; c < tab.first[tab.count]; c += gridDim.x) {

@@ -45,7 +45,7 @@ extern "C" int moe_adamw_step(const moe_adamw *h, int32_t n,
     if (!(h->lr >= 0.0 && h->lr < 1e30) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
         !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps > 0.0 && h->eps < 1e30) ||
         (!h->steps && h->step < 1) ||
-        (h->norm && !(h->max_norm >= 0.0f && h->max_norm <= 3.4028234e38f)) ||
+        (h->norm && !(h->max_norm >= 0.0 && h->max_norm <= 1.7e308)) ||
         (h->stochastic != 0 && h->stochastic != 1) ||
         ((uintptr_t)h->steps & 7) || ((uintptr_t)h->lr_scale & 3) ||
         ((uintptr_t)h->norm & 3) ||

@@ -1,0 +1,399 @@
+"""The dense layer's and the optimizer's entry points on a host without a GPU:
+sizes, refusals and the binding's own checks, all before any HIP call; and
+the float64 references against differences."""
+import ctypes
+import itertools
+
+import pytest
+import torch
+
+import dense_bounds as ref
+import sparse_mixture_experts_50_amd as moe
+import sparse_mixture_experts_50_amd.dense as dense_module
+import sparse_mixture_experts_50_amd.optim as optim_module
+from sparse_mixture_experts_50_amd import _lib
+
+STEP = 1 << 40       # apart, and never dereferenced
+BF, F32 = torch.bfloat16, torch.float32
+INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -3
+
+
+def places(struct, first):
+    return {n: (first + i) * STEP for i, (n, _) in enumerate(struct._fields_)}
+
+
+LW, LG = places(_lib.MoeLinearWeights, 10), places(_lib.MoeLinearGrads, 20)
+DW, DG = places(_lib.MoeDenseWeights, 10), places(_lib.MoeDenseGrads, 20)
+
+
+def linear_desc(**kw):
+    base = dict(M=64, N=128, K=256, dtype=1, activation=2)
+    base.update(kw)
+    return _lib.MoeLinearDesc(**base)
+
+
+def dense_desc(**kw):
+    base = dict(T=64, d=128, d_ff=256, dtype=1, activation=2)
+    base.update(kw)
+    return _lib.MoeDenseDesc(**base)
+
+
+def linear(d, w=LW, x=STEP, res=None, y=2 * STEP, ws=3 * STEP, n=1 << 39):
+    return _lib.lib().moe_linear(
+        ctypes.byref(d), x, ctypes.byref(_lib.MoeLinearWeights(**w)), res, y,
+        ws, n, None)
+
+
+def linear_grad(d, w=LW, x=STEP, dy=2 * STEP, add=None, g=LG, ws=3 * STEP,
+                n=1 << 39):
+    return _lib.lib().moe_linear_grad(
+        ctypes.byref(d), x, ctypes.byref(_lib.MoeLinearWeights(**w)), dy, add,
+        ctypes.byref(_lib.MoeLinearGrads(**g)), ws, n, None)
+
+
+def dense(d, w=DW, x=STEP, res=None, y=2 * STEP, ws=3 * STEP, n=1 << 39):
+    return _lib.lib().moe_dense_forward(
+        ctypes.byref(d), x, ctypes.byref(_lib.MoeDenseWeights(**w)), res, y,
+        ws, n, None)
+
+
+def dense_grad(d, w=DW, x=STEP, dy=2 * STEP, add=None, g=DG, ws=3 * STEP,
+               n=1 << 39):
+    return _lib.lib().moe_dense_backward(
+        ctypes.byref(d), x, ctypes.byref(_lib.MoeDenseWeights(**w)), dy, add,
+        ctypes.byref(_lib.MoeDenseGrads(**g)), ws, n, None)
+
+
+BAD = [({0: -1}, INVALID), ({1: 0}, INVALID), ({1: 100}, UNSUPPORTED),
+       ({2: 32}, UNSUPPORTED), ({2: 1 << 21}, UNSUPPORTED),
+       ({0: (1 << 22) + 1}, UNSUPPORTED), ({3: 2}, UNSUPPORTED),
+       ({4: 5}, INVALID), ({4: -1}, INVALID)]
+
+
+@pytest.mark.parametrize("change,status", BAD)
+def test_descriptors_refused(change, status):
+    L = _lib.lib()
+    for make, calls, sizes in (
+            (linear_desc, (linear, linear_grad),
+             ("moe_linear_workspace_size", "moe_linear_grad_workspace_size")),
+            (dense_desc, (dense, dense_grad),
+             ("moe_dense_workspace_size", "moe_dense_grad_workspace_size"))):
+        d = make()
+        for i, v in change.items():
+            setattr(d, d._fields_[i][0], v)
+        for call in calls:
+            assert call(d) == status
+        for name in sizes:
+            assert getattr(L, name)(ctypes.byref(d)) == 0
+    assert dense(dense_desc(activation=_lib.MOE_ACT_NONE)) == INVALID
+
+
+def test_missing_and_misplaced_arguments():
+    L = _lib.lib()
+    d, e = linear_desc(), dense_desc()
+    for call, desc in ((linear, d), (linear_grad, d), (dense, e),
+                       (dense_grad, e)):
+        out = "y" if call in (linear, dense) else "dy"
+        assert call(desc, x=None) == INVALID
+        assert call(desc, x=STEP + 8) == INVALID
+        assert call(desc, **{out: None}) == INVALID
+        assert call(desc, **{out: 2 * STEP + 4}) == INVALID
+        assert call(desc, ws=None) == WORKSPACE
+        assert call(desc, ws=3 * STEP + 8) == WORKSPACE
+    for size, call, desc in (
+            (L.moe_linear_workspace_size, linear, d),
+            (L.moe_linear_grad_workspace_size, linear_grad, d),
+            (L.moe_dense_workspace_size, dense, e),
+            (L.moe_dense_grad_workspace_size, dense_grad, e)):
+        assert call(desc, n=size(ctypes.byref(desc)) - 1) == WORKSPACE
+    for name in ("w", "w3"):
+        assert linear(d, w={**LW, name: None}) == INVALID
+        assert linear_grad(d, w={**LW, name: None}) == INVALID
+    for name in ("w1", "w2", "w3"):
+        assert dense(e, w={**DW, name: None}) == INVALID
+        assert dense_grad(e, w={**DW, name: None}) == INVALID
+    for name in LW:
+        assert linear(d, w={**LW, name: LW[name] + 2}) == INVALID
+    for name in DG:
+        assert dense_grad(e, g={**DG, name: DG[name] + 2}) == INVALID
+    assert linear(d, res=5 * STEP + 2) == INVALID
+    assert linear_grad(d, add=5 * STEP + 2) == INVALID
+
+
+def test_outputs_over_inputs_or_each_other():
+    d, e = linear_desc(), dense_desc()
+    for v in (STEP, 3 * STEP, 5 * STEP, *LW.values()):
+        assert linear(d, y=v, res=5 * STEP) == INVALID
+    for v in (STEP, 3 * STEP, 5 * STEP, *DW.values()):
+        assert dense(e, y=v, res=5 * STEP) == INVALID
+    for call, desc, w, g in ((linear_grad, d, LW, LG),
+                             (dense_grad, e, DW, DG)):
+        for name in g:
+            for v in (STEP, 2 * STEP, 3 * STEP, 5 * STEP, *w.values()):
+                assert call(desc, add=5 * STEP, g={**g, name: v}) == INVALID
+        for a, b in itertools.combinations(g, 2):
+            assert call(desc, g={**g, a: g[b]}) == INVALID
+
+
+def test_no_rows_and_nothing_wanted():
+    """No rows: nothing is looked at; no gradient wanted: nothing to do."""
+    assert linear(linear_desc(M=0), x=None, y=None, ws=None) == 0
+    assert dense(dense_desc(T=0), x=None, y=None, ws=None) == 0
+    none = {n: None for n in LG}
+    assert linear_grad(linear_desc(M=0), x=None, dy=None, ws=None,
+                       g=none) == 0
+    assert linear_grad(linear_desc(), g=none) == 0
+    none = {n: None for n in DG}
+    assert dense_grad(dense_desc(T=0), x=None, dy=None, ws=None, g=none) == 0
+    assert dense_grad(dense_desc(), g=none) == 0
+
+
+# ------------------------------------------------------------- optimizer
+
+def adamw(t=None, n=1, **kw):
+    base = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, step=1, steps=None,
+                lr_scale=None, norm=None, max_norm=1.0, state_bits=32,
+                stochastic=0, seed=0)
+    base.update(kw)
+    arr = (_lib.MoeAdamwTensor * 1)(t if t is not None else tensor())
+    return _lib.lib().moe_adamw_step(
+        ctypes.byref(_lib.MoeAdamw(**base)), n, arr, None)
+
+
+def tensor(**kw):
+    base = dict(param=STEP, grad=2 * STEP, master=None, m=3 * STEP,
+                v=4 * STEP, m_scale=5 * STEP, v_scale=6 * STEP, numel=100,
+                weight_decay=0.1, param_dtype=1, grad_dtype=1)
+    base.update(kw)
+    return _lib.MoeAdamwTensor(**base)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(lr=-1.0), INVALID), (dict(lr=float("nan")), INVALID),
+    (dict(lr=float("inf")), INVALID), (dict(beta1=1.0), INVALID),
+    (dict(beta1=-0.1), INVALID), (dict(beta2=1.0), INVALID),
+    (dict(beta2=float("nan")), INVALID), (dict(eps=0.0), INVALID),
+    (dict(eps=float("inf")), INVALID), (dict(step=0), INVALID),
+    (dict(norm=7 * STEP, max_norm=-1.0), INVALID),
+    (dict(norm=7 * STEP, max_norm=float("nan")), INVALID),
+    (dict(norm=7 * STEP + 2), INVALID), (dict(steps=7 * STEP + 4), INVALID),
+    (dict(stochastic=2), INVALID), (dict(state_bits=16), UNSUPPORTED),
+    (dict(steps=STEP), INVALID), (dict(lr_scale=STEP), INVALID),
+    (dict(steps=8 * STEP, norm=8 * STEP), INVALID), (dict(n=-1), INVALID)])
+def test_step_refused(kw, status):
+    assert adamw(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(numel=-1), INVALID), (dict(numel=1 << 41), UNSUPPORTED),
+    (dict(param=None), INVALID), (dict(grad=None), INVALID),
+    (dict(m=None), INVALID), (dict(v=None), INVALID),
+    (dict(param=STEP + 1), INVALID), (dict(grad=2 * STEP + 1), INVALID),
+    (dict(m=3 * STEP + 8), INVALID), (dict(v=4 * STEP + 4), INVALID),
+    (dict(master=9 * STEP + 4), INVALID),
+    (dict(master=9 * STEP, param_dtype=0), INVALID),
+    (dict(param_dtype=2), UNSUPPORTED), (dict(grad_dtype=-1), UNSUPPORTED),
+    (dict(weight_decay=-0.1), INVALID),
+    (dict(weight_decay=float("nan")), INVALID),
+    (dict(grad=STEP), INVALID), (dict(v=3 * STEP), INVALID),
+    (dict(master=2 * STEP), INVALID)])
+def test_tensor_refused(kw, status):
+    assert adamw(tensor(**kw)) == status
+    assert adamw(tensor(**kw), state_bits=8) == status
+
+
+def test_scales_are_needed_for_8_bits_alone():
+    for name in ("m_scale", "v_scale"):
+        assert adamw(tensor(**{name: None}), state_bits=8) == INVALID
+        assert adamw(tensor(**{name: 3 * STEP}), state_bits=8) == INVALID
+
+
+def test_empty_steps():
+    assert adamw(n=0) == 0
+    assert adamw(tensor(numel=0, param=None, grad=None, m=None)) == 0
+
+
+def test_optimizer_checks():
+    p = [torch.zeros(4), torch.zeros(3, dtype=BF)]
+    with pytest.raises(ValueError):
+        moe.AdamW([], lr=1.0)
+    with pytest.raises(ValueError):
+        moe.AdamW(p, lr=1.0, state_bits=16)
+    with pytest.raises(ValueError):
+        moe.AdamW([p[0], p[0]], lr=1.0)
+    with pytest.raises(ValueError):
+        moe.AdamW([torch.zeros(4, dtype=torch.float16)], lr=1.0)
+    with pytest.raises(ValueError):
+        moe.AdamW([torch.zeros(4, 4).t()], lr=1.0)
+    with pytest.raises(ValueError):
+        moe.AdamW(p, lr=1.0, weight_decay=[0.1])
+    opt = moe.AdamW(p, lr=1.0, state_bits=8, master=True)
+    assert opt.master[0] is None and opt.master[1].dtype == F32
+    assert opt.m[1].dtype == torch.float8_e4m3fn and opt.m[1].shape == (3,)
+    assert opt.v_scale[0].shape == (1,) and opt.steps == 0
+    for grads in ([p[0]], [torch.zeros(5), p[1]],
+                  [torch.zeros(4, dtype=torch.float16), p[1]],
+                  [torch.zeros(8)[::2], p[1]]):
+        with pytest.raises(ValueError):
+            opt.step(grads)
+    with pytest.raises(ValueError):
+        opt.step(p, norm=torch.zeros(2))
+    with pytest.raises(ValueError):
+        opt.steps = -1
+    opt.params[0].data = torch.zeros(4)
+    with pytest.raises(ValueError):
+        opt.step([torch.zeros(4), torch.zeros(3)])
+    assert opt.steps == 0
+
+
+def test_captured_steps_are_counted_on_the_gpu(monkeypatch):
+    opt = moe.AdamW([torch.zeros(4)], lr=1.0)
+    monkeypatch.setattr(optim_module, "_capturing", lambda device: True)
+    with pytest.raises(ValueError, match="device_steps"):
+        opt.step([torch.zeros(4)])
+
+
+# --------------------------------------------------------------- binding
+
+def test_linear_binding_checks():
+    z = torch.zeros
+    w = moe.LinearWeights(z(64, 128), b=z(64))
+    d = moe.make_linear_desc(3, 64, 128, F32)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    for kw in (dict(x=z(4, 128)), dict(y=z(3, 128)), dict(x=z(3, 128).to(BF)),
+               dict(x=z(128, 3).t()), dict(residual=z(64)),
+               dict(ws=ws[:10]), dict(ws=ws[::2])):
+        args = {**dict(x=z(3, 128), y=z(3, 64), ws=ws, residual=None), **kw}
+        with pytest.raises(ValueError):
+            moe.moe_linear(d, args["x"], w, args["y"], args["ws"],
+                           residual=args["residual"])
+    with pytest.raises(ValueError):
+        moe.moe_linear(moe.make_linear_desc(3, 64, 128, F32, "swiglu"),
+                       z(3, 128), w, z(3, 64), ws)
+    with pytest.raises(ValueError):
+        moe.LinearWeights(z(64, 128), b3=z(64))
+    with pytest.raises(ValueError):
+        moe.LinearWeights(z(64, 128), b=z(63))
+    with pytest.raises(ValueError):
+        moe.LinearWeights(z(64, 128, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        moe.make_linear_desc(3, 64, 128, torch.float16)
+    with pytest.raises(ValueError):
+        moe.make_linear_desc(3, 64, 128, F32, "relu")
+    with pytest.raises(ValueError):
+        moe.LinearGrads(d, "cpu", ["w1"])
+    with pytest.raises(ValueError):
+        moe.LinearGrads(d, "cpu", w=z(64, 64))
+    with pytest.raises(moe.MoeError):
+        moe.moe_linear_workspace_size(moe.make_linear_desc(3, 65, 128, F32))
+    g = moe.LinearGrads(d, "cpu", ["x", "w"])
+    assert set(g.as_dict()) == {"x", "w"}
+    with pytest.raises(ValueError):
+        moe.moe_linear_grad(d, z(3, 128), w, z(3, 64), g, ws[:100])
+    with pytest.raises(ValueError):
+        moe.moe_linear_grad(d, z(3, 128), w, z(3, 128), g, ws)
+
+
+def test_block_binding_checks():
+    z = torch.zeros
+    w = moe.DenseWeights(z(128, 64), z(64, 128))
+    for act in ("none", "swiglu", "geglu", "relu"):
+        with pytest.raises(ValueError):
+            moe.DenseLayer(w, act)
+    gated = moe.DenseWeights(z(128, 64), z(64, 128), w3=z(128, 64))
+    with pytest.raises(ValueError):
+        moe.DenseLayer(gated, "gelu")
+    assert moe.DenseLayer(gated).activation == "swiglu"
+    assert moe.DenseLayer(w).activation == "gelu"
+    with pytest.raises(ValueError):
+        moe.DenseWeights(z(128, 64), z(128, 64))
+    layer = moe.DenseLayer(w)
+    with pytest.raises(ValueError):
+        layer.forward(z(3, 128))
+    with pytest.raises(ValueError):
+        layer.forward(z(3, 64), residual=z(4, 64))
+    with pytest.raises(ValueError):
+        layer.backward(z(3, 64), z(4, 64))
+
+
+def test_workspace_does_not_grow_with_the_token_counts_seen(monkeypatch):
+    """One workspace for every token count and direction, as large as the
+    largest call needs (and the growth's quarter); captured calls keep
+    theirs."""
+    z = torch.zeros
+    layer = moe.DenseLayer(moe.DenseWeights(z(128, 64), z(64, 128)))
+    monkeypatch.setattr(dense_module, "_capturing", lambda device: True)
+    first = layer._plan(40, True)
+    monkeypatch.undo()
+    most = 0
+    for T in (5, 300, 301, 1, 2000, 700):
+        for back in (False, True):
+            desc, ws = layer._plan(T, back)
+            need = (moe.moe_dense_grad_workspace_size if back else
+                    moe.moe_dense_workspace_size)(desc)
+            assert desc.T == T and ws.numel() >= need
+            most = max(most, need)
+    assert layer._plan(40, True) is first
+    assert layer._ws.numel() <= 1.25 * most
+    held = {p[1].data_ptr() for p in layer._plans.values()}
+    assert held <= {first[1].data_ptr(), layer._ws.data_ptr()}
+
+
+# ------------------------------------------------------------ references
+
+@pytest.mark.parametrize("act", ["gelu", "silu", "swiglu", "geglu"])
+def test_reference_against_differences(act):
+    """The float64 gradients against central differences (error of the order
+    of h^2 and of rounding / h)."""
+    g = torch.Generator().manual_seed(1)
+    T, d, F, h = 3, 4, 5, 1e-5
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, dtype=torch.float64)
+
+    gated = act in ref.GATED
+    t = [normal(T, d), normal(F, d), normal(d, F),
+         normal(F, d) if gated else None, normal(F), normal(d),
+         normal(F) if gated else None]
+    dy = normal(T, d)
+    grads = ref.dense_grad(act, 0.0, *t, dy, None)
+    lin = ref.linear_grad(act, 0.0, t[0], t[1], t[4], t[3], t[6],
+                          dy @ t[2], None)
+    for i, name in enumerate(("x", "w1", "w2", "w3", "b1", "b2", "b3")):
+        if t[i] is None:
+            continue
+        want = torch.zeros_like(t[i])
+        for j in range(t[i].numel()):
+            sums = []
+            for s in (h, -h):
+                t[i].view(-1)[j] += s
+                sums.append(float((dy * ref.dense(act, 0.0, *t,
+                                                  None)[0]).sum()))
+                t[i].view(-1)[j] -= s
+            want.view(-1)[j] = (sums[0] - sums[1]) / (2 * h)
+        assert (grads[name][0] - want).abs().max() < 1e-7, name
+        # the block's first layer is a linear layer with this dy
+        short = {"x": "x", "w1": "w", "w3": "w3", "b1": "b", "b3": "b3"}
+        if name in short:
+            assert (lin[short[name]][0] - want).abs().max() < 1e-7, name
+
+
+def test_bounds_catch_mistakes():
+    """A row, a column block or a bias left out, planted in the values that
+    are checked."""
+    g = torch.Generator().manual_seed(2)
+    x, w = (torch.randn(s, generator=g, dtype=torch.float64)
+            for s in ((40, 64), (64, 64)))
+    b = torch.randn(64, generator=g, dtype=torch.float64)
+    want = ref.linear("gelu", 2.0 ** -8, x, w / 8, b, None, None, None)
+    ref.check(want[0].to(BF), want, 2.0 ** -8, 1, "y")
+    for change in ("row", "columns", "bias"):
+        y = want[0].clone()
+        if change == "row":
+            y[39] = y[38]
+        elif change == "columns":
+            y[:, 48:] = 0
+        else:
+            y = ref.linear("gelu", 0.0, x, w / 8, None, None, None, None)[0]
+        with pytest.raises(AssertionError):
+            ref.check(y.to(BF), want, 2.0 ** -8, 1, change)
