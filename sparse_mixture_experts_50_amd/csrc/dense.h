@@ -17,11 +17,11 @@ enum DenseEpilogue {
 };
 
 // How a product is cut: tiles of 32 * rb rows (small: 64) by 256 (small: 128)
-// columns, K in `splits` ranges of `per` stages.
+// columns, K in `splits` ranges of `per` stages.  stream: the kernel for few
+// rows, which cuts by itself.
 struct DensePlan {
     bool small, stream;
     int rb, mt, nt, splits, per;
-    int nb, waves;            // stream: see dense_stream.hip
 };
 
 // out[M][N] = A B over K: A [M][K]; B [N][K] (transposed product), or [K][N]

@@ -60,9 +60,6 @@ DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, b
     p.splits = 1;
     if (M <= 64 && !bk) {
         p.stream = true;
-        const int mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-        p.nb = 1;
-        while (p.nb < 4 && 2 * p.nb * mb * panels <= 8 && N / (16 * 2 * p.nb) >= 2 * CUS) p.nb *= 2;
         return p;
     }
     const int stages = K / 64;
