@@ -112,6 +112,7 @@ __global__ __launch_bounds__(256) void dense_finish(DenseRows p) {
     Vec<T> z, u, a, o;
     z.clear();
     u.clear();
+#pragma unroll 4
     for (int s = 0; s < p.plan.splits; ++s) {
         const float *q = p.plane + (size_t)s * PANELS * plane + at;
         z.add(q);
@@ -166,6 +167,7 @@ template <typename T> __global__ __launch_bounds__(256) void dense_weight_finish
     if (at >= size) return;
     Vec<T> s;
     s.clear();
+#pragma unroll 4
     for (int i = 0; i < p.splits; ++i) s.add(p.plane + p.offset[blockIdx.y] + i * size + at);
     s.store((T *)m.out + at);
 }

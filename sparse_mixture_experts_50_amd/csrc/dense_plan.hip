@@ -9,22 +9,25 @@ constexpr int CUS = 256;
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-// Time estimates in us.  Each tile of a round runs beside the others.
+// Time estimates in us, fitted to kernel times: stage[o - 1] is one 64-deep
+// stage of a tile while o tiles share a CU, tile a tile's start and epilogue.
 struct Cost {
-    double stage;             // one 64-deep stage of a tile
-    double tile;              // start and epilogue
-    int places;               // tiles at a time
+    int occupancy;
+    double stage[4], tile;
 };
-
+// Tiles in rounds of all CUs' places; the last one's share what they find.
 double product_us(const Cost &c, long long units, int per) {
-    return ceil_div(units, c.places) * (c.tile + per * c.stage);
+    const long long places = (long long)CUS * c.occupancy, rounds = units / places;
+    const int rest = ceil_div(units - rounds * places, CUS);
+    return 2.5 + rounds * (c.stage[c.occupancy - 1] * per + c.tile) +
+           (rest ? c.stage[rest - 1] * per + c.tile : 0.0);
 }
 // Planes of fp32 sums, written and read, and the launch that joins them.
 double plane_us(double elements, int splits) {
-    return splits > 1 ? 4.0 + elements * splits * 8.0 / 4e6 : 0.0;
+    return splits > 1 ? 6.0 + elements * splits * 8.0 / 7e6 : 0.0;
 }
 
-// The best number of ranges of `stages`, at least four stages each; even: of
+// The best number of ranges of `stages`, at least two stages each; even: of
 // an even number of stages.
 template <typename F>
 int best_splits(int stages, int most, bool even, double &us, int &per, F cost) {
@@ -32,7 +35,7 @@ int best_splits(int stages, int most, bool even, double &us, int &per, F cost) {
     for (int s = 1; s <= most; ++s) {
         int len = ceil_div(stages, s);
         if (s > 1 && even) len = (len + 1) & ~1;
-        if (s > 1 && (len < 4 || (even && (stages & 1)) || (s - 1) * (long long)len >= stages))
+        if (s > 1 && (len < 2 || (even && (stages & 1)) || (s - 1) * (long long)len >= stages))
             continue;
         const double t = cost(s, len);
         if (best == 0 || t < us) {
@@ -63,16 +66,31 @@ DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, b
         return p;
     }
     const int stages = K / 64;
+    const double elements = (double)M * N * panels;
     if (dtype != 1) {
         p.small = true;
         p.mt = ceil_div(M, 64);
-        p.nt = N / 64;
-        const long long tiles = (long long)p.mt * p.nt;
-        const Cost c = {3.0 * panels * (two ? 2 : 1), 4.0, 4 * CUS};
+        p.nt = ceil_div(N, 64 / panels);
+        // (2048 x 2048 x 2048: 1024 tiles 155 us; 1021 x 1984 x 1024: 496
+        // tiles 46; 512 x 1024 x 2048: 128 tiles 56)
+        const int n = two ? 2 : 1;
+        const Cost c = {4, {1.7 * n, 2.65 * n, 4.0 * n, 4.7 * n}, 2.0};
         double us = 0;
         p.splits = best_splits(stages, 16, false, us, p.per, [&](int s, int len) {
-            return product_us(c, tiles * s, len) + plane_us((double)M * N * panels, s);
+            return product_us(c, (long long)p.mt * p.nt * s, len) + plane_us(elements, s);
         });
+        if (two || N < 128 / panels) return p;
+        // (4096 x 4096 x 4096: 1074 us, with the small tiles 1199; 2048 x
+        // 2048 x 2048 151; 1021 x 1984 x 1024 77)
+        const Cost b = {2, {4.65, 8.3}, 3.0};
+        const int mt = ceil_div(M, 128), nt = ceil_div(N, 128 / panels);
+        if (product_us(b, (long long)mt * nt, stages) < us) {
+            p.small = false;
+            p.mt = mt;
+            p.nt = nt;
+            p.splits = 1;
+            p.per = stages;
+        }
         return p;
     }
     const int all = two ? 2 * stages : stages;
@@ -82,9 +100,10 @@ DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, b
     a.mt = ceil_div(M, 64);
     a.nt = ceil_div(N, 128 / panels);
     double us = 0;
-    const double elements = (double)M * N * panels;
     {
-        const Cost c = {0.9, 3.0, 2 * CUS};
+        // (512 x 4096 x 4096: 256 tiles 25 us; 1024 x 4096 x 4096: 512 41;
+        // 2048 x 8192 x 1024: 2048 45)
+        const Cost c = {2, {0.3, 0.57}, 2.0};
         const long long tiles = (long long)a.mt * a.nt;
         a.splits = best_splits(all, 16, false, us, a.per, [&](int s, int len) {
             return product_us(c, tiles * s, len) + plane_us(elements, s);
@@ -97,9 +116,13 @@ DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, b
     b.nt = ceil_div(N, 256 / panels);
     double big = 0;
     {
-        const Cost c = {0.6 + 1.4 * b.rb / 8, 6.0, CUS};
+        // (8192 x 7168 x 2048: 896 tiles 185 us; 2048 x 8192 x 1024: 256 31;
+        // with half of the CUs at work the clock is higher: 2048 x 4096 x
+        // 4096: 128 tiles 73.  With the small tiles 275, 45 and 75.)
         const long long tiles = (long long)b.mt * b.nt;
         b.splits = best_splits(all, 16, true, big, b.per, [&](int s, int len) {
+            const double rate = tiles * s <= CUS / 2 ? 1.08 : 1.4;
+            const Cost c = {1, {rate * (0.3 + 0.7 * b.rb / 8)}, 6.0};
             return product_us(c, tiles * s, len) + plane_us(elements, s);
         });
     }
@@ -114,11 +137,12 @@ size_t dense_weights_plan(DenseWeights &p, int dtype) {
         elements += (double)p.m[k].R * p.m[k].C;
         big = big && p.m[k].R >= 256 && p.m[k].C >= 256;
     }
-    auto cut = [&](int tile, const Cost &c, double &us, int &per) {
+    auto cut = [&](int tile, Cost c, double &us, int &per) {
         long long tiles = 0;
         for (int k = 0; k < p.count; ++k)
             tiles += (long long)ceil_div(p.m[k].R, tile) * ceil_div(p.m[k].C, tile);
         return best_splits(stages, 16, false, us, per, [&](int s, int len) {
+            if (tile == 256) c.stage[0] = tiles * s <= CUS / 2 ? 1.08 : 1.45;
             return product_us(c, tiles * s, len) + plane_us(elements, s);
         });
     };
@@ -126,13 +150,15 @@ size_t dense_weights_plan(DenseWeights &p, int dtype) {
     int per = 0, per_big = 0;
     if (dtype != 1) {
         p.small = true;
-        p.splits = cut(64, Cost{3.0, 4.0, 4 * CUS}, us, p.per);
+        p.splits = cut(64, Cost{4, {1.7, 2.65, 4.0, 4.7}, 2.0}, us, p.per);
     } else {
         p.small = true;
-        p.splits = cut(128, Cost{1.5, 4.0, 2 * CUS}, us, per);
+        // (4096 rows, 1024 x 1024: 64 tiles 43 us, in four ranges 23; 2048 x
+        // 2048: 256 tiles 52; 4096 x 4096: 1024 137 us, the large tiles 98)
+        p.splits = cut(128, Cost{2, {0.7, 1.05}, 2.5}, us, per);
         p.per = per;
         if (big) {
-            const int s = cut(256, Cost{2.0, 8.0, CUS}, us_big, per_big);
+            const int s = cut(256, Cost{1, {1.45}, 6.0}, us_big, per_big);
             if (us_big <= us) {
                 p.small = false;
                 p.splits = s;
