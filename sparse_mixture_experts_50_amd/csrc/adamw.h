@@ -8,7 +8,9 @@
 
 // Elements of an 8-bit state that share a scale.
 #define MOE_ADAMW_BLOCK 32
-// Elements of the unit of work that tensors are dealt out in.
+// Elements of the unit of work that tensors are dealt out in: multiples of the
+// least, at most the other.
+#define MOE_ADAMW_LEAST 2048
 #define MOE_ADAMW_CHUNK 16384
 // Tensors of one launch (the table travels as a kernel argument).
 #define MOE_ADAMW_TENSORS 40
@@ -41,6 +43,7 @@ struct AdamwParams {
     float b1, c1, b2, c2, eps;
     uint32_t seed;
     int32_t index0;           // index of the table's first tensor
+    int32_t chunk;
     int32_t stochastic;       // bf16 parameters without a master copy
 };
 hipError_t launch_adamw(const AdamwTable &tab, const AdamwParams &p, int bits,

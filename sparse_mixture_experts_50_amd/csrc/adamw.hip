@@ -25,8 +25,9 @@
 // that plain elementary operations reproduce bit for bit.
 //
 // Bound by HBM: every operand is read and written once, by 32 KB and more of
-// loads in flight per CU; chunks of 16384 elements of all tensors are dealt
-// round-robin to the blocks, as the clipping's are.
+// loads in flight per CU; chunks of 16384 elements of all tensors (fewer where
+// that leaves blocks without work) are dealt round-robin to the blocks, as the
+// clipping's are.
 #include "adamw.h"
 
 namespace {
@@ -109,9 +110,19 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));
 }
 
-// The lane's 8 codes of 32 as fp32.
-__device__ __forceinline__ void decode(float (&x)[8], u32x2 code, uint32_t scale) {
-    const float s = __uint_as_float(scale << 23);
+// Correctly rounded root of v >= 0 (from 2^-96 on; below, off by 2^-24 of it at
+// most): the hardware's, off by one place at most, moved to a neighbour where
+// the residual says so.  0, infinity and NaN fail both comparisons.
+__device__ __forceinline__ float root_of(float v) {
+    const float s = __builtin_amdgcn_sqrtf(v);
+    const float under = __uint_as_float(__float_as_uint(s) - 1);
+    const float over = __uint_as_float(__float_as_uint(s) + 1);
+    float r = fmaf(-under, s, v) <= 0.0f ? under : s;
+    return fmaf(-over, s, v) > 0.0f ? over : r;
+}
+
+// The lane's 8 codes times s as fp32.
+__device__ __forceinline__ void decode(float (&x)[8], u32x2 code, float s) {
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(code[w], false);
@@ -124,8 +135,10 @@ __device__ __forceinline__ void decode(float (&x)[8], u32x2 code, uint32_t scale
 }
 
 // The 8 codes of a lane's values, in a block of 4 lanes; scale: exponent + 127
-// of the block's power of two.  rnd: 16 random bits of each.  A block with a
-// value that is not finite is not-a-number throughout.
+// of the block's power of two.  16 bits of rnd make the rounding (ROOT: the
+// upper ones), as the top ones of the 20 that the conversion adds to the bits
+// it drops (checked against that definition over values and bits).  A block
+// with a value that is not finite is not-a-number throughout.
 template <bool ROOT>
 __device__ __forceinline__ u32x2 encode(const float (&x)[8], const uint32_t (&rnd)[8],
                                         uint32_t &scale) {
@@ -139,22 +152,25 @@ __device__ __forceinline__ u32x2 encode(const float (&x)[8], const uint32_t (&rn
     const bool finite = top < 0x7F800000u;
     if (!finite) e = 127;
     scale = (uint32_t)e;
+    const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+    auto value = [&](int i) __attribute__((always_inline)) {
+        const float y = x[i] * inv;
+        // 2^-9: the least code that is not 0
+        return ROOT ? fmaxf(y, x[i] > 0.0f ? 0.001953125f : 0.0f) : y;
+    };
+    auto seed = [&](int i) __attribute__((always_inline)) {
+        return ROOT ? rnd[i] & 0xFFFF0000u : rnd[i] << 16;
+    };
     u32x2 out;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-        uint32_t word = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const float v = x[4 * w + b];
-            // e4m3's smallest normal number to fp32's, 2^20 units a step
-            const float y = __builtin_amdgcn_ldexpf(fabsf(v), 7 - e);
-            uint32_t c = (__float_as_uint(y) + (rnd[4 * w + b] << 4)) >> 20;
-            c = min(c, 0x7Eu);
-            if (ROOT) c = v > 0.0f ? max(c, 1u) : c;
-            else c |= (__float_as_uint(v) >> 24) & (v != 0.0f ? 0x80u : 0u);
-            word |= c << (8 * b);
-        }
-        out[w] = finite ? word : 0x7F7F7F7Fu;
+        const int i = 4 * w;
+        int word = 0;
+        word = __builtin_amdgcn_cvt_sr_fp8_f32(value(i), seed(i), word, 0);
+        word = __builtin_amdgcn_cvt_sr_fp8_f32(value(i + 1), seed(i + 1), word, 1);
+        word = __builtin_amdgcn_cvt_sr_fp8_f32(value(i + 2), seed(i + 2), word, 2);
+        word = __builtin_amdgcn_cvt_sr_fp8_f32(value(i + 3), seed(i + 3), word, 3);
+        out[w] = finite ? (uint32_t)word : 0x7F7F7F7Fu;
     }
     return out;
 }
@@ -179,6 +195,7 @@ __global__ __launch_bounds__(THREADS) void adamw(AdamwTable tab, AdamwParams p) 
         const double c = p.max_norm / ((double)*p.norm + 1e-6);
         f = c >= 1.0 ? 1.0f : (float)c;
     }
+    const int chunk = p.chunk;
     for (int c = blockIdx.x; c < tab.first[tab.count]; c += gridDim.x) {
         int lo = 0, hi = tab.count;
         while (hi - lo > 1) {
@@ -193,8 +210,8 @@ __global__ __launch_bounds__(THREADS) void adamw(AdamwTable tab, AdamwParams p) 
         const uint32_t key = p.seed * 0x9E3779B1u + step * 0x85EBCA77u +
                              (uint32_t)(p.index0 + lo) * 0xC2B2AE3Du;
         const bool any = p.stochastic && !pf32 && !t.master;
-        const long long start = (long long)(c - tab.first[lo]) * MOE_ADAMW_CHUNK;
-        const long long end = min(start + MOE_ADAMW_CHUNK, n);
+        const long long start = (long long)(c - tab.first[lo]) * chunk;
+        const long long end = min(start + chunk, n);
         // (whole blocks of 4 lanes go round together)
         for (long long b0 = start; b0 < end; b0 += THREADS * V) {
             const long long e0 = b0 + (long long)threadIdx.x * V;
@@ -220,8 +237,9 @@ __global__ __launch_bounds__(THREADS) void adamw(AdamwTable tab, AdamwParams p) 
                     ms = t.m_scale[e0 / MOE_ADAMW_BLOCK];
                     vs = t.v_scale[e0 / MOE_ADAMW_BLOCK];
                 }
-                decode(m, mc, ms);
-                decode(v, vc, vs);
+                // (a power of two: the products with b1 are rounded alike)
+                decode(m, mc, __uint_as_float(ms << 23) * p.b1);
+                decode(v, vc, __uint_as_float(vs << 23));
             } else {
                 load(m, t.m, true, e0, n, whole);
                 load(v, t.v, true, e0, n, whole);
@@ -231,30 +249,32 @@ __global__ __launch_bounds__(THREADS) void adamw(AdamwTable tab, AdamwParams p) 
             for (int i = 0; i < V; ++i) {
                 const float gi = g[i] * f;
                 if (Q8) v[i] = v[i] * v[i];
-                m[i] = m[i] * p.b1 + gi * p.c1;
+                m[i] = (Q8 ? m[i] : m[i] * p.b1) + gi * p.c1;
                 v[i] = v[i] * p.b2 + gi * gi * p.c2;
-                root[i] = sqrtf(v[i]);
+                root[i] = root_of(v[i]);
                 const float upd = size * m[i] * __builtin_amdgcn_rcpf(root[i] * unbias + p.eps);
                 x[i] = x[i] - (x[i] * decay + upd);
             }
-            uint32_t rm[V], rv[V];
+            uint32_t rnd[V];
             if (Q8 || any) {
+                const uint32_t base = (uint32_t)e0 ^ key;       // (e0 % V == 0)
+#pragma unroll
+                for (int i = 0; i < V; ++i) rnd[i] = hash32(base ^ (uint32_t)i);
+            }
+            if (any) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const uint32_t r = hash32((uint32_t)(e0 + i) ^ key);
-                    rm[i] = r & 0xFFFFu;
-                    rv[i] = r >> 16;
-                    // (kept apart from the states' bits; a NaN stays one)
-                    if (any && x[i] == x[i])
-                        x[i] = __uint_as_float((__float_as_uint(x[i]) +
-                                                (hash32(r ^ 0x5BD1E995u) >> 16)) & 0xFFFF0000u);
+                    // (bits apart from the states'; a NaN stays one)
+                    const uint32_t u = __float_as_uint(x[i]);
+                    const uint32_t up = u + (hash32(rnd[i] ^ 0x5BD1E995u) >> 16);
+                    x[i] = __uint_as_float((x[i] == x[i] ? up : u) & 0xFFFF0000u);
                 }
             }
             if (t.master) store(x, t.master, true, e0, n, whole);
             store(x, t.param, pf32, e0, n, vec);
             if constexpr (Q8) {
-                mc = encode<false>(m, rm, ms);
-                vc = encode<true>(root, rv, vs);
+                mc = encode<false>(m, rnd, ms);
+                vc = encode<true>(root, rnd, vs);
                 if (whole) {
                     *(u32x2 *)((uint8_t *)t.m + e0) = mc;
                     *(u32x2 *)((uint8_t *)t.v + e0) = vc;

@@ -79,13 +79,17 @@ extern "C" int moe_adamw_step(const moe_adamw *h, int32_t n,
     p.seed = h->seed;
     p.stochastic = h->stochastic;
     const int most = 8 * device_cus();
+    double total = 0;
+    for (int i = 0; i < n; ++i) total += (double)tensors[i].numel;
+    p.chunk = MOE_ADAMW_CHUNK;
+    while (p.chunk > MOE_ADAMW_LEAST && total < (double)p.chunk * most) p.chunk /= 2;
     // the tensors from i on that one launch takes
     auto fill = [&](int &i, AdamwTable &tab) {
         tab = AdamwTable{};
         long long chunks = 0;
         for (; i < n && tab.count < MOE_ADAMW_TENSORS; ++i) {
             const moe_adamw_tensor &t = tensors[i];
-            const long long own = (t.numel + MOE_ADAMW_CHUNK - 1) / MOE_ADAMW_CHUNK;
+            const long long own = (t.numel + p.chunk - 1) / p.chunk;
             if (chunks + own > 0x7fffffffll - most) break;
             const bool ok = aligned(t.param) && aligned(t.grad);
             const int flags = (t.param_dtype == MOE_F32 ? ADAMW_PARAM_F32 : 0) |
