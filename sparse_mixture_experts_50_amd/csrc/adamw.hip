@@ -51,15 +51,15 @@ __device__ __forceinline__ void load(float (&x)[V], const void *p, bool f32, lon
         if (f32) {
 #pragma unroll
             for (int i = 0; i < V; i += 4) {
-                const floatx4 q = *(const floatx4 *)((const float *)p + e0 + i);
+                const floatx4 q = __builtin_nontemporal_load((const floatx4 *)((const float *)p + e0 + i));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[i + e] = q[e];
             }
         } else {
             const uint16_t *h = (const uint16_t *)p + e0;
             uint32_t w[V / 2];
-            if (V == 8) *(u32x4 *)w = *(const u32x4 *)h;
-            else *(u32x2 *)w = *(const u32x2 *)h;
+            if (V == 8) *(u32x4 *)w = __builtin_nontemporal_load((const u32x4 *)h);
+            else *(u32x2 *)w = __builtin_nontemporal_load((const u32x2 *)h);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
                 x[2 * i] = bf16_lo(w[i]);
@@ -84,15 +84,15 @@ __device__ __forceinline__ void store(const float (&x)[V], void *p, bool f32, lo
         if (f32) {
 #pragma unroll
             for (int i = 0; i < V; i += 4)
-                *(floatx4 *)((float *)p + e0 + i) =
-                    floatx4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+                __builtin_nontemporal_store(floatx4{x[i], x[i + 1], x[i + 2], x[i + 3]},
+                                            (floatx4 *)((float *)p + e0 + i));
         } else {
             uint16_t *h = (uint16_t *)p + e0;
             uint32_t w[V / 2];
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-            if (V == 8) *(u32x4 *)h = *(u32x4 *)w;
-            else *(u32x2 *)h = *(u32x2 *)w;
+            if (V == 8) __builtin_nontemporal_store(*(u32x4 *)w, (u32x4 *)h);
+            else __builtin_nontemporal_store(*(u32x2 *)w, (u32x2 *)h);
         }
     } else {
 #pragma unroll
@@ -176,7 +176,7 @@ __device__ __forceinline__ u32x2 encode(const float (&x)[8], const uint32_t (&rn
 }
 
 template <bool Q8>
-__global__ __launch_bounds__(THREADS) void adamw(AdamwTable tab, AdamwParams p) {
+__global__ __launch_bounds__(THREADS, 8) void adamw(AdamwTable tab, AdamwParams p) {
 #pragma clang fp contract(off)
     constexpr int V = Q8 ? 8 : 4;
     double lr = p.lr, bias1 = p.bias1, bias2 = p.bias2;
@@ -225,8 +225,8 @@ __global__ __launch_bounds__(THREADS) void adamw(AdamwTable tab, AdamwParams p) 
             else load(x, t.param, pf32, e0, n, vec);
             if constexpr (Q8) {
                 if (whole) {
-                    mc = *(const u32x2 *)((const uint8_t *)t.m + e0);
-                    vc = *(const u32x2 *)((const uint8_t *)t.v + e0);
+                    mc = __builtin_nontemporal_load((const u32x2 *)((const uint8_t *)t.m + e0));
+                    vc = __builtin_nontemporal_load((const u32x2 *)((const uint8_t *)t.v + e0));
                 } else if (live) {
                     for (int i = 0; i < n - e0; ++i) {
                         mc[i >> 2] |= (uint32_t)((const uint8_t *)t.m)[e0 + i] << (8 * (i & 3));
@@ -276,8 +276,8 @@ __global__ __launch_bounds__(THREADS) void adamw(AdamwTable tab, AdamwParams p) 
                 mc = encode<false>(m, rnd, ms);
                 vc = encode<true>(root, rnd, vs);
                 if (whole) {
-                    *(u32x2 *)((uint8_t *)t.m + e0) = mc;
-                    *(u32x2 *)((uint8_t *)t.v + e0) = vc;
+                    __builtin_nontemporal_store(mc, (u32x2 *)((uint8_t *)t.m + e0));
+                    __builtin_nontemporal_store(vc, (u32x2 *)((uint8_t *)t.v + e0));
                 } else if (live) {
                     for (int i = 0; i < n - e0; ++i) {
                         ((uint8_t *)t.m)[e0 + i] = (uint8_t)(mc[i >> 2] >> (8 * (i & 3)));

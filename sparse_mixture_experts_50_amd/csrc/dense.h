@@ -95,11 +95,9 @@ struct DenseTails {
     } t[MOE_DENSE_TAILS];
     int count;
 };
-hipError_t launch_dense_tails(const DenseTails &p, hipStream_t s);
-
 // Column sums (bias gradients) of up to three [M][C] tensors: by ranges of
 // rows into part, then joined.
-#define MOE_DENSE_SUM_ROWS 128
+#define MOE_DENSE_SUM_ROWS 256
 struct DenseSums {
     struct Item {
         const void *src;
@@ -112,4 +110,6 @@ struct DenseSums {
 __host__ __device__ inline int dense_sum_ranges(int M) {
     return (M + MOE_DENSE_SUM_ROWS - 1) / MOE_DENSE_SUM_ROWS;
 }
-hipError_t launch_dense_sums(const DenseSums &p, int dtype, hipStream_t s);
+// The sums by ranges (one range: the results) and the tails; the ranges joined.
+hipError_t launch_dense_sums(const DenseSums &p, const DenseTails &t, int dtype, hipStream_t s);
+hipError_t launch_dense_sums_join(const DenseSums &p, int dtype, hipStream_t s);

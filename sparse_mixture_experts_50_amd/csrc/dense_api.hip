@@ -52,6 +52,11 @@ DensePlan linear_plan(const moe_linear_desc *d) {
     return dense_rows_plan(d->dtype, d->M, d->N, d->K, gated(d->activation) ? 2 : 1, false, false);
 }
 
+size_t linear_bytes(const moe_linear_desc *d, const DensePlan &plan) {
+    const size_t n = align_up(plane_bytes(plan, d->M, d->N, gated(d->activation) ? 2 : 1));
+    return n ? n : kAlign;
+}
+
 struct LinearLayout {
     size_t dz, du, x_tail, dz_tail, plane, sums, total;
     DensePlan up, dx;
@@ -169,9 +174,7 @@ int zero(void *p, size_t bytes, hipStream_t s) {
 extern "C" {
 
 size_t moe_linear_workspace_size(const moe_linear_desc *d) {
-    if (check_linear(d) != MOE_OK) return 0;
-    const size_t n = align_up(plane_bytes(linear_plan(d), d->M, d->N, gated(d->activation) ? 2 : 1));
-    return n ? n : kAlign;
+    return check_linear(d) == MOE_OK ? linear_bytes(d, linear_plan(d)) : 0;
 }
 
 int moe_linear(const moe_linear_desc *d, const void *x, const moe_linear_weights *w,
@@ -181,14 +184,15 @@ int moe_linear(const moe_linear_desc *d, const void *x, const moe_linear_weights
     if (d->M == 0) return MOE_OK;
     if (!x || !y || !aligned(x, y, residual)) return MOE_ERR_INVALID_ARG;
     if ((st = check_linear_weights(d, w)) != MOE_OK) return st;
-    if (!ws || ws_bytes < moe_linear_workspace_size(d) || !aligned(ws)) return MOE_ERR_WORKSPACE;
+    const DensePlan plan = linear_plan(d);
+    if (!ws || ws_bytes < linear_bytes(d, plan) || !aligned(ws)) return MOE_ERR_WORKSPACE;
     if (clash({y}, {x, w->w, w->b, w->w3, w->b3, residual, ws})) return MOE_ERR_INVALID_ARG;
     DenseRows p = up_rows(d->M, d->N, d->K, d->activation, x, w->w, w->b, w->w3, w->b3);
     p.epilogue = DENSE_FORWARD;
     p.res = residual;
     p.y = y;
     p.plane = (float *)ws;
-    p.plan = linear_plan(d);
+    p.plan = plan;
     return to_status(launch_dense_rows(p, d->dtype, (hipStream_t)stream));
 }
 
@@ -209,11 +213,12 @@ int moe_linear_grad(const moe_linear_desc *d, const void *x, const moe_linear_we
               {x, dy, dx_add, ws, w ? w->w : nullptr, w ? w->b : nullptr, w ? w->w3 : nullptr,
                w ? w->b3 : nullptr}))
         return MOE_ERR_INVALID_ARG;
+    LinearLayout L = {};
     if (d->M > 0) {
         if (!x || !dy || !aligned(x, dy, dx_add)) return MOE_ERR_INVALID_ARG;
         if ((st = check_linear_weights(d, w)) != MOE_OK) return st;
-        if (!ws || ws_bytes < moe_linear_grad_workspace_size(d) || !aligned(ws))
-            return MOE_ERR_WORKSPACE;
+        L = linear_layout(d);
+        if (!ws || ws_bytes < L.total || !aligned(ws)) return MOE_ERR_WORKSPACE;
     }
     // gradients of what the layer does not have, and of no rows
     if (!two || d->M == 0) {
@@ -224,7 +229,6 @@ int moe_linear_grad(const moe_linear_desc *d, const void *x, const moe_linear_we
         if ((st = zero(g->w, mat, s)) != MOE_OK) return st;
         return zero(g->b, d->N * es, s);
     }
-    const LinearLayout L = linear_layout(d);
     const void *dz = none ? dy : at(ws, L.dz), *du = two ? at(ws, L.du) : nullptr;
     float *plane = (float *)at(ws, L.plane);
     if (!g->x && !g->w && !g->b && !(two && (g->w3 || g->b3))) return MOE_OK;
@@ -244,29 +248,29 @@ int moe_linear_grad(const moe_linear_desc *d, const void *x, const moe_linear_we
         p.plan = L.dx;
         if (launch_dense_rows(p, d->dtype, s) != hipSuccess) return MOE_ERR_HIP;
     }
-    DenseWeights q = linear_weights(d, x, dz, du, g);
-    if (q.count) {
-        if (d->dtype == MOE_BF16) {
-            Tails tails;
-            tails.M = d->M;
-            const void *xt = tails.of(x, at(ws, L.x_tail), d->K);
-            for (int k = 0; k < q.count; ++k) {
-                q.m[k].a2 = tails.of(q.m[k].a, none ? at(ws, L.dz_tail) : nullptr, d->N);
-                q.m[k].b2 = xt;
-            }
-            if (launch_dense_tails(tails.t, s) != hipSuccess) return MOE_ERR_HIP;
-        }
-        dense_weights_plan(q, d->dtype);
-        q.plane = plane;
-        if (launch_dense_weights(q, d->dtype, s) != hipSuccess) return MOE_ERR_HIP;
-    }
     DenseSums b = {};
     b.M = d->M;
     float *part = (float *)at(ws, L.sums);
     if (g->b) b.t[b.count++] = {dz, g->b, part, d->N};
     if (two && g->b3)
         b.t[b.count++] = {du, g->b3, part + (size_t)dense_sum_ranges(d->M) * d->N, d->N};
-    return to_status(launch_dense_sums(b, d->dtype, s));
+    DenseWeights q = linear_weights(d, x, dz, du, g);
+    Tails tails;
+    tails.M = d->M;
+    if (q.count && d->dtype == MOE_BF16) {
+        const void *xt = tails.of(x, at(ws, L.x_tail), d->K);
+        for (int k = 0; k < q.count; ++k) {
+            q.m[k].a2 = tails.of(q.m[k].a, none ? at(ws, L.dz_tail) : nullptr, d->N);
+            q.m[k].b2 = xt;
+        }
+    }
+    if (launch_dense_sums(b, tails.t, d->dtype, s) != hipSuccess) return MOE_ERR_HIP;
+    if (q.count) {
+        dense_weights_plan(q, d->dtype);
+        q.plane = plane;
+        if (launch_dense_weights(q, d->dtype, s) != hipSuccess) return MOE_ERR_HIP;
+    }
+    return to_status(launch_dense_sums_join(b, d->dtype, s));
 }
 
 }  // extern "C"
@@ -347,11 +351,11 @@ int moe_dense_forward(const moe_dense_desc *d, const void *x, const moe_dense_we
     if (d->T == 0) return MOE_OK;
     if (!x || !y || !aligned(x, y, residual)) return MOE_ERR_INVALID_ARG;
     if ((st = check_dense_weights(d, w)) != MOE_OK) return st;
-    if (!ws || ws_bytes < moe_dense_workspace_size(d) || !aligned(ws)) return MOE_ERR_WORKSPACE;
+    const DenseLayout L = forward_layout(d);
+    if (!ws || ws_bytes < L.total || !aligned(ws)) return MOE_ERR_WORKSPACE;
     if (clash({y}, {x, w->w1, w->b1, w->w2, w->b2, w->w3, w->b3, residual, ws}))
         return MOE_ERR_INVALID_ARG;
     hipStream_t s = (hipStream_t)stream;
-    const DenseLayout L = forward_layout(d);
     DenseRows p = up_rows(d->T, d->d_ff, d->d, d->activation, x, w->w1, w->b1, w->w3, w->b3);
     p.epilogue = DENSE_FORWARD;
     p.y = at(ws, L.h);
@@ -385,11 +389,12 @@ int moe_dense_backward(const moe_dense_desc *d, const void *x, const moe_dense_w
     const bool two = gated(d->activation);
     const int T = d->T, F = d->d_ff, D = d->d, dt = d->dtype;
     const size_t es = elem_bytes(dt), mat = (size_t)F * D * es;
+    DenseLayout L = {};
     if (T > 0) {
         if (!x || !dy || !aligned(x, dy, dx_add)) return MOE_ERR_INVALID_ARG;
         if ((st = check_dense_weights(d, w)) != MOE_OK) return st;
-        if (!ws || ws_bytes < moe_dense_grad_workspace_size(d) || !aligned(ws))
-            return MOE_ERR_WORKSPACE;
+        L = backward_layout(d);
+        if (!ws || ws_bytes < L.total || !aligned(ws)) return MOE_ERR_WORKSPACE;
     }
     if (!two || T == 0) {
         if ((st = zero(g->w3, mat, s)) != MOE_OK) return st;
@@ -401,7 +406,6 @@ int moe_dense_backward(const moe_dense_desc *d, const void *x, const moe_dense_w
         if ((st = zero(g->b1, F * es, s)) != MOE_OK) return st;
         return zero(g->b2, D * es, s);
     }
-    const DenseLayout L = backward_layout(d);
     float *plane = (float *)at(ws, L.plane);
     char *h = at(ws, L.h), *dz = at(ws, L.dz), *du = two ? at(ws, L.du) : nullptr;
     const bool w3 = two && g->w3, b3 = two && g->b3;
@@ -429,28 +433,6 @@ int moe_dense_backward(const moe_dense_desc *d, const void *x, const moe_dense_w
         p.plan = L.dx;
         if (launch_dense_rows(p, dt, s) != hipSuccess) return MOE_ERR_HIP;
     }
-    DenseWeights q = {};
-    q.M = T;
-    if (g->w1) q.m[q.count++] = {dz, x, nullptr, nullptr, g->w1, F, D};
-    if (w3) q.m[q.count++] = {du, x, nullptr, nullptr, g->w3, F, D};
-    if (g->w2) q.m[q.count++] = {dy, h, nullptr, nullptr, g->w2, D, F};
-    if (q.count) {
-        if (dt == MOE_BF16) {
-            Tails tails;
-            tails.M = T;
-            const void *xt = g->w1 || w3 ? tails.of(x, at(ws, L.x_tail), D) : nullptr;
-            for (int k = 0; k < q.count; ++k) {
-                DenseMat &m = q.m[k];
-                const bool second = m.a == dy;
-                m.a2 = tails.of(m.a, second ? at(ws, L.dy_tail) : nullptr, m.R);
-                m.b2 = second ? tails.of(h, nullptr, F) : xt;
-            }
-            if (launch_dense_tails(tails.t, s) != hipSuccess) return MOE_ERR_HIP;
-        }
-        dense_weights_plan(q, dt);
-        q.plane = plane;
-        if (launch_dense_weights(q, dt, s) != hipSuccess) return MOE_ERR_HIP;
-    }
     DenseSums b = {};
     b.M = T;
     float *part = (float *)at(ws, L.sums);
@@ -458,7 +440,29 @@ int moe_dense_backward(const moe_dense_desc *d, const void *x, const moe_dense_w
     if (g->b1) b.t[b.count++] = {dz, g->b1, part, F};
     if (b3) b.t[b.count++] = {du, g->b3, part + ranges * F, F};
     if (g->b2) b.t[b.count++] = {dy, g->b2, part + 2 * ranges * F, D};
-    return to_status(launch_dense_sums(b, dt, s));
+    DenseWeights q = {};
+    q.M = T;
+    if (g->w1) q.m[q.count++] = {dz, x, nullptr, nullptr, g->w1, F, D};
+    if (w3) q.m[q.count++] = {du, x, nullptr, nullptr, g->w3, F, D};
+    if (g->w2) q.m[q.count++] = {dy, h, nullptr, nullptr, g->w2, D, F};
+    Tails tails;
+    tails.M = T;
+    if (q.count && dt == MOE_BF16) {
+        const void *xt = g->w1 || w3 ? tails.of(x, at(ws, L.x_tail), D) : nullptr;
+        for (int k = 0; k < q.count; ++k) {
+            DenseMat &m = q.m[k];
+            const bool second = m.a == dy;
+            m.a2 = tails.of(m.a, second ? at(ws, L.dy_tail) : nullptr, m.R);
+            m.b2 = second ? tails.of(h, nullptr, F) : xt;
+        }
+    }
+    if (launch_dense_sums(b, tails.t, dt, s) != hipSuccess) return MOE_ERR_HIP;
+    if (q.count) {
+        dense_weights_plan(q, dt);
+        q.plane = plane;
+        if (launch_dense_weights(q, dt, s) != hipSuccess) return MOE_ERR_HIP;
+    }
+    return to_status(launch_dense_sums_join(b, dt, s));
 }
 
 }  // extern "C"

@@ -1,16 +1,17 @@
-// Small kernels around the dense layer's products: the last rows copied
-// beside zeros, bias gradients, and the epilogue of products whose sums lie in
+// Small kernels around the dense layer's products: bias gradients (and in the
+// same launch the last rows copied beside zeros), and the epilogue of products whose sums lie in
 // planes.  All bound by memory.
 #include "act.h"
 #include "dense.h"
 
 namespace {
 
-__global__ __launch_bounds__(256) void dense_tails(DenseTails p) {
-    const DenseTails::Item &t = p.t[blockIdx.y];
+// Rows copied, and rows zeroed after them, by all blocks of a plane of the grid.
+__device__ void copy_tail(const DenseTails::Item &t) {
     const size_t bytes = (size_t)t.row_bytes * t.rows, copied = (size_t)t.row_bytes * t.copied;
-    for (size_t b = ((size_t)blockIdx.x * 256 + threadIdx.x) * 16; b < bytes;
-         b += (size_t)gridDim.x * 256 * 16)
+    const size_t first = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
+    for (size_t b = (first * 256 + threadIdx.x) * 16; b < bytes;
+         b += (size_t)gridDim.x * gridDim.y * 256 * 16)
         *(u32x4 *)((char *)t.dst + b) =
             b < copied ? *(const u32x4 *)((const char *)t.src + b) : u32x4{0, 0, 0, 0};
 }
@@ -55,8 +56,17 @@ template <typename T> struct Vec {
 };
 
 // Block (c, r, k): columns [256 c, 256 c + 256) (fp32: 128) of range r of
-// item k, eight rows side by side.
-template <typename T> __global__ __launch_bounds__(256) void dense_sums(DenseSums p) {
+// item k, eight rows side by side; one range: the result itself.  Items after
+// the sums' are tails.
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(uint16_t *p, float v) { *p = (uint16_t)f32_to_bf16_bits(v); }
+
+template <typename T>
+__global__ __launch_bounds__(256) void dense_sums(DenseSums p, DenseTails tails) {
+    if ((int)blockIdx.z >= p.count) {
+        copy_tail(tails.t[blockIdx.z - p.count]);
+        return;
+    }
     constexpr int N = Vec<T>::N;
     __shared__ float red[8][32 * N];
     const DenseSums::Item &t = p.t[blockIdx.z];
@@ -67,6 +77,7 @@ template <typename T> __global__ __launch_bounds__(256) void dense_sums(DenseSum
     Vec<T> sum, x;
     sum.clear();
     if (c < t.C)
+#pragma unroll 4
         for (int m = m0 + lane; m < m1; m += 8) {
             x.load((const T *)t.src + (size_t)m * t.C + c);
 #pragma unroll
@@ -80,7 +91,9 @@ template <typename T> __global__ __launch_bounds__(256) void dense_sums(DenseSum
 #pragma unroll
         for (int l = 0; l < 8; ++l) s += red[l][i];
         const int at = blockIdx.x * 32 * N + i;
-        if (at < t.C) t.part[(size_t)blockIdx.y * t.C + at] = s;
+        if (at >= t.C) continue;
+        if (gridDim.y == 1) put((T *)t.out + at, s);
+        else t.part[(size_t)blockIdx.y * t.C + at] = s;
     }
 }
 // 64 columns by four ranges at a time.
@@ -96,8 +109,7 @@ template <typename T> __global__ __launch_bounds__(256) void dense_sums_join(Den
     __syncthreads();
     if (lane) return;
     s = (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
-    if (sizeof(T) == 2) ((uint16_t *)t.out)[c] = (uint16_t)f32_to_bf16_bits(s);
-    else ((float *)t.out)[c] = s;
+    put((T *)t.out + c, s);
 }
 
 // y = res + act(sums + bias), or h, dz, du: one vector of a row a thread.
@@ -188,31 +200,25 @@ template <typename T, int EPI> void finish_as(const DenseRows &p, hipStream_t s)
 
 }  // namespace
 
-hipError_t launch_dense_tails(const DenseTails &p, hipStream_t s) {
-    if (p.count == 0) return hipSuccess;
-    long long most = 1;
-    for (int i = 0; i < p.count; ++i) {
-        const long long n = ((long long)p.t[i].row_bytes * p.t[i].rows / 16 + 255) / 256;
-        if (n > most) most = n;
-    }
-    hipLaunchKernelGGL(dense_tails, dim3((unsigned)(most < 128 ? most : 128), p.count), dim3(256),
-                       0, s, p);
-    return hipGetLastError();
-}
-
-hipError_t launch_dense_sums(const DenseSums &p, int dtype, hipStream_t s) {
-    if (p.count == 0) return hipSuccess;
+hipError_t launch_dense_sums(const DenseSums &p, const DenseTails &t, int dtype, hipStream_t s) {
+    if (p.count + t.count == 0) return hipSuccess;
     int widest = 0;
     for (int i = 0; i < p.count; ++i) widest = p.t[i].C > widest ? p.t[i].C : widest;
     const int per = dtype == 1 ? 256 : 128;
-    const dim3 grid((widest + per - 1) / per, dense_sum_ranges(p.M), p.count), join(widest / 64, p.count);
-    if (dtype == 1) {
-        hipLaunchKernelGGL((dense_sums<uint16_t>), grid, dim3(256), 0, s, p);
-        hipLaunchKernelGGL((dense_sums_join<uint16_t>), join, dim3(256), 0, s, p);
-    } else {
-        hipLaunchKernelGGL((dense_sums<float>), grid, dim3(256), 0, s, p);
-        hipLaunchKernelGGL((dense_sums_join<float>), join, dim3(256), 0, s, p);
-    }
+    const dim3 grid(p.count ? (widest + per - 1) / per : 32, p.count ? dense_sum_ranges(p.M) : 1,
+                    p.count + t.count);
+    if (dtype == 1) hipLaunchKernelGGL((dense_sums<uint16_t>), grid, dim3(256), 0, s, p, t);
+    else hipLaunchKernelGGL((dense_sums<float>), grid, dim3(256), 0, s, p, t);
+    return hipGetLastError();
+}
+
+hipError_t launch_dense_sums_join(const DenseSums &p, int dtype, hipStream_t s) {
+    if (p.count == 0 || dense_sum_ranges(p.M) == 1) return hipSuccess;
+    int widest = 0;
+    for (int i = 0; i < p.count; ++i) widest = p.t[i].C > widest ? p.t[i].C : widest;
+    const dim3 join(widest / 64, p.count);
+    if (dtype == 1) hipLaunchKernelGGL((dense_sums_join<uint16_t>), join, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((dense_sums_join<float>), join, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 

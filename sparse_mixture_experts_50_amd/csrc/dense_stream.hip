@@ -252,6 +252,7 @@ template <typename T, int EPI, int P, int MB> void launch(const DenseRows &p, hi
 template <typename T, int EPI, int P> void by_rows(const DenseRows &p, hipStream_t s) {
     if (p.M <= 16) launch<T, EPI, P, 1>(p, s);
     else if (p.M <= 32) launch<T, EPI, P, 2>(p, s);
+    else if (p.M <= 48) launch<T, EPI, P, 3>(p, s);
     else launch<T, EPI, P, 4>(p, s);
 }
 template <typename T> void by_form(const DenseRows &p, hipStream_t s) {

@@ -10,6 +10,7 @@ Activations: "none", "gelu", "silu", and gated "swiglu" (SiLU(x w^T + b) *
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -34,11 +35,24 @@ def _type_and_act(dtype, activation):
     return _DT[dtype], _ACT[activation]
 
 
-def _size(name: str, desc) -> int:
+@functools.lru_cache(maxsize=1024)
+def _size_of(name: str, kind, sizes: tuple) -> int:
+    """A function of the descriptor's numbers alone."""
+    desc = kind(*sizes)
     n = getattr(_lib.lib(), name)(ctypes.byref(desc))
     if n == 0:
         raise _lib.MoeError(name, _lib.MOE_ERR_INVALID_ARG)
     return n
+
+
+def _linear_size(name: str, d) -> int:
+    return _size_of(name, MoeLinearDesc,
+                    (d.M, d.N, d.K, d.dtype, d.activation))
+
+
+def _dense_size(name: str, d) -> int:
+    return _size_of(name, MoeDenseDesc,
+                    (d.T, d.d, d.d_ff, d.dtype, d.activation))
 
 
 class _Weights:
@@ -165,11 +179,11 @@ def make_linear_desc(M: int, N: int, K: int, dtype: torch.dtype,
 
 
 def moe_linear_workspace_size(desc: MoeLinearDesc) -> int:
-    return _size("moe_linear_workspace_size", desc)
+    return _linear_size("moe_linear_workspace_size", desc)
 
 
 def moe_linear_grad_workspace_size(desc: MoeLinearDesc) -> int:
-    return _size("moe_linear_grad_workspace_size", desc)
+    return _linear_size("moe_linear_grad_workspace_size", desc)
 
 
 def _of_linear(desc, x, w, what):
@@ -216,11 +230,11 @@ def make_dense_desc(T: int, d: int, d_ff: int, dtype: torch.dtype,
 
 
 def moe_dense_workspace_size(desc: MoeDenseDesc) -> int:
-    return _size("moe_dense_workspace_size", desc)
+    return _dense_size("moe_dense_workspace_size", desc)
 
 
 def moe_dense_grad_workspace_size(desc: MoeDenseDesc) -> int:
-    return _size("moe_dense_grad_workspace_size", desc)
+    return _dense_size("moe_dense_grad_workspace_size", desc)
 
 
 def _of_dense(desc, x, w, what):

@@ -91,20 +91,25 @@ class AdamW:
         self._build()
 
     def _build(self):
-        """The list of moe_adamw_step; a step fills in the gradients."""
-        self._list = (_lib.MoeAdamwTensor * len(self.params))()
-        self._at = [0] * len(self.params)
+        """The list of moe_adamw_step, as its 64-bit words; a step fills in
+        the gradients, the counts and the types."""
+        count = len(self.params)
+        self._list = (_lib.MoeAdamwTensor * count)()
+        self._words = (ctypes.c_int64 * (10 * count)).from_buffer(self._list)
+        self._of = []                # shape, place and size of each
         ptr = lambda t: None if t is None else t.data_ptr()
         for i, p in enumerate(self.params):
             e = self._list[i]
-            e.param = self._at[i] = p.data_ptr()
+            e.param = p.data_ptr()
             e.m, e.v = ptr(self.m[i]), ptr(self.v[i])
             e.master = ptr(self.master[i])
             if self.state_bits == 8:
                 e.m_scale = ptr(self.m_scale[i])
                 e.v_scale = ptr(self.v_scale[i])
             e.weight_decay = self.weight_decay[i]
-            e.param_dtype = _DT[p.dtype]
+            # the last word: the parameter's type, the gradient's above it
+            types = {t: _DT[p.dtype] | code << 32 for t, code in _DT.items()}
+            self._of.append((p, p.shape, p.data_ptr(), p.numel(), types))
 
     @property
     def steps(self) -> int:
@@ -128,31 +133,31 @@ class AdamW:
         and its states as they are.  ``norm``: float32 [1] as moe_grad_norm
         leaves it: the gradients are scaled by min(1, max_norm / (norm +
         1e-6)) on the way."""
-        params, lst = self.params, self._list
-        if len(grads) != len(params):
+        if len(grads) != len(self.params):
             raise ValueError("as many gradients as there are parameters")
         if self._dev_steps is None and _capturing(self.device):
             raise ValueError("a captured step needs device_steps=True")
         if norm is not None:
             _need(norm, "norm", (1,), torch.float32, self.device)
-        device = self.device
-        for i, (p, g) in enumerate(zip(params, grads)):
-            e = lst[i]
+        device, words, k = self.device, self._words, 0
+        for g, (p, shape, at, n, types) in zip(grads, self._of):
             if g is None:
-                e.numel = 0
+                words[k + 7] = 0
+                k += 10
                 continue
-            dtype = _DT.get(g.dtype)
-            if dtype is None or g.shape != p.shape or g.device != device \
-                    or not g.is_contiguous():
-                if dtype is None:
-                    raise ValueError(f"gradient {i}: unsupported dtype "
-                                     f"{g.dtype}")
-                _need(g, f"gradient {i}", p.shape, g.dtype, device)
-            if p.data_ptr() != self._at[i]:
-                raise ValueError(f"parameter {i} has moved")
-            e.grad = g.data_ptr()
-            e.grad_dtype = dtype
-            e.numel = p.numel()
+            word = types.get(g.dtype)
+            if word is None:
+                raise ValueError(f"gradient {k // 10}: unsupported dtype "
+                                 f"{g.dtype}")
+            if g.shape != shape or g.device != device or \
+                    not g.is_contiguous():
+                _need(g, f"gradient {k // 10}", shape, g.dtype, device)
+            if p.data_ptr() != at:
+                raise ValueError(f"parameter {k // 10} has moved")
+            words[k + 1] = g.data_ptr()
+            words[k + 7] = n
+            words[k + 9] = word
+            k += 10
         h = _lib.MoeAdamw(
             self.lr, self.betas[0], self.betas[1], self.eps,
             self._host_steps + 1,
@@ -160,5 +165,6 @@ class AdamW:
             None if self.lr_scale is None else self.lr_scale.data_ptr(),
             None if norm is None else norm.data_ptr(), max_norm,
             self.state_bits, int(self.stochastic), self.seed & 0xFFFFFFFF)
-        _run("moe_adamw_step", device, ctypes.byref(h), len(params), lst)
+        _run("moe_adamw_step", device, ctypes.byref(h), len(self.params),
+             self._list)
         self._host_steps += 1
