@@ -71,8 +71,25 @@ LINEAR = [
 ]
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("M,N,K,act", LINEAR)
+# The large tiles: of 128 to 256 rows, an odd and an even number of stages,
+# whole and in ranges of K, with one and with two panels; single precision's.
+LARGE = [("bf16", *c) for c in [
+    (266, 6592, 4992, "none"), (1110, 7296, 512, "gelu"),
+    (1095, 9088, 320, "silu"), (203, 9792, 5120, "none"),
+    (4845, 3008, 128, "none"), (2282, 3648, 64, "gelu"),
+    (1417, 1536, 5120, "silu"), (96, 8960, 4224, "swiglu"),
+    (564, 8128, 2176, "geglu"), (558, 7808, 704, "swiglu"),
+    (132, 5632, 3712, "geglu"), (822, 7936, 256, "geglu"),
+    (849, 5952, 320, "swiglu"), (2670, 2112, 128, "swiglu"),
+    (1012, 5504, 64, "geglu"), (256, 4288, 4992, "swiglu")]] + [
+    ("f32", *c) for c in [
+        (2562, 2944, 256, "gelu"), (2984, 2432, 64, "none"),
+        (4531, 768, 128, "swiglu"), (1336, 2112, 64, "geglu")]]
+
+
+@pytest.mark.parametrize("dtype,M,N,K,act",
+                         [(t, *c) for c in LINEAR for t in ("bf16", "f32")] +
+                         LARGE)
 def test_linear(dtype, M, N, K, act):
     half = ref.HALF[DT[dtype]]
     for bias, res in ((False, False), (True, True)):
@@ -95,8 +112,26 @@ LINEAR_GRAD = [
 ]
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("M,N,K,act", LINEAR_GRAD)
+# Large tiles in the rows' gradient (of one and of two products), the weights'
+# and the pre-activations computed again.
+LARGE_GRAD = [("bf16", *c) for c in [
+    (277, 4736, 6720, "none"), (1057, 128, 8000, "none"),
+    (862, 192, 9920, "none"), (219, 4608, 8256, "none"),
+    (3718, 64, 4032, "none"), (1762, 5504, 1216, "silu"),
+    (83, 4992, 8960, "swiglu"), (291, 2304, 6848, "geglu"),
+    (1032, 448, 8448, "swiglu"), (1487, 64, 5440, "geglu"),
+    (2804, 2496, 704, "swiglu"), (77, 2624, 5120, "none"),
+    (4242, 1728, 1600, "none"), (4137, 960, 1408, "swiglu"),
+    (1110, 7296, 512, "gelu"), (1095, 9088, 320, "silu"),
+    (2282, 3648, 64, "gelu"), (558, 7808, 704, "swiglu"),
+    (2670, 2112, 128, "geglu"), (1012, 5504, 64, "swiglu")]] + [
+    ("f32", 993, 64, 6208, "none"), ("f32", 2562, 2944, 256, "silu"),
+    ("f32", 1336, 2112, 64, "swiglu")]
+
+
+@pytest.mark.parametrize("dtype,M,N,K,act",
+                         [(t, *c) for c in LINEAR_GRAD
+                          for t in ("bf16", "f32")] + LARGE_GRAD)
 def test_linear_grad(dtype, M, N, K, act):
     half = ref.HALF[DT[dtype]]
     rounds = 1 if act == "none" else 2
@@ -139,6 +174,7 @@ DENSE = [
     (64, 64, 1024, "geglu"), (65, 128, 320, "swiglu"),
     (256, 64, 256, "gelu"), (1000, 1024, 704, "swiglu"),
     (2050, 2048, 1408, "swiglu"), (1537, 1088, 2048, "gelu"),
+    (1057, 128, 8000, "silu"), (862, 192, 9920, "geglu"),
 ]
 OF_BLOCK = ("x", "w1", "w2", "w3", "b1", "b2", "b3")
 
