@@ -126,7 +126,7 @@ template <int B, int WN> struct Tiles {
                             part[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
                                 y[j][e], x[i][e], part[i][j], 0, 0, 0);
                 // (one half's fragments in registers at a time)
-                __builtin_amdgcn_sched_barrier(0);
+                if (B == 128) __builtin_amdgcn_sched_barrier(0);
             }
             if (more) {
                 // (last read before the barrier above)
