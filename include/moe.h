@@ -608,7 +608,8 @@ typedef struct moe_adamw {
  *            + lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps))
  * in fp32, from m and v before they are rounded to 8 bits.  A block of 8-bit
  * states with a value that is not finite becomes not-a-number throughout.
- * Needs 0 <= beta1, beta2 < 1, eps > 0, lr and weight_decay finite and >= 0.
+ * Needs 0 <= beta1, beta2 < 1, eps >= 2^-126, lr and weight_decay >= 0, all
+ * below 1e30.
  * `tensors` is a HOST array, read during the call.  No buffer of one tensor
  * may be one of another's (only a tensor's own are compared). */
 int moe_adamw_step(const moe_adamw *h, int32_t n,

@@ -110,9 +110,10 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));
 }
 
-// Correctly rounded root of v >= 0 (from 2^-96 on; below, off by 2^-24 of it at
-// most): the hardware's, off by one place at most, moved to a neighbour where
-// the residual says so.  0, infinity and NaN fail both comparisons.
+// Correctly rounded root of v >= 2^-96: the hardware's, off by one place at
+// most, moved to a neighbour where the residual says so.  0, infinity and NaN
+// fail both comparisons.  (Below, the residual loses bits, and the hardware
+// takes a denormal for 0.)
 __device__ __forceinline__ float root_of(float v) {
     const float s = __builtin_amdgcn_sqrtf(v);
     const float under = __uint_as_float(__float_as_uint(s) - 1);
@@ -245,6 +246,7 @@ __global__ __launch_bounds__(THREADS, 8) void adamw(AdamwTable tab, AdamwParams 
                 load(v, t.v, true, e0, n, whole);
             }
             float root[V];
+            uint32_t least = 0xFFFFFFFFu;            // (0 counts as the most)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float gi = g[i] * f;
@@ -252,6 +254,15 @@ __global__ __launch_bounds__(THREADS, 8) void adamw(AdamwTable tab, AdamwParams 
                 m[i] = (Q8 ? m[i] : m[i] * p.b1) + gi * p.c1;
                 v[i] = v[i] * p.b2 + gi * gi * p.c2;
                 root[i] = root_of(v[i]);
+                least = min(least, __float_as_uint(v[i]) - 1);
+            }
+            if (least < 0x0F800000u - 1) {           // 2^-96
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (v[i] < 0x1p-96f) root[i] = root_of(v[i] * 0x1p64f) * 0x1p-32f;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
                 const float upd = size * m[i] * __builtin_amdgcn_rcpf(root[i] * unbias + p.eps);
                 x[i] = x[i] - (x[i] * decay + upd);
             }

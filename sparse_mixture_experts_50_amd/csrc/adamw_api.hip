@@ -7,7 +7,6 @@ using namespace moe_host;
 
 namespace {
 
-
 int check_tensor(const moe_adamw *h, const moe_adamw_tensor &t) {
     if (t.numel < 0 || !(t.weight_decay >= 0.0) || t.weight_decay > 1e30)
         return MOE_ERR_INVALID_ARG;
@@ -41,9 +40,9 @@ int check_tensor(const moe_adamw *h, const moe_adamw_tensor &t) {
 extern "C" int moe_adamw_step(const moe_adamw *h, int32_t n,
                               const moe_adamw_tensor *tensors, void *stream) {
     if (!h || n < 0 || (n > 0 && !tensors)) return MOE_ERR_INVALID_ARG;
-    // (negated, so that what is not a number fails)
+    // (negated, so that what is not a number fails; 1 / eps has to be finite)
     if (!(h->lr >= 0.0 && h->lr < 1e30) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
-        !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps > 0.0 && h->eps < 1e30) ||
+        !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps >= 0x1p-126 && h->eps < 1e30) ||
         (!h->steps && h->step < 1) ||
         (h->norm && !(h->max_norm >= 0.0 && h->max_norm <= 1.7e308)) ||
         (h->stochastic != 0 && h->stochastic != 1) ||

@@ -377,3 +377,30 @@ def test_side_stream_and_norm():
     for x, y, k, t in zip(a, b, keep, grads):
         assert torch.equal(k, t)
         assert torch.equal(x, y)
+
+
+def test_tiny_second_moments():
+    """Second moments down to denormals: their roots are not 0, and with an
+    eps below them the update is m over the root.  Powers of two, so that the
+    states are exact; left are eight roundings (the reciprocal, off by one
+    place, counts two) and the root's."""
+    k = torch.arange(90, 141, device=device())
+    one = torch.ones(len(k), dtype=torch.float64, device=device())
+    p = torch.zeros(len(k), device=device())
+    opt = moe.AdamW([p], lr=1.0, betas=(0.5, 0.5), eps=2.0 ** -80,
+                    weight_decay=0.0)
+    opt.v[0].copy_(ref.ldexp(one, -k))
+    opt.m[0].fill_(2.0 ** -70)
+    opt.step([torch.zeros_like(p)])
+    assert torch.equal(opt.v[0].double(), ref.ldexp(one, -k - 1))
+    want = -2.0 ** -70 / (ref.ldexp(one, -k).sqrt() + 2.0 ** -80)
+    assert bool(((p.double() - want).abs() <=
+                 9 * 2.0 ** -24 * 1.001 * want.abs()).all())
+
+
+def test_least_eps():
+    """1 / eps stays finite: what has no gradient does not move."""
+    p = torch.ones(64, device=device())
+    opt = moe.AdamW([p], lr=1.0, eps=2.0 ** -126, weight_decay=0.0)
+    opt.step([torch.zeros_like(p)])
+    assert bool((p == 1).all())

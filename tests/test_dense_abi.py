@@ -173,6 +173,7 @@ def tensor(**kw):
     (dict(lr=float("inf")), INVALID), (dict(beta1=1.0), INVALID),
     (dict(beta1=-0.1), INVALID), (dict(beta2=1.0), INVALID),
     (dict(beta2=float("nan")), INVALID), (dict(eps=0.0), INVALID),
+    (dict(eps=1.1e-38), INVALID),
     (dict(eps=float("inf")), INVALID), (dict(step=0), INVALID),
     (dict(norm=7 * STEP, max_norm=-1.0), INVALID),
     (dict(norm=7 * STEP, max_norm=float("nan")), INVALID),
