@@ -268,7 +268,7 @@ __global__ __launch_bounds__(256, 4) void dense_weight_f32(DenseWeights p) {
 template <int PANELS, bool BK, bool TWO, int EPI, int ACT>
 hipError_t launch(const DenseRows &p, hipStream_t s) {
     const dim3 grid(p.plan.mt * p.plan.nt * p.plan.splits);
-    if constexpr (EPI != DENSE_PLANE && !TWO)
+    if constexpr (!TWO)
         if (!p.plan.small) {
             hipLaunchKernelGGL((dense_rows_f32<128, 4, PANELS, BK, TWO, EPI, ACT>), grid,
                                dim3(512), 0, s, p);

@@ -176,11 +176,14 @@ DENSE = [
     (2050, 2048, 1408, "swiglu"), (1537, 1088, 2048, "gelu"),
     (1057, 128, 8000, "silu"), (862, 192, 9920, "geglu"),
 ]
+# (every product on its large tiles, the gradient of h among them)
+DENSE_LARGE = [(2048, 1024, 4096, "silu"), (1500, 832, 7040, "swiglu"),
+               (4100, 704, 2112, "geglu")]
 OF_BLOCK = ("x", "w1", "w2", "w3", "b1", "b2", "b3")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("T,d,F,act", DENSE)
+@pytest.mark.parametrize("T,d,F,act", DENSE + DENSE_LARGE)
 def test_dense(dtype, T, d, F, act):
     half = ref.HALF[DT[dtype]]
     for bias in (False, True):
