@@ -50,6 +50,8 @@ struct DenseRows {
 // dtype: a moe_dtype.
 DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, bool two);
 hipError_t launch_dense_rows(const DenseRows &p, int dtype, hipStream_t s);
+// (a split one's sums are left in p.plane)
+hipError_t launch_dense_product(const DenseRows &p, int dtype, hipStream_t s);
 // The epilogue of a product whose sums lie in p.plane (plan.splits of them).
 hipError_t launch_dense_finish(const DenseRows &p, int dtype, hipStream_t s);
 // (parts of launch_dense_rows, by source file)
@@ -80,9 +82,7 @@ struct DenseWeights {
 };
 // Fills in small, splits, per and offset; returns the planes' elements.
 size_t dense_weights_plan(DenseWeights &p, int dtype);
-hipError_t launch_dense_weights(const DenseWeights &p, int dtype, hipStream_t s);
 hipError_t launch_dense_weights_mfma(const DenseWeights &p, hipStream_t s);
-hipError_t launch_dense_weights_f32(const DenseWeights &p, hipStream_t s);
 
 // Rows copied and rows zeroed, up to five items: dst[0, copied) = src, then
 // zeros up to rows.
@@ -110,6 +110,19 @@ struct DenseSums {
 __host__ __device__ inline int dense_sum_ranges(int M) {
     return (M + MOE_DENSE_SUM_ROWS - 1) / MOE_DENSE_SUM_ROWS;
 }
-// The sums by ranges (one range: the results) and the tails; the ranges joined.
+// The sums by ranges (one range: the results) and the tails.
 hipError_t launch_dense_sums(const DenseSums &p, const DenseTails &t, int dtype, hipStream_t s);
-hipError_t launch_dense_sums_join(const DenseSums &p, int dtype, hipStream_t s);
+
+// What a backward pass does once the pre-activations' gradients are there,
+// each part of which may be missing: the rows' gradient, the weights', the
+// biases'.
+struct DenseBack {
+    bool rows;
+    DenseRows dx;
+    DenseWeights w;
+    DenseSums b;
+    DenseTails t;
+};
+hipError_t launch_dense_back(const DenseBack &p, int dtype, hipStream_t s);
+// Products and sums of ranges, not yet joined (fp32, small tiles).
+hipError_t launch_dense_back_f32(const DenseBack &p, hipStream_t s);

@@ -58,7 +58,7 @@ size_t linear_bytes(const moe_linear_desc *d, const DensePlan &plan) {
 }
 
 struct LinearLayout {
-    size_t dz, du, x_tail, dz_tail, plane, sums, total;
+    size_t dz, du, x_tail, dz_tail, plane, w_plane, sums, total;
     DensePlan up, dx;
     DenseWeights w;
 };
@@ -86,9 +86,10 @@ LinearLayout linear_layout(const moe_linear_desc *d) {
     L.du = take(two ? rows * d->N * es : 0);
     L.x_tail = take((size_t)64 * d->K * es);
     L.dz_tail = take(none ? (size_t)64 * d->N * es : 0);
-    // (every wanted set of gradients fits the planes of all, and of one)
-    size_t planes = most(none ? 0 : plane_bytes(L.up, d->M, d->N, two ? 2 : 1),
-                         plane_bytes(L.dx, d->M, d->K, 1));
+    L.plane = take(most(none ? 0 : plane_bytes(L.up, d->M, d->N, two ? 2 : 1),
+                        plane_bytes(L.dx, d->M, d->K, 1)));
+    // (any number of the matrices' gradients may be wanted)
+    size_t planes = 0;
     for (int k = 1; k <= (two ? 2 : 1); ++k) {
         DenseWeights w = {};
         w.M = d->M;
@@ -96,7 +97,7 @@ LinearLayout linear_layout(const moe_linear_desc *d) {
         for (int i = 0; i < k; ++i) w.m[i] = {nullptr, nullptr, nullptr, nullptr, nullptr, d->N, d->K};
         planes = most(planes, dense_weights_plan(w, d->dtype) * 4);
     }
-    L.plane = take(planes);
+    L.w_plane = take(planes);
     L.sums = take((size_t)dense_sum_ranges(d->M) * d->N * 4 * (two ? 2 : 1));
     L.total = take.off ? take.off : kAlign;
     return L;
@@ -149,8 +150,9 @@ DenseRows down_rows(int M, int N, int K, const void *dz, const void *w, const vo
 // gradients: a tensor of the caller's is copied beside zeros, one of the
 // workspace (rows up to the next multiple of 64) gets zero rows.
 struct Tails {
-    DenseTails t = {};
     int M;
+    DenseTails &t;
+    Tails(int M, DenseTails &t) : M(M), t(t) {}
     const void *of(const void *src, void *tail, int cols) {
         const int whole = M / 64 * 64;
         const char *from = (const char *)src + (size_t)whole * cols * 2;
@@ -242,35 +244,32 @@ int moe_linear_grad(const moe_linear_desc *d, const void *x, const moe_linear_we
         p.plan = L.up;
         if (launch_dense_rows(p, d->dtype, s) != hipSuccess) return MOE_ERR_HIP;
     }
+    DenseBack back = {};
     if (g->x) {
-        DenseRows p = down_rows(d->M, d->K, d->N, dz, w->w, du, two ? w->w3 : nullptr, dx_add, g->x);
-        p.plane = plane;
-        p.plan = L.dx;
-        if (launch_dense_rows(p, d->dtype, s) != hipSuccess) return MOE_ERR_HIP;
+        back.rows = true;
+        back.dx = down_rows(d->M, d->K, d->N, dz, w->w, du, two ? w->w3 : nullptr, dx_add, g->x);
+        back.dx.plane = plane;
+        back.dx.plan = L.dx;
     }
-    DenseSums b = {};
+    DenseSums &b = back.b;
     b.M = d->M;
     float *part = (float *)at(ws, L.sums);
     if (g->b) b.t[b.count++] = {dz, g->b, part, d->N};
     if (two && g->b3)
         b.t[b.count++] = {du, g->b3, part + (size_t)dense_sum_ranges(d->M) * d->N, d->N};
-    DenseWeights q = linear_weights(d, x, dz, du, g);
-    Tails tails;
-    tails.M = d->M;
+    DenseWeights &q = back.w;
+    q = linear_weights(d, x, dz, du, g);
     if (q.count && d->dtype == MOE_BF16) {
+        Tails tails(d->M, back.t);
         const void *xt = tails.of(x, at(ws, L.x_tail), d->K);
         for (int k = 0; k < q.count; ++k) {
             q.m[k].a2 = tails.of(q.m[k].a, none ? at(ws, L.dz_tail) : nullptr, d->N);
             q.m[k].b2 = xt;
         }
     }
-    if (launch_dense_sums(b, tails.t, d->dtype, s) != hipSuccess) return MOE_ERR_HIP;
-    if (q.count) {
-        dense_weights_plan(q, d->dtype);
-        q.plane = plane;
-        if (launch_dense_weights(q, d->dtype, s) != hipSuccess) return MOE_ERR_HIP;
-    }
-    return to_status(launch_dense_sums_join(b, d->dtype, s));
+    dense_weights_plan(q, d->dtype);
+    q.plane = (float *)at(ws, L.w_plane);
+    return to_status(launch_dense_back(back, d->dtype, s));
 }
 
 }  // extern "C"
@@ -281,7 +280,7 @@ namespace {
 
 struct DenseLayout {
     size_t h, plane, total;                       // forward
-    size_t q, dz, du, x_tail, dy_tail, sums;      // backward
+    size_t q, dz, du, x_tail, dy_tail, w_plane, sums;     // backward
     DensePlan up, down, qp, dx;
 };
 
@@ -312,8 +311,9 @@ DenseLayout backward_layout(const moe_dense_desc *d) {
     L.du = take(two ? rows * F * es : 0);
     L.x_tail = take((size_t)64 * d->d * es);
     L.dy_tail = take((size_t)64 * d->d * es);
-    size_t planes = most(plane_bytes(L.up, d->T, d->d_ff, two ? 2 : 1),
-                         plane_bytes(L.dx, d->T, d->d, 1));
+    L.plane = take(most(plane_bytes(L.up, d->T, d->d_ff, two ? 2 : 1),
+                        plane_bytes(L.dx, d->T, d->d, 1)));
+    size_t planes = 0;
     // (any number of the matrices' gradients may be wanted)
     for (int k = 1; k <= (two ? 3 : 2); ++k) {
         DenseWeights w = {};
@@ -323,7 +323,7 @@ DenseLayout backward_layout(const moe_dense_desc *d) {
             w.m[i] = {nullptr, nullptr, nullptr, nullptr, nullptr, d->d_ff, d->d};
         planes = most(planes, dense_weights_plan(w, d->dtype) * 4);
     }
-    L.plane = take(planes);
+    L.w_plane = take(planes);
     L.sums = take((size_t)dense_sum_ranges(d->T) * (2 * F + d->d) * 4);
     L.total = take.off ? take.off : kAlign;
     return L;
@@ -427,27 +427,27 @@ int moe_dense_backward(const moe_dense_desc *d, const void *x, const moe_dense_w
         p.plan = L.up;
         if (launch_dense_rows(p, dt, s) != hipSuccess) return MOE_ERR_HIP;
     }
+    DenseBack back = {};
     if (g->x) {
-        DenseRows p = down_rows(T, D, F, dz, w->w1, du, two ? w->w3 : nullptr, dx_add, g->x);
-        p.plane = plane;
-        p.plan = L.dx;
-        if (launch_dense_rows(p, dt, s) != hipSuccess) return MOE_ERR_HIP;
+        back.rows = true;
+        back.dx = down_rows(T, D, F, dz, w->w1, du, two ? w->w3 : nullptr, dx_add, g->x);
+        back.dx.plane = plane;
+        back.dx.plan = L.dx;
     }
-    DenseSums b = {};
+    DenseSums &b = back.b;
     b.M = T;
     float *part = (float *)at(ws, L.sums);
     const size_t ranges = dense_sum_ranges(T);
     if (g->b1) b.t[b.count++] = {dz, g->b1, part, F};
     if (b3) b.t[b.count++] = {du, g->b3, part + ranges * F, F};
     if (g->b2) b.t[b.count++] = {dy, g->b2, part + 2 * ranges * F, D};
-    DenseWeights q = {};
+    DenseWeights &q = back.w;
     q.M = T;
     if (g->w1) q.m[q.count++] = {dz, x, nullptr, nullptr, g->w1, F, D};
     if (w3) q.m[q.count++] = {du, x, nullptr, nullptr, g->w3, F, D};
     if (g->w2) q.m[q.count++] = {dy, h, nullptr, nullptr, g->w2, D, F};
-    Tails tails;
-    tails.M = T;
     if (q.count && dt == MOE_BF16) {
+        Tails tails(T, back.t);
         const void *xt = g->w1 || w3 ? tails.of(x, at(ws, L.x_tail), D) : nullptr;
         for (int k = 0; k < q.count; ++k) {
             DenseMat &m = q.m[k];
@@ -456,13 +456,9 @@ int moe_dense_backward(const moe_dense_desc *d, const void *x, const moe_dense_w
             m.b2 = second ? tails.of(h, nullptr, F) : xt;
         }
     }
-    if (launch_dense_sums(b, tails.t, dt, s) != hipSuccess) return MOE_ERR_HIP;
-    if (q.count) {
-        dense_weights_plan(q, dt);
-        q.plane = plane;
-        if (launch_dense_weights(q, dt, s) != hipSuccess) return MOE_ERR_HIP;
-    }
-    return to_status(launch_dense_sums_join(b, dt, s));
+    dense_weights_plan(q, dt);
+    q.plane = (float *)at(ws, L.w_plane);
+    return to_status(launch_dense_back(back, dt, s));
 }
 
 }  // extern "C"

@@ -11,8 +11,7 @@
 // banks.  Sums run over 64 k at a time and are then added to the total, which
 // keeps their error near one rounding's.
 // Bound by the MFMAs (157 TFLOP/s).
-#include "act.h"
-#include "dense.h"
+#include "dense_parts.h"
 
 namespace {
 
@@ -160,12 +159,12 @@ __device__ __forceinline__ Tile tile_at(int L, int mt, int nt, int bm, int bn) {
 }
 
 template <int B, int WN, int PANELS, bool BK, bool TWO, int EPI, int ACT>
-__global__ __launch_bounds__(128 * WN, 4) void dense_rows_f32(DenseRows p) {
+__device__ __forceinline__ void rows_tile(const DenseRows &p, int L,
+                                          typename Tiles<B, WN>::Stage &st) {
     typedef Tiles<B, WN> P;
     constexpr int BN = B / PANELS, NJ = P::NJ / PANELS;
-    __shared__ typename P::Stage st;
     const int M = p.M, N = p.N, K = p.K;
-    const Tile t = tile_at(blockIdx.x, p.plan.mt, p.plan.nt, B, BN);
+    const Tile t = tile_at(L, p.plan.mt, p.plan.nt, B, BN);
     const int rows = min(B, M - t.m0), columns = min(BN, N - t.n0);
     const int k0 = t.split * p.plan.per * 64, k = min(p.plan.per * 64, K - k0);
     const size_t bat = BK ? (size_t)k0 * N + t.n0 : (size_t)t.n0 * K + k0;
@@ -228,12 +227,17 @@ __global__ __launch_bounds__(128 * WN, 4) void dense_rows_f32(DenseRows p) {
     }
 }
 
-__global__ __launch_bounds__(256, 4) void dense_weight_f32(DenseWeights p) {
+template <int B, int WN, int PANELS, bool BK, bool TWO, int EPI, int ACT>
+__global__ __launch_bounds__(128 * WN, 4) void dense_rows_f32(DenseRows p) {
+    __shared__ typename Tiles<B, WN>::Stage st;
+    rows_tile<B, WN, PANELS, BK, TWO, EPI, ACT>(p, blockIdx.x, st);
+}
+
+__device__ __forceinline__ void weight_tile(const DenseWeights &p, int L, Tiles<64, 2>::Stage &st) {
     constexpr int B = 64, WN = 2;
     typedef Tiles<B, WN> P;
-    __shared__ typename P::Stage st;
     auto tiles = [&](int n) { return (n + B - 1) / B; };
-    int L = blockIdx.x, k = 0;
+    int k = 0;
     for (; k + 1 < p.count; ++k) {
         const int n = tiles(p.m[k].R) * tiles(p.m[k].C) * p.splits;
         if (L < n) break;
@@ -265,27 +269,52 @@ __global__ __launch_bounds__(256, 4) void dense_weight_f32(DenseWeights p) {
     }
 }
 
-template <int PANELS, bool BK, bool TWO, int EPI, int ACT>
-hipError_t launch(const DenseRows &p, hipStream_t s) {
-    const dim3 grid(p.plan.mt * p.plan.nt * p.plan.splits);
-    if constexpr (!TWO)
-        if (!p.plan.small) {
-            hipLaunchKernelGGL((dense_rows_f32<128, 4, PANELS, BK, TWO, EPI, ACT>), grid,
-                               dim3(512), 0, s, p);
-            return hipGetLastError();
+// The rows' gradient (blocks up to `rows`), the weights' (up to `weights`
+// more) and the column sums: nothing here waits for another.
+template <bool TWO, int EPI>
+__global__ __launch_bounds__(256, 4) void dense_back_f32(DenseBack p, int rows, int weights) {
+    __shared__ Tiles<64, 2>::Stage st;
+    static_assert(sizeof(st) >= dense_parts::SUMS_LDS, "sums in a stage");
+    int block = blockIdx.x;
+    if (block < rows) {
+        rows_tile<64, 2, 1, true, TWO, EPI, ACT_NONE>(p.dx, block, st);
+    } else if ((block -= rows) < weights) {
+        weight_tile(p.w, block, st);
+    } else {
+        block -= weights;
+        const int ranges = dense_sum_ranges(p.b.M);
+        int k = 0;
+        for (;; ++k) {
+            const int n = (p.b.t[k].C + 127) / 128 * ranges;
+            if (block < n) break;
+            block -= n;
         }
-    hipLaunchKernelGGL((dense_rows_f32<64, 2, PANELS, BK, TWO, EPI, ACT>), grid, dim3(256), 0, s,
-                       p);
+        dense_parts::sum_columns<float>(p.b.t[k], p.b.M, block / ranges, block % ranges,
+                                        (float *)&st);
+    }
+}
+
+template <int PANELS, bool BK, int EPI, int ACT>
+hipError_t launch_large(const DenseRows &p, hipStream_t s) {
+    hipLaunchKernelGGL((dense_rows_f32<128, 4, PANELS, BK, false, EPI, ACT>),
+                       dim3(p.plan.mt * p.plan.nt), dim3(512), 0, s, p);
+    return hipGetLastError();
+}
+template <int PANELS, bool BK, int EPI, int ACT>
+hipError_t launch(const DenseRows &p, hipStream_t s) {
+    if (!p.plan.small) return launch_large<PANELS, BK, EPI, ACT>(p, s);
+    hipLaunchKernelGGL((dense_rows_f32<64, 2, PANELS, BK, false, EPI, ACT>),
+                       dim3(p.plan.mt * p.plan.nt * p.plan.splits), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
 template <int EPI> hipError_t by_act(const DenseRows &p, hipStream_t s) {
     switch (p.act) {
-    case ACT_GELU: return launch<1, false, false, EPI, ACT_GELU>(p, s);
-    case ACT_SILU: return launch<1, false, false, EPI, ACT_SILU>(p, s);
-    case ACT_SWIGLU: return launch<2, false, false, EPI, ACT_SWIGLU>(p, s);
-    case ACT_GEGLU: return launch<2, false, false, EPI, ACT_GEGLU>(p, s);
-    default: return launch<1, false, false, EPI, ACT_NONE>(p, s);
+    case ACT_GELU: return launch<1, false, EPI, ACT_GELU>(p, s);
+    case ACT_SILU: return launch<1, false, EPI, ACT_SILU>(p, s);
+    case ACT_SWIGLU: return launch<2, false, EPI, ACT_SWIGLU>(p, s);
+    case ACT_GEGLU: return launch<2, false, EPI, ACT_GEGLU>(p, s);
+    default: return launch<1, false, EPI, ACT_NONE>(p, s);
     }
 }
 
@@ -293,21 +322,33 @@ template <int EPI> hipError_t by_act(const DenseRows &p, hipStream_t s) {
 
 hipError_t launch_dense_rows_f32(const DenseRows &p, hipStream_t s) {
     if (p.epilogue == DENSE_PLANE) {
-        if (p.two) return launch<1, true, true, DENSE_PLANE, ACT_NONE>(p, s);
-        if (p.bk) return launch<1, true, false, DENSE_PLANE, ACT_NONE>(p, s);
-        return p.panels() == 2 ? launch<2, false, false, DENSE_PLANE, ACT_SWIGLU>(p, s)
-                               : launch<1, false, false, DENSE_PLANE, ACT_NONE>(p, s);
+        if (p.bk) return launch<1, true, DENSE_PLANE, ACT_NONE>(p, s);
+        return p.panels() == 2 ? launch<2, false, DENSE_PLANE, ACT_SWIGLU>(p, s)
+                               : launch<1, false, DENSE_PLANE, ACT_NONE>(p, s);
     }
-    if (p.two) return launch<1, true, true, DENSE_FORWARD, ACT_NONE>(p, s);
-    if (p.bk) return launch<1, true, false, DENSE_FORWARD, ACT_NONE>(p, s);
+    // (with small tiles a part of the backward pass's launch)
+    if (p.bk) return launch_large<1, true, DENSE_FORWARD, ACT_NONE>(p, s);
     return p.epilogue == DENSE_FORWARD ? by_act<DENSE_FORWARD>(p, s) : by_act<DENSE_GRAD>(p, s);
 }
 
-hipError_t launch_dense_weights_f32(const DenseWeights &p, hipStream_t s) {
+hipError_t launch_dense_back_f32(const DenseBack &p, hipStream_t s) {
     constexpr int b = 64;
-    long long tiles = 0;
-    for (int k = 0; k < p.count; ++k)
-        tiles += (long long)((p.m[k].R + b - 1) / b) * ((p.m[k].C + b - 1) / b) * p.splits;
-    hipLaunchKernelGGL(dense_weight_f32, dim3((unsigned)tiles), dim3(256), 0, s, p);
-    return hipGetLastError();
+    long long weights = 0;
+    for (int k = 0; k < p.w.count; ++k)
+        weights += (long long)((p.w.m[k].R + b - 1) / b) * ((p.w.m[k].C + b - 1) / b) * p.w.splits;
+    const int rows = p.rows ? p.dx.plan.mt * p.dx.plan.nt * p.dx.plan.splits : 0;
+    int sums = 0;
+    for (int k = 0; k < p.b.count; ++k)
+        sums += (p.b.t[k].C + 127) / 128 * dense_sum_ranges(p.b.M);
+    if (rows + weights + sums == 0) return hipSuccess;
+    const dim3 grid((unsigned)(rows + weights + sums));
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, p, rows, (int)weights);
+        return hipGetLastError();
+    };
+    if (p.rows && p.dx.plan.splits > 1)
+        return p.dx.two ? run(dense_back_f32<true, DENSE_PLANE>)
+                        : run(dense_back_f32<false, DENSE_PLANE>);
+    return p.rows && p.dx.two ? run(dense_back_f32<true, DENSE_FORWARD>)
+                              : run(dense_back_f32<false, DENSE_FORWARD>);
 }

@@ -1,10 +1,12 @@
-// Small kernels around the dense layer's products: bias gradients (and in the
-// same launch the last rows copied beside zeros), and the epilogue of products whose sums lie in
-// planes.  All bound by memory.
-#include "act.h"
-#include "dense.h"
+// Small kernels around the dense layer's products, and what is launched of
+// them: bias gradients (and in the same launch the last rows copied beside
+// zeros), the epilogue of products whose sums lie in planes, planes and ranges
+// joined.  All bound by memory.
+#include "dense_parts.h"
 
 namespace {
+
+using namespace dense_parts;
 
 // Rows copied, and rows zeroed after them, by all blocks of a plane of the grid.
 __device__ void copy_tail(const DenseTails::Item &t) {
@@ -16,95 +18,60 @@ __device__ void copy_tail(const DenseTails::Item &t) {
             b < copied ? *(const u32x4 *)((const char *)t.src + b) : u32x4{0, 0, 0, 0};
 }
 
-// Eight (fp32: four) columns of a row as fp32.
-template <typename T> struct Vec {
-    static constexpr int N = sizeof(T) == 2 ? 8 : 4;
-    float v[N];
-    __device__ __forceinline__ void load(const T *p) {
-        const u32x4 q = *(const u32x4 *)p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (N == 8) {
-                v[2 * i] = bf16_lo(q[i]);
-                v[2 * i + 1] = bf16_hi(q[i]);
-            } else {
-                v[i] = __uint_as_float(q[i]);
-            }
-        }
-    }
-    __device__ __forceinline__ void store(T *p) const {
-        u32x4 q;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            q[i] = N == 8 ? pack_bf16x2(v[(2 * i) % N], v[(2 * i + 1) % N])
-                          : __float_as_uint(v[i]);
-        *(u32x4 *)p = q;
-    }
-    // += N fp32 values
-    __device__ __forceinline__ void add(const float *p) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const floatx4 q = *(const floatx4 *)(p + i);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[i + e] += q[e];
-        }
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    }
-};
-
-// Block (c, r, k): columns [256 c, 256 c + 256) (fp32: 128) of range r of
-// item k, eight rows side by side; one range: the result itself.  Items after
-// the sums' are tails.
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(uint16_t *p, float v) { *p = (uint16_t)f32_to_bf16_bits(v); }
-
+// Block (c, r, k): columns c of range r of item k; items after the sums' are
+// tails.
 template <typename T>
 __global__ __launch_bounds__(256) void dense_sums(DenseSums p, DenseTails tails) {
-    if ((int)blockIdx.z >= p.count) {
-        copy_tail(tails.t[blockIdx.z - p.count]);
+    __shared__ float lds[SUMS_LDS / 4];
+    if ((int)blockIdx.z >= p.count) copy_tail(tails.t[blockIdx.z - p.count]);
+    else sum_columns<T>(p.t[blockIdx.z], p.M, blockIdx.x, blockIdx.y, lds);
+}
+
+// What products and sums of ranges left behind, added up: the rows' gradient
+// (blocks up to `rows`), the weights' (up to `weights`, as many for each
+// matrix), the column sums (64 columns by four ranges at a time).
+template <typename T>
+__global__ __launch_bounds__(256) void dense_joins(DenseRows p, DenseWeights w, DenseSums b,
+                                                   int rows, int weights) {
+    constexpr int N = Vec<T>::N;
+    int block = blockIdx.x;
+    if (block < rows) {
+        const size_t plane = (size_t)p.M * p.N, at = ((size_t)block * 256 + threadIdx.x) * N;
+        if (at >= plane) return;
+        Vec<T> s, a;
+        s.clear();
+#pragma unroll 4
+        for (int i = 0; i < p.plan.splits; ++i) s.add(p.plane + i * plane + at);
+        if (p.res) {
+            a.load((const T *)p.res + at);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s.v[i] += a.v[i];
+        }
+        s.store((T *)p.y + at);
         return;
     }
-    constexpr int N = Vec<T>::N;
-    __shared__ float red[8][32 * N];
-    const DenseSums::Item &t = p.t[blockIdx.z];
-    const int col = threadIdx.x & 31, lane = threadIdx.x >> 5;
-    const int c = (blockIdx.x * 32 + col) * N;
-    if (blockIdx.x * 32 * N >= t.C) return;
-    const int m0 = blockIdx.y * MOE_DENSE_SUM_ROWS, m1 = min(p.M, m0 + MOE_DENSE_SUM_ROWS);
-    Vec<T> sum, x;
-    sum.clear();
-    if (c < t.C)
+    block -= rows;
+    if (block < weights) {
+        const int each = weights / w.count, k = block / each;
+        const DenseMat &m = w.m[k];
+        const size_t size = (size_t)m.R * m.C;
+        const size_t at = ((size_t)(block - k * each) * 256 + threadIdx.x) * N;
+        if (at >= size) return;
+        Vec<T> s;
+        s.clear();
 #pragma unroll 4
-        for (int m = m0 + lane; m < m1; m += 8) {
-            x.load((const T *)t.src + (size_t)m * t.C + c);
-#pragma unroll
-            for (int i = 0; i < N; ++i) sum.v[i] += x.v[i];
-        }
-#pragma unroll
-    for (int i = 0; i < N; ++i) red[lane][col * N + i] = sum.v[i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 32 * N; i += 256) {
-        float s = 0.0f;
-#pragma unroll
-        for (int l = 0; l < 8; ++l) s += red[l][i];
-        const int at = blockIdx.x * 32 * N + i;
-        if (at >= t.C) continue;
-        if (gridDim.y == 1) put((T *)t.out + at, s);
-        else t.part[(size_t)blockIdx.y * t.C + at] = s;
+        for (int i = 0; i < w.splits; ++i) s.add(w.plane + w.offset[k] + i * size + at);
+        s.store((T *)m.out + at);
+        return;
     }
-}
-// 64 columns by four ranges at a time.
-template <typename T> __global__ __launch_bounds__(256) void dense_sums_join(DenseSums p) {
+    block -= weights;
     __shared__ float red[4][64];
-    const DenseSums::Item &t = p.t[blockIdx.y];
-    const int c = blockIdx.x * 64 + (threadIdx.x & 63), lane = threadIdx.x >> 6;
-    const int ranges = dense_sum_ranges(p.M);
-    if (blockIdx.x * 64 >= t.C) return;
+    int k = 0;
+    while (block >= b.t[k].C / 64) block -= b.t[k++].C / 64;
+    const DenseSums::Item &t = b.t[k];
+    const int c = block * 64 + (threadIdx.x & 63), lane = threadIdx.x >> 6;
     float s = 0.0f;
-    for (int r = lane; r < ranges; r += 4) s += t.part[(size_t)r * t.C + c];
+    for (int r = lane; r < dense_sum_ranges(b.M); r += 4) s += t.part[(size_t)r * t.C + c];
     red[lane][threadIdx.x & 63] = s;
     __syncthreads();
     if (lane) return;
@@ -170,20 +137,6 @@ __global__ __launch_bounds__(256) void dense_finish(DenseRows p) {
     if (p.h) h.store((T *)p.h + at);
 }
 
-// The planes of weight gradients, added up: block row k is matrix k.
-template <typename T> __global__ __launch_bounds__(256) void dense_weight_finish(DenseWeights p) {
-    constexpr int N = Vec<T>::N;
-    const DenseMat &m = p.m[blockIdx.y];
-    const size_t size = (size_t)m.R * m.C;
-    const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * N;
-    if (at >= size) return;
-    Vec<T> s;
-    s.clear();
-#pragma unroll 4
-    for (int i = 0; i < p.splits; ++i) s.add(p.plane + p.offset[blockIdx.y] + i * size + at);
-    s.store((T *)m.out + at);
-}
-
 template <typename T, int EPI> void finish_as(const DenseRows &p, hipStream_t s) {
     const long long vectors = (long long)p.M * p.N / Vec<T>::N;
     const dim3 grid((unsigned)((vectors + 255) / 256)), block(256);
@@ -212,16 +165,6 @@ hipError_t launch_dense_sums(const DenseSums &p, const DenseTails &t, int dtype,
     return hipGetLastError();
 }
 
-hipError_t launch_dense_sums_join(const DenseSums &p, int dtype, hipStream_t s) {
-    if (p.count == 0 || dense_sum_ranges(p.M) == 1) return hipSuccess;
-    int widest = 0;
-    for (int i = 0; i < p.count; ++i) widest = p.t[i].C > widest ? p.t[i].C : widest;
-    const dim3 join(widest / 64, p.count);
-    if (dtype == 1) hipLaunchKernelGGL((dense_sums_join<uint16_t>), join, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((dense_sums_join<float>), join, dim3(256), 0, s, p);
-    return hipGetLastError();
-}
-
 hipError_t launch_dense_finish(const DenseRows &p, int dtype, hipStream_t s) {
     if (dtype == 1) {
         if (p.epilogue == DENSE_FORWARD) finish_as<uint16_t, DENSE_FORWARD>(p, s);
@@ -234,32 +177,59 @@ hipError_t launch_dense_finish(const DenseRows &p, int dtype, hipStream_t s) {
 }
 
 // A split product leaves its planes, and the epilogue is a kernel of its own.
-hipError_t launch_dense_rows(const DenseRows &p, int dtype, hipStream_t s) {
+hipError_t launch_dense_product(const DenseRows &p, int dtype, hipStream_t s) {
     if (p.plan.stream) return launch_dense_stream(p, dtype, s);
     DenseRows q = p;
     if (p.plan.splits > 1) q.epilogue = DENSE_PLANE;
-    hipError_t e;
-    if (dtype != 1) e = launch_dense_rows_f32(q, s);
-    else if (q.epilogue == DENSE_PLANE) e = launch_dense_plane_mfma(q, s);
-    else if (q.epilogue == DENSE_FORWARD) e = launch_dense_forward_mfma(q, s);
-    else e = launch_dense_grad_mfma(q, s);
-    if (e != hipSuccess || q.epilogue == p.epilogue) return e;
+    if (dtype != 1) return launch_dense_rows_f32(q, s);
+    if (q.epilogue == DENSE_PLANE) return launch_dense_plane_mfma(q, s);
+    return q.epilogue == DENSE_FORWARD ? launch_dense_forward_mfma(q, s)
+                                       : launch_dense_grad_mfma(q, s);
+}
+
+hipError_t launch_dense_rows(const DenseRows &p, int dtype, hipStream_t s) {
+    const hipError_t e = launch_dense_product(p, dtype, s);
+    if (e != hipSuccess || p.plan.stream || p.plan.splits == 1 || p.epilogue == DENSE_PLANE)
+        return e;
     return launch_dense_finish(p, dtype, s);
 }
 
-hipError_t launch_dense_weights(const DenseWeights &p, int dtype, hipStream_t s) {
-    if (p.count == 0) return hipSuccess;
-    const hipError_t e =
-        dtype == 1 ? launch_dense_weights_mfma(p, s) : launch_dense_weights_f32(p, s);
-    if (e != hipSuccess || p.splits == 1) return e;
-    size_t most = 0;
-    for (int k = 0; k < p.count; ++k) {
-        const size_t n = (size_t)p.m[k].R * p.m[k].C;
-        if (n > most) most = n;
+// A launch that waits for another costs 4 to 6 us, so what does not depend on
+// each other shares one (fp32, 256 tokens, 64 x 256, every gradient: by
+// products and sums 36 us, so 26).
+hipError_t launch_dense_back(const DenseBack &p, int dtype, hipStream_t s) {
+    hipError_t e;
+    if (dtype != 1 && (!p.rows || p.dx.plan.small)) {
+        e = launch_dense_back_f32(p, s);
+    } else {
+        e = launch_dense_sums(p.b, p.t, dtype, s);
+        if (e == hipSuccess && p.rows) e = launch_dense_product(p.dx, dtype, s);
+        if (e == hipSuccess && p.w.count)
+            e = dtype == 1 ? launch_dense_weights_mfma(p.w, s)
+                           : launch_dense_back_f32({false, {}, p.w, {}, {}}, s);
     }
+    if (e != hipSuccess) return e;
     const int per = 256 * (dtype == 1 ? 8 : 4);
-    const dim3 grid((unsigned)((most + per - 1) / per), p.count);
-    if (dtype == 1) hipLaunchKernelGGL((dense_weight_finish<uint16_t>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((dense_weight_finish<float>), grid, dim3(256), 0, s, p);
+    int rows = 0, weights = 0, sums = 0;
+    if (p.rows && p.dx.plan.splits > 1)
+        rows = (int)(((size_t)p.dx.M * p.dx.N + per - 1) / per);
+    if (p.w.count && p.w.splits > 1) {
+        size_t most = 0;
+        for (int k = 0; k < p.w.count; ++k) {
+            const size_t n = (size_t)p.w.m[k].R * p.w.m[k].C;
+            if (n > most) most = n;
+        }
+        weights = (int)((most + per - 1) / per) * p.w.count;
+    }
+    if (dense_sum_ranges(p.b.M) > 1)
+        for (int k = 0; k < p.b.count; ++k) sums += p.b.t[k].C / 64;
+    if (rows + weights + sums == 0) return hipSuccess;
+    const dim3 grid(rows + weights + sums);
+    if (dtype == 1)
+        hipLaunchKernelGGL((dense_joins<uint16_t>), grid, dim3(256), 0, s, p.dx, p.w, p.b, rows,
+                           weights);
+    else
+        hipLaunchKernelGGL((dense_joins<float>), grid, dim3(256), 0, s, p.dx, p.w, p.b, rows,
+                           weights);
     return hipGetLastError();
 }
