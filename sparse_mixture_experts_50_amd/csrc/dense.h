@@ -126,3 +126,7 @@ struct DenseBack {
 hipError_t launch_dense_back(const DenseBack &p, int dtype, hipStream_t s);
 // Products and sums of ranges, not yet joined (fp32, small tiles).
 hipError_t launch_dense_back_f32(const DenseBack &p, hipStream_t s);
+// The rows' gradient (small tiles; a split one's sums are left in its plane)
+// and launch_dense_sums, bf16.
+hipError_t launch_dense_dx_sums(const DenseRows &p, const DenseSums &b, const DenseTails &t,
+                                hipStream_t s);

@@ -281,16 +281,7 @@ __global__ __launch_bounds__(256, 4) void dense_back_f32(DenseBack p, int rows, 
     } else if ((block -= rows) < weights) {
         weight_tile(p.w, block, st);
     } else {
-        block -= weights;
-        const int ranges = dense_sum_ranges(p.b.M);
-        int k = 0;
-        for (;; ++k) {
-            const int n = (p.b.t[k].C + 127) / 128 * ranges;
-            if (block < n) break;
-            block -= n;
-        }
-        dense_parts::sum_columns<float>(p.b.t[k], p.b.M, block / ranges, block % ranges,
-                                        (float *)&st);
+        dense_parts::sums_and_tails<float>(p.b, p.t, block - weights, (float *)&st);
     }
 }
 
@@ -337,9 +328,7 @@ hipError_t launch_dense_back_f32(const DenseBack &p, hipStream_t s) {
     for (int k = 0; k < p.w.count; ++k)
         weights += (long long)((p.w.m[k].R + b - 1) / b) * ((p.w.m[k].C + b - 1) / b) * p.w.splits;
     const int rows = p.rows ? p.dx.plan.mt * p.dx.plan.nt * p.dx.plan.splits : 0;
-    int sums = 0;
-    for (int k = 0; k < p.b.count; ++k)
-        sums += (p.b.t[k].C + 127) / 128 * dense_sum_ranges(p.b.M);
+    const int sums = dense_parts::sums_blocks(p.b, p.t, 128);
     if (rows + weights + sums == 0) return hipSuccess;
     const dim3 grid((unsigned)(rows + weights + sums));
     auto run = [&](auto kernel) {

@@ -8,23 +8,10 @@ namespace {
 
 using namespace dense_parts;
 
-// Rows copied, and rows zeroed after them, by all blocks of a plane of the grid.
-__device__ void copy_tail(const DenseTails::Item &t) {
-    const size_t bytes = (size_t)t.row_bytes * t.rows, copied = (size_t)t.row_bytes * t.copied;
-    const size_t first = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
-    for (size_t b = (first * 256 + threadIdx.x) * 16; b < bytes;
-         b += (size_t)gridDim.x * gridDim.y * 256 * 16)
-        *(u32x4 *)((char *)t.dst + b) =
-            b < copied ? *(const u32x4 *)((const char *)t.src + b) : u32x4{0, 0, 0, 0};
-}
-
-// Block (c, r, k): columns c of range r of item k; items after the sums' are
-// tails.
 template <typename T>
 __global__ __launch_bounds__(256) void dense_sums(DenseSums p, DenseTails tails) {
     __shared__ float lds[SUMS_LDS / 4];
-    if ((int)blockIdx.z >= p.count) copy_tail(tails.t[blockIdx.z - p.count]);
-    else sum_columns<T>(p.t[blockIdx.z], p.M, blockIdx.x, blockIdx.y, lds);
+    sums_and_tails<T>(p, tails, blockIdx.x, lds);
 }
 
 // What products and sums of ranges left behind, added up: the rows' gradient
@@ -154,12 +141,8 @@ template <typename T, int EPI> void finish_as(const DenseRows &p, hipStream_t s)
 }  // namespace
 
 hipError_t launch_dense_sums(const DenseSums &p, const DenseTails &t, int dtype, hipStream_t s) {
-    if (p.count + t.count == 0) return hipSuccess;
-    int widest = 0;
-    for (int i = 0; i < p.count; ++i) widest = p.t[i].C > widest ? p.t[i].C : widest;
-    const int per = dtype == 1 ? 256 : 128;
-    const dim3 grid(p.count ? (widest + per - 1) / per : 32, p.count ? dense_sum_ranges(p.M) : 1,
-                    p.count + t.count);
+    const dim3 grid(sums_blocks(p, t, dtype == 1 ? 256 : 128));
+    if (grid.x == 0) return hipSuccess;
     if (dtype == 1) hipLaunchKernelGGL((dense_sums<uint16_t>), grid, dim3(256), 0, s, p, t);
     else hipLaunchKernelGGL((dense_sums<float>), grid, dim3(256), 0, s, p, t);
     return hipGetLastError();
@@ -194,16 +177,22 @@ hipError_t launch_dense_rows(const DenseRows &p, int dtype, hipStream_t s) {
     return launch_dense_finish(p, dtype, s);
 }
 
-// A launch that waits for another costs 4 to 6 us, so what does not depend on
-// each other shares one (fp32, 256 tokens, 64 x 256, every gradient: by
-// products and sums 36 us, so 26).
+// A launch that waits for another costs 4 to 6 us, so small parts that do not
+// depend on each other share one: the sums and the last rows with a product,
+// what is joined with each other, in fp32 both products (fp32, 256 tokens, 64 x
+// 256, all gradients 36 us apart, 26 so; bf16, 33 rows, 1024 to 2816: 27 and
+// 24; 1030 tokens, 1024 x 704: 54 and 49).
 hipError_t launch_dense_back(const DenseBack &p, int dtype, hipStream_t s) {
     hipError_t e;
     if (dtype != 1 && (!p.rows || p.dx.plan.small)) {
         e = launch_dense_back_f32(p, s);
     } else {
-        e = launch_dense_sums(p.b, p.t, dtype, s);
-        if (e == hipSuccess && p.rows) e = launch_dense_product(p.dx, dtype, s);
+        if (dtype == 1 && p.rows && p.dx.plan.small) {
+            e = launch_dense_dx_sums(p.dx, p.b, p.t, s);
+        } else {
+            e = launch_dense_sums(p.b, p.t, dtype, s);
+            if (e == hipSuccess && p.rows) e = launch_dense_product(p.dx, dtype, s);
+        }
         if (e == hipSuccess && p.w.count)
             e = dtype == 1 ? launch_dense_weights_mfma(p.w, s)
                            : launch_dense_back_f32({false, {}, p.w, {}, {}}, s);

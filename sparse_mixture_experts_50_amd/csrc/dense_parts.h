@@ -84,4 +84,40 @@ __device__ __forceinline__ void sum_columns(const DenseSums::Item &t, int M, int
     }
 }
 
+// Rows copied, and rows zeroed after them, by block `block` of TAIL_BLOCKS.
+constexpr int TAIL_BLOCKS = 8;
+__device__ __forceinline__ void copy_tail(const DenseTails::Item &t, int block) {
+    const size_t bytes = (size_t)t.row_bytes * t.rows, copied = (size_t)t.row_bytes * t.copied;
+    for (size_t b = ((size_t)block * 256 + threadIdx.x) * 16; b < bytes; b += TAIL_BLOCKS * 256 * 16)
+        *(u32x4 *)((char *)t.dst + b) =
+            b < copied ? *(const u32x4 *)((const char *)t.src + b) : u32x4{0, 0, 0, 0};
+}
+
+// Blocks of all items' sums, and of the tails.  per: columns of a block.
+inline int sums_blocks(const DenseSums &p, const DenseTails &t, int per) {
+    int n = t.count * TAIL_BLOCKS;
+    for (int k = 0; k < p.count; ++k) n += (p.t[k].C + per - 1) / per * dense_sum_ranges(p.M);
+    return n;
+}
+// Block `block` of them: the tails come first.
+template <typename T>
+__device__ __forceinline__ void sums_and_tails(const DenseSums &p, const DenseTails &t, int block,
+                                               float *lds) {
+    if (block < t.count * TAIL_BLOCKS) {
+        copy_tail(t.t[block / TAIL_BLOCKS], block % TAIL_BLOCKS);
+        return;
+    }
+    block -= t.count * TAIL_BLOCKS;
+    constexpr int per = 32 * Vec<T>::N;
+    const int ranges = dense_sum_ranges(p.M);
+    int k = 0;
+    for (; k + 1 < p.count; ++k) {
+        const int n = (p.t[k].C + per - 1) / per * ranges;
+        if (block < n) break;
+        block -= n;
+    }
+    const int columns = (p.t[k].C + per - 1) / per;
+    sum_columns<T>(p.t[k], p.M, block % columns, block / columns, lds);
+}
+
 }  // namespace dense_parts

@@ -43,6 +43,11 @@ __device__ __forceinline__ Tile tile_at(int L, int mt, int nt) {
     return t;
 }
 
+// mt::tile_of for block `block` of `blocks` (multiples of 8).
+__device__ __forceinline__ int tile_of(int r, int block, int blocks) {
+    return r * blocks + (block & 7) * (blocks >> 3) + (block >> 3);
+}
+
 // f(integral_constant<rb>)
 template <bool SMALL, typename F> __device__ __forceinline__ void by_height(int rb, F f) {
     if (SMALL) f(std::integral_constant<int, 2>{});
@@ -89,20 +94,25 @@ __device__ __forceinline__ floatx4 unpack4(u32x2 v) {
     return floatx4{bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
 }
 
+// The tile product of rows.
+template <int PANELS, bool BK, bool TWO, bool SMALL>
+using RowTiles = mt::Tiles<Shape<SMALL>::BM, Shape<SMALL>::BN / PANELS, 2, 2, PANELS, false, BK,
+                           TWO>;
+
+// The tiles of one block.  slot2: SMALL; scr: 128 TN vectors, large tiles that
+// leave no plane.
 template <int PANELS, bool BK, bool TWO, int EPI, int ACT, bool RES, mt::Stages KIND, bool SMALL>
-__global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void dense_rows(DenseRows p) {
-    constexpr int BM = Shape<SMALL>::BM, BN = Shape<SMALL>::BN / PANELS;
-    typedef mt::Tiles<BM, BN, 2, 2, PANELS, false, BK, TWO> P;
+__device__ __forceinline__ void rows_work(const DenseRows &p, int block, int blocks, u32x4 *slot0,
+                                          u32x4 *slot1, u32x4 *slot2, u32x4 *scr) {
+    constexpr int BN = Shape<SMALL>::BN / PANELS;
+    typedef RowTiles<PANELS, BK, TWO, SMALL> P;
     constexpr int TN = P::TN;
-    constexpr bool TURN = !SMALL && EPI != DENSE_PLANE;
-    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], slot2[SMALL ? P::STAGE : 1];
-    __shared__ u32x4 scr[TURN ? 4 * 32 * TN : 1];
     const int M = p.M, N = p.N, K = p.K, mt_ = p.plan.mt, nt = p.plan.nt;
     const int total = mt_ * nt * p.plan.splits;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / 2, wn = wave % 2;
     const int kt = (TWO ? 2 : 1) * K / mt::SK, per = p.plan.per;
-    int L = mt::tile_of(0);
+    int L = tile_of(0, block, blocks);
     if (L >= total) return;
     by_height<SMALL>(p.plan.rb, [&](auto height) __attribute__((always_inline)) {
         constexpr int RB = decltype(height)::value;
@@ -135,7 +145,7 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void dense_rows(DenseRow
         mt::wait_loads<0>();
         for (int r = 1;; ++r) {
             const int lane = mt::tile_lane();
-            L = mt::tile_of(r);
+            L = tile_of(r, block, blocks);
             const bool more = L < total;
             const Tile tn = more ? tile_at(L, mt_, nt) : t;
             const typename P::Source next = source(tn);
@@ -274,7 +284,8 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void dense_rows(DenseRow
                         }
                     const int lr = (wm * RB + i) * 16;
                     const size_t at = (size_t)row0 * N + c0;
-                    auto put = [&](void *out, const float (&v)[TN][4]) __attribute__((always_inline)) {
+                    auto put = [&](void *out, const float (&v)[TN][4])
+                                   __attribute__((always_inline)) {
                         if constexpr (SMALL) {
                             store_pieces<TN>(v, (bf16 *)out + row_of(i) * N + c0, lo, hi, lane);
                         } else {
@@ -303,22 +314,36 @@ __global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void dense_rows(DenseRow
 }
 
 template <int PANELS, bool BK, bool TWO, int EPI, int ACT, bool RES, mt::Stages KIND, bool SMALL>
+__global__ __launch_bounds__(256, Shape<SMALL>::BLOCKS) void dense_rows(DenseRows p) {
+    typedef RowTiles<PANELS, BK, TWO, SMALL> P;
+    constexpr bool TURN = !SMALL && EPI != DENSE_PLANE;
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], slot2[SMALL ? P::STAGE : 1];
+    __shared__ u32x4 scr[TURN ? 128 * P::TN : 1];
+    rows_work<PANELS, BK, TWO, EPI, ACT, RES, KIND, SMALL>(p, blockIdx.x, gridDim.x, slot0, slot1,
+                                                          slot2, scr);
+}
+
+template <int PANELS, bool BK, bool TWO, int EPI, int ACT, bool RES, mt::Stages KIND, bool SMALL>
 hipError_t launch_as(const DenseRows &p, hipStream_t s) {
     const long long tiles = (long long)p.plan.mt * p.plan.nt * p.plan.splits;
     const dim3 grid(mt::grid_for(tiles, Shape<SMALL>::BLOCKS));
-    hipLaunchKernelGGL((dense_rows<PANELS, BK, TWO, EPI, ACT, RES, KIND, SMALL>), grid, dim3(256), 0,
-                       s, p);
+    hipLaunchKernelGGL((dense_rows<PANELS, BK, TWO, EPI, ACT, RES, KIND, SMALL>), grid, dim3(256),
+                       0, s, p);
     return hipGetLastError();
 }
 
 // By the parity of a tile's stages, and the tiles' size.
 template <int PANELS, bool BK, bool TWO, int EPI, int ACT, bool RES>
-hipError_t launch_by_plan(const DenseRows &p, hipStream_t s) {
-    if (p.plan.small) return launch_as<PANELS, BK, TWO, EPI, ACT, RES, mt::EVEN, true>(p, s);
+hipError_t launch_large(const DenseRows &p, hipStream_t s) {
     if constexpr (!TWO)
         if (p.plan.per & 1)
             return launch_as<PANELS, BK, TWO, EPI, ACT, RES, mt::ODD, false>(p, s);
     return launch_as<PANELS, BK, TWO, EPI, ACT, RES, mt::EVEN, false>(p, s);
+}
+template <int PANELS, bool BK, bool TWO, int EPI, int ACT, bool RES>
+hipError_t launch_by_plan(const DenseRows &p, hipStream_t s) {
+    return p.plan.small ? launch_as<PANELS, BK, TWO, EPI, ACT, RES, mt::EVEN, true>(p, s)
+                        : launch_large<PANELS, BK, TWO, EPI, ACT, RES>(p, s);
 }
 
 // The forward's epilogue, with or without a residual.
