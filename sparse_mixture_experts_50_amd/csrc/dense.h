@@ -110,8 +110,8 @@ struct DenseSums {
 __host__ __device__ inline int dense_sum_ranges(int M) {
     return (M + MOE_DENSE_SUM_ROWS - 1) / MOE_DENSE_SUM_ROWS;
 }
-// The sums by ranges (one range: the results) and the tails.
-hipError_t launch_dense_sums(const DenseSums &p, const DenseTails &t, int dtype, hipStream_t s);
+// The sums by ranges (one range: the results) and the tails (bf16).
+hipError_t launch_dense_sums(const DenseSums &p, const DenseTails &t, hipStream_t s);
 
 // What a backward pass does once the pre-activations' gradients are there,
 // each part of which may be missing: the rows' gradient, the weights', the
@@ -124,7 +124,7 @@ struct DenseBack {
     DenseTails t;
 };
 hipError_t launch_dense_back(const DenseBack &p, int dtype, hipStream_t s);
-// Products and sums of ranges, not yet joined (fp32, small tiles).
+// Products and sums of ranges, not yet joined (fp32).
 hipError_t launch_dense_back_f32(const DenseBack &p, hipStream_t s);
 // The rows' gradient (small tiles; a split one's sums are left in its plane)
 // and launch_dense_sums, bf16.

@@ -8,10 +8,9 @@ namespace {
 
 using namespace dense_parts;
 
-template <typename T>
 __global__ __launch_bounds__(256) void dense_sums(DenseSums p, DenseTails tails) {
     __shared__ float lds[SUMS_LDS / 4];
-    sums_and_tails<T>(p, tails, blockIdx.x, lds);
+    sums_and_tails<uint16_t>(p, tails, blockIdx.x, lds);
 }
 
 // What products and sums of ranges left behind, added up: the rows' gradient
@@ -140,11 +139,10 @@ template <typename T, int EPI> void finish_as(const DenseRows &p, hipStream_t s)
 
 }  // namespace
 
-hipError_t launch_dense_sums(const DenseSums &p, const DenseTails &t, int dtype, hipStream_t s) {
-    const dim3 grid(sums_blocks(p, t, dtype == 1 ? 256 : 128));
-    if (grid.x == 0) return hipSuccess;
-    if (dtype == 1) hipLaunchKernelGGL((dense_sums<uint16_t>), grid, dim3(256), 0, s, p, t);
-    else hipLaunchKernelGGL((dense_sums<float>), grid, dim3(256), 0, s, p, t);
+hipError_t launch_dense_sums(const DenseSums &p, const DenseTails &t, hipStream_t s) {
+    const int blocks = sums_blocks(p, t, 256);
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(dense_sums, dim3(blocks), dim3(256), 0, s, p, t);
     return hipGetLastError();
 }
 
@@ -184,18 +182,16 @@ hipError_t launch_dense_rows(const DenseRows &p, int dtype, hipStream_t s) {
 // 24; 1030 tokens, 1024 x 704: 54 and 49).
 hipError_t launch_dense_back(const DenseBack &p, int dtype, hipStream_t s) {
     hipError_t e;
-    if (dtype != 1 && (!p.rows || p.dx.plan.small)) {
+    if (dtype != 1) {
         e = launch_dense_back_f32(p, s);
     } else {
-        if (dtype == 1 && p.rows && p.dx.plan.small) {
+        if (p.rows && p.dx.plan.small) {
             e = launch_dense_dx_sums(p.dx, p.b, p.t, s);
         } else {
-            e = launch_dense_sums(p.b, p.t, dtype, s);
+            e = launch_dense_sums(p.b, p.t, s);
             if (e == hipSuccess && p.rows) e = launch_dense_product(p.dx, dtype, s);
         }
-        if (e == hipSuccess && p.w.count)
-            e = dtype == 1 ? launch_dense_weights_mfma(p.w, s)
-                           : launch_dense_back_f32({false, {}, p.w, {}, {}}, s);
+        if (e == hipSuccess && p.w.count) e = launch_dense_weights_mfma(p.w, s);
     }
     if (e != hipSuccess) return e;
     const int per = 256 * (dtype == 1 ? 8 : 4);

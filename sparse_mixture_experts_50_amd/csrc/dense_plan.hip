@@ -71,26 +71,27 @@ DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, b
         p.small = true;
         p.mt = ceil_div(M, 64);
         p.nt = ceil_div(N, 64 / panels);
-        // (2048 x 2048 x 2048: 1024 tiles 155 us; 1021 x 1984 x 1024: 496
-        // tiles 46; 512 x 1024 x 2048: 128 tiles 56)
+        // (4096 x 4096 x 4096: 4096 tiles 962 us; 2048 x 2048 x 2048: 1024
+        // 127; 1021 x 1984 x 1024: 496 37; 512 x 1024 x 2048: 128 51, in four
+        // ranges 25)
         const int n = two ? 2 : 1;
-        const Cost c = {4, {1.7 * n, 2.65 * n, 4.0 * n, 4.7 * n}, 2.0};
-        double us = 0;
+        const Cost c = {4, {1.5 * n, 2.05 * n, 3.2 * n, 3.85 * n}, 2.0};
+        double us = 0, big = 0;
         p.splits = best_splits(stages, 16, false, us, p.per, [&](int s, int len) {
             return product_us(c, (long long)p.mt * p.nt * s, len) + plane_us(elements, s);
         });
-        if (two || N < 128 / panels) return p;
-        // (4096 x 4096 x 4096: 1074 us, with the small tiles 1199; 2048 x
-        // 2048 x 2048 151; 1021 x 1984 x 1024 77)
-        const Cost b = {2, {4.65, 8.3}, 3.0};
-        const int mt = ceil_div(M, 128), nt = ceil_div(N, 128 / panels);
-        if (product_us(b, (long long)mt * nt, stages) < us) {
-            p.small = false;
-            p.mt = mt;
-            p.nt = nt;
-            p.splits = 1;
-            p.per = stages;
-        }
+        if (N < 128 / panels) return p;
+        // (of those: 944 us, 127, 64, 122 and 40)
+        const Cost l = {2, {3.7 * n, 7.25 * n}, 3.0};
+        DensePlan b = p;
+        b.small = false;
+        b.mt = ceil_div(M, 128);
+        b.nt = ceil_div(N, 128 / panels);
+        b.splits = best_splits(stages, 16, false, big, b.per, [&](int s, int len) {
+            return product_us(l, (long long)b.mt * b.nt * s, len) + plane_us(elements, s);
+        });
+        // (as good: the small ones share launches)
+        if (big < 0.98 * us) return b;
         return p;
     }
     const int all = two ? 2 * stages : stages;
@@ -150,7 +151,15 @@ size_t dense_weights_plan(DenseWeights &p, int dtype) {
     int per = 0, per_big = 0;
     if (dtype != 1) {
         p.small = true;
-        p.splits = cut(64, Cost{4, {1.7, 2.65, 4.0, 4.7}, 2.0}, us, p.per);
+        // (4096 rows, 4096 x 4096: 1047 us, the large tiles 975; 6836, three of
+        // 960 x 2240: 1575 tiles 790, in four ranges 727, the large tiles 742)
+        p.splits = cut(64, Cost{4, {1.6, 2.2, 3.4, 4.05}, 2.0}, us, p.per);
+        const int s = cut(128, Cost{2, {3.9, 7.55}, 3.0}, us_big, per_big);
+        if (us_big < 0.98 * us) {
+            p.small = false;
+            p.splits = s;
+            p.per = per_big;
+        }
     } else {
         p.small = true;
         // (4096 rows, 1024 x 1024: 64 tiles 43 us, in four ranges 23; 2048 x

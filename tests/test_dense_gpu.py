@@ -84,7 +84,11 @@ LARGE = [("bf16", *c) for c in [
     (1012, 5504, 64, "geglu"), (256, 4288, 4992, "swiglu")]] + [
     ("f32", *c) for c in [
         (2562, 2944, 256, "gelu"), (2984, 2432, 64, "none"),
-        (4531, 768, 128, "swiglu"), (1336, 2112, 64, "geglu")]]
+        (4531, 768, 128, "swiglu"), (1336, 2112, 64, "geglu"),
+        (1910, 4288, 128, "none"), (4216, 1600, 64, "gelu"),
+        (69, 6848, 3200, "none"), (68, 4928, 5760, "silu"),
+        (5075, 768, 128, "swiglu"), (362, 8960, 64, "geglu"),
+        (65, 4224, 2560, "swiglu"), (67, 6400, 2240, "geglu")]]
 
 
 @pytest.mark.parametrize("dtype,M,N,K,act",
@@ -126,7 +130,14 @@ LARGE_GRAD = [("bf16", *c) for c in [
     (2282, 3648, 64, "gelu"), (558, 7808, 704, "swiglu"),
     (2670, 2112, 128, "geglu"), (1012, 5504, 64, "swiglu")]] + [
     ("f32", 993, 64, 6208, "none"), ("f32", 2562, 2944, 256, "silu"),
-    ("f32", 1336, 2112, 64, "swiglu")]
+    ("f32", 1336, 2112, 64, "swiglu")] + [("f32", *c) for c in [
+        (1818, 128, 4160, "none"), (1601, 64, 4032, "gelu"),
+        (74, 4416, 8640, "none"), (66, 3648, 6976, "silu"),
+        (965, 128, 7360, "swiglu"), (1962, 64, 10112, "geglu"),
+        (77, 1088, 6976, "swiglu"), (73, 2880, 4224, "geglu"),
+        (65, 1280, 5440, "none"), (2437, 1408, 768, "silu"),
+        (89, 1088, 3520, "swiglu"), (4951, 2432, 128, "geglu"),
+        (375, 2048, 6848, "none")]]
 
 
 @pytest.mark.parametrize("dtype,M,N,K,act",
