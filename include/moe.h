@@ -1,6 +1,7 @@
 /*
  * moe.h -- C ABI of the MI355X (gfx950) sparse Mixture-of-Experts FFN layer:
- * forward, gradient, and what a training step needs around them.
+ * forward, gradient, and what a training step needs around them; dense linear
+ * and feed-forward layers beside it, and the optimizer's step.
  *
  * The layer (sources are the pages' titles and sections):
  *   1. router logits  l[t,e] = x[t,:] . Wr[e,:] + add[e] - b[e], softmax

@@ -1,5 +1,6 @@
 """Sparse Mixture-of-Experts FFN layer for MI355X (gfx950): forward,
-gradient, and the training operators around them.
+gradient, and the training operators around them; dense linear and
+feed-forward layers, and AdamW.
 
 The layer runs in hand-written HIP kernels behind the C ABI of
 include/moe.h (libmoe.so, built in-tree).  This package is the thin torch
@@ -26,7 +27,6 @@ from .layer import (Grads, MoeLayer, RouterWeights, Routing,  # noqa: F401
                     moe_router_grad, moe_router_grad_workspace_size,
                     moe_router_topk,
                     moe_workspace_size)
-
 from .optim import AdamW  # noqa: F401
 
 __version__ = "0.1.0"

@@ -24,10 +24,14 @@
 // the root is correctly rounded: the codes are then a function of the inputs
 // that plain elementary operations reproduce bit for bit.
 //
-// Bound by HBM: every operand is read and written once, by 32 KB and more of
-// loads in flight per CU; chunks of 16384 elements of all tensors (fewer where
-// that leaves blocks without work) are dealt round-robin to the blocks, as the
-// clipping's are.
+// Bound by HBM: every operand is read and written once, none comes back soon
+// enough for a cache (non-temporal), and eight waves a SIMD hide what stands
+// between a load and its store.  0.18 G bf16 elements with master copies (28
+// bytes each) 0.99 ms, 5.1 TB/s; 0.58 G with 8-bit states (10.1 bytes) 1.25 ms,
+// 4.7 TB/s, with four waves 1.47, by way of the caches 1.32, with the codes'
+// rounding by integer steps instead of the conversion's 0.04 more.  Chunks of
+// 16384 elements of all tensors (fewer where that leaves blocks without work)
+// are dealt round-robin to the blocks, as the clipping's are.
 #include "adamw.h"
 
 namespace {
@@ -51,7 +55,8 @@ __device__ __forceinline__ void load(float (&x)[V], const void *p, bool f32, lon
         if (f32) {
 #pragma unroll
             for (int i = 0; i < V; i += 4) {
-                const floatx4 q = __builtin_nontemporal_load((const floatx4 *)((const float *)p + e0 + i));
+                const floatx4 q =
+                    __builtin_nontemporal_load((const floatx4 *)((const float *)p + e0 + i));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[i + e] = q[e];
             }

@@ -94,7 +94,8 @@ LinearLayout linear_layout(const moe_linear_desc *d) {
         DenseWeights w = {};
         w.M = d->M;
         w.count = k;
-        for (int i = 0; i < k; ++i) w.m[i] = {nullptr, nullptr, nullptr, nullptr, nullptr, d->N, d->K};
+        for (int i = 0; i < k; ++i)
+            w.m[i] = {nullptr, nullptr, nullptr, nullptr, nullptr, d->N, d->K};
         planes = most(planes, dense_weights_plan(w, d->dtype) * 4);
     }
     L.w_plane = take(planes);

@@ -127,12 +127,18 @@ template <typename T, int EPI> void finish_as(const DenseRows &p, hipStream_t s)
     const long long vectors = (long long)p.M * p.N / Vec<T>::N;
     const dim3 grid((unsigned)((vectors + 255) / 256)), block(256);
     switch (p.act) {
-    case ACT_GELU: hipLaunchKernelGGL((dense_finish<T, EPI, ACT_GELU>), grid, block, 0, s, p); break;
-    case ACT_SILU: hipLaunchKernelGGL((dense_finish<T, EPI, ACT_SILU>), grid, block, 0, s, p); break;
+    case ACT_GELU:
+        hipLaunchKernelGGL((dense_finish<T, EPI, ACT_GELU>), grid, block, 0, s, p);
+        break;
+    case ACT_SILU:
+        hipLaunchKernelGGL((dense_finish<T, EPI, ACT_SILU>), grid, block, 0, s, p);
+        break;
     case ACT_SWIGLU:
         hipLaunchKernelGGL((dense_finish<T, EPI, ACT_SWIGLU>), grid, block, 0, s, p);
         break;
-    case ACT_GEGLU: hipLaunchKernelGGL((dense_finish<T, EPI, ACT_GEGLU>), grid, block, 0, s, p); break;
+    case ACT_GEGLU:
+        hipLaunchKernelGGL((dense_finish<T, EPI, ACT_GEGLU>), grid, block, 0, s, p);
+        break;
     default: hipLaunchKernelGGL((dense_finish<T, EPI, ACT_NONE>), grid, block, 0, s, p);
     }
 }

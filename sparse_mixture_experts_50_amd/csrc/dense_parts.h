@@ -88,7 +88,8 @@ __device__ __forceinline__ void sum_columns(const DenseSums::Item &t, int M, int
 constexpr int TAIL_BLOCKS = 8;
 __device__ __forceinline__ void copy_tail(const DenseTails::Item &t, int block) {
     const size_t bytes = (size_t)t.row_bytes * t.rows, copied = (size_t)t.row_bytes * t.copied;
-    for (size_t b = ((size_t)block * 256 + threadIdx.x) * 16; b < bytes; b += TAIL_BLOCKS * 256 * 16)
+    for (size_t b = ((size_t)block * 256 + threadIdx.x) * 16; b < bytes;
+         b += TAIL_BLOCKS * 256 * 16)
         *(u32x4 *)((char *)t.dst + b) =
             b < copied ? *(const u32x4 *)((const char *)t.src + b) : u32x4{0, 0, 0, 0};
 }

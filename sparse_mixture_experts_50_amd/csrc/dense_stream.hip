@@ -153,8 +153,8 @@ __global__ __launch_bounds__(256, 2) void dense_stream(DenseRows p) {
             const int row = wave + 4 * i;
             uint32_t c = (uint32_t)(lane ^ (row & 7)) * 16;
             c *= c < left;
-            if constexpr (J < MB) dma16<false>(base + (size_t)min(J * 16 + row, M - 1) * row_bytes + c, to + 4 * i * (CB / 16));
-            else dma16<true>(base + (size_t)row * row_bytes + c, to + 4 * i * (CB / 16));
+            const int m = J < MB ? min(J * 16 + row, M - 1) : row;
+            dma16<(J >= MB)>(base + (size_t)m * row_bytes + c, to + 4 * i * (CB / 16));
         }
         if constexpr (J == STAGES - 1) {
             if (++lr == trips * R) {
@@ -203,14 +203,15 @@ __global__ __launch_bounds__(256, 2) void dense_stream(DenseRows p) {
 #pragma unroll
             for (int g = 0; g < P; ++g) acc[m][g] = floatx4{0.f, 0.f, 0.f, 0.f};
         for (int t = 0; t < trips; ++t) {
-            each_of(std::make_integer_sequence<int, R * STAGES>{}, [&](auto at) __attribute__((always_inline)) {
+            auto next = [&](auto at) __attribute__((always_inline)) {
                 if constexpr (decltype(at)::value % STAGES == 0) {
                     // the waves share the range's steps of 64 bytes
                     const int left = (int)row_bytes - (t * R + decltype(at)::value / STAGES) * CB;
                     steps = max(min(left, CB), 0) / 64;
                 }
                 stage(at);
-            });
+            };
+            each_of(std::make_integer_sequence<int, R * STAGES>{}, next);
         }
 #pragma unroll
         for (int m = 0; m < MB; ++m) {

@@ -8,6 +8,13 @@
 // the first row's and are stored over it with the same bits; columns past the
 // end are not stored.  So no operand is read out of range and, in the large
 // tiles, no store is a branch.
+//
+// Bound by the matrix cores, and in long products by the power that they draw:
+// 4096 x 4096 to 14336 gated 653 us, 1.47 PFLOP/s, cores busy 75 % at 1.71 GHz;
+// the same with the gradient's epilogue 721.  Short K: 8192 x 2048 to 7168 with
+// a residual 220, 1.09 PFLOP/s: 896 tiles are 3.5 rounds of the CUs, and while a
+// tile's epilogue reads and writes 128 KB its matrix cores wait.  The first of
+// the residual fetched ahead of the product: 224.
 #pragma once
 
 #include "act.h"

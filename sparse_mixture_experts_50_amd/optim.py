@@ -20,7 +20,8 @@ class AdamW:
     """AdamW with decoupled weight decay over contiguous float32 / bfloat16
     tensors of one GPU, updated in place.
 
-    ``weight_decay``: one number, or one for each parameter.
+    ``lr``, ``betas``, ``eps``: attributes that may change between steps.
+    ``weight_decay``: one number, or one for each parameter; fixed.
     ``state_bits``: 32 (float32 moments) or 8 (E4M3 codes in blocks of 32
     that share a power of two; the second moment as its square root).
     ``master``: keep a float32 copy of every bfloat16 parameter, on which the
@@ -34,7 +35,8 @@ class AdamW:
     The states are the lists ``m`` and ``v`` (float32, or float8_e4m3fn with
     ``m_scale`` and ``v_scale``: uint8 exponents + 127, one per block) and
     ``master`` (None where there is no copy); ``steps`` counts the steps done.
-    A loaded checkpoint is copied into them."""
+    A loaded checkpoint is copied into them, and parameters that are loaded
+    into their master copies too."""
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float,
                  betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
