@@ -18,10 +18,15 @@ enum DenseEpilogue {
 
 // How a product is cut: tiles of 32 * rb rows (small: 64) by 256 (small: 128)
 // columns, K in `splits` ranges of `per` stages.  stream: the kernel for few
-// rows, which cuts by itself.
+// rows, which cuts by itself.  The last nt2 columns of tiles may be lower ones
+// (rb2, mt2 of them a column), which come after the others.
 struct DensePlan {
     bool small, stream;
     int rb, mt, nt, splits, per;
+    int rb2, mt2, nt2;
+    __host__ __device__ long long tiles() const {
+        return (long long)mt * (nt - nt2) * splits + (long long)mt2 * nt2;
+    }
 };
 
 // out[M][N] = A B over K: A [M][K]; B [N][K] (transposed product), or [K][N]

@@ -39,7 +39,7 @@ hipError_t launch_dense_dx_mfma(const DenseRows &p, hipStream_t s) {
 
 hipError_t launch_dense_dx_sums(const DenseRows &p, const DenseSums &b, const DenseTails &t,
                                 hipStream_t s) {
-    const int rows = mt::grid_for((long long)p.plan.mt * p.plan.nt * p.plan.splits, 2);
+    const int rows = mt::grid_for(p.plan.tiles(), 2);
     const dim3 grid(rows + dense_parts::sums_blocks(b, t, 256));
     auto run = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, p, b, t, rows);

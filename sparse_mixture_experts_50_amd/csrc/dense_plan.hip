@@ -22,6 +22,19 @@ double product_us(const Cost &c, long long units, int per) {
     return 2.5 + rounds * (c.stage[c.occupancy - 1] * per + c.tile) +
            (rest ? c.stage[rest - 1] * per + c.tile : 0.0);
 }
+// The same for one place a CU, where the last nt2 columns of tiles are lower:
+// us1 a tile of mt * nt1, then us2 of mt2 * nt2, first by those with one less.
+double two_heights_us(double us1, long long tiles1, double us2, long long tiles2) {
+    const long long r1 = tiles1 / CUS, rest1 = tiles1 % CUS;
+    const long long r2 = tiles2 / CUS, rest2 = tiles2 % CUS;
+    double most = 0;
+    for (int o = 0; o < CUS; ++o) {
+        const long long place = (o - rest1 + CUS) % CUS, n2 = r2 + (place < rest2);
+        const double us = (r1 + (o < rest1)) * us1 + n2 * us2 + (n2 && r1 + rest1 ? 2.0 : 0.0);
+        most = us > most ? us : most;
+    }
+    return 2.5 + most;
+}
 // Planes of fp32 sums, written and read, and the launch that joins them.
 double plane_us(double elements, int splits) {
     return splits > 1 ? 6.0 + elements * splits * 8.0 / 7e6 : 0.0;
@@ -127,7 +140,27 @@ DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, b
             return product_us(c, tiles * s, len) + plane_us(elements, s);
         });
     }
-    return big <= us ? b : a;
+    if (big > us) return a;
+    if (b.splits == 1 && b.rb == 8) {
+        // lower tiles in the last columns, where they leave less of the last
+        // round empty (8192 x 7168 x 2048 with a residual, 896 tiles: 227 us,
+        // the last 128 as 256 of half the height 218; 5100 x 4480 x 1024: 60
+        // and 54)
+        auto tile_us = [&](int rb) { return 1.4 * (0.3 + 0.7 * rb / 8) * all + 6.0; };
+        const DensePlan whole = b;
+        for (int n = 1; n <= whole.nt && n <= 32; ++n) {
+            const int rb2 = 4, mt2 = ceil_div(M, 32 * rb2);
+            const double t = two_heights_us(tile_us(whole.rb), (long long)whole.mt * (whole.nt - n),
+                                            tile_us(rb2), (long long)mt2 * n);
+            if (t < big * 0.97) {
+                big = t;
+                b.rb2 = rb2;
+                b.mt2 = mt2;
+                b.nt2 = n;
+            }
+        }
+    }
+    return b;
 }
 
 size_t dense_weights_plan(DenseWeights &p, int dtype) {

@@ -81,7 +81,12 @@ LARGE = [("bf16", *c) for c in [
     (564, 8128, 2176, "geglu"), (558, 7808, 704, "swiglu"),
     (132, 5632, 3712, "geglu"), (822, 7936, 256, "geglu"),
     (849, 5952, 320, "swiglu"), (2670, 2112, 128, "swiglu"),
-    (1012, 5504, 64, "geglu"), (256, 4288, 4992, "swiglu")]] + [
+    (1012, 5504, 64, "geglu"), (256, 4288, 4992, "swiglu"),
+    # (lower tiles in the last columns, or in all)
+    (3308, 6336, 384, "none"), (2680, 7744, 448, "gelu"),
+    (920, 6720, 2368, "silu"), (4981, 1216, 2176, "none"),
+    (1177, 8832, 384, "swiglu"), (1881, 5504, 448, "geglu"),
+    (1975, 1664, 2240, "swiglu")]] + [
     ("f32", *c) for c in [
         (2562, 2944, 256, "gelu"), (2984, 2432, 64, "none"),
         (4531, 768, 128, "swiglu"), (1336, 2112, 64, "geglu"),
@@ -128,7 +133,12 @@ LARGE_GRAD = [("bf16", *c) for c in [
     (4242, 1728, 1600, "none"), (4137, 960, 1408, "swiglu"),
     (1110, 7296, 512, "gelu"), (1095, 9088, 320, "silu"),
     (2282, 3648, 64, "gelu"), (558, 7808, 704, "swiglu"),
-    (2670, 2112, 128, "geglu"), (1012, 5504, 64, "swiglu")]] + [
+    (2670, 2112, 128, "geglu"), (1012, 5504, 64, "swiglu"),
+    # (lower tiles in the last columns, or in all)
+    (1881, 5504, 448, "swiglu"), (2680, 7744, 448, "silu"),
+    (2875, 384, 7296, "none"), (6583, 448, 3136, "none"),
+    (6209, 2368, 960, "none"), (2197, 192, 9600, "swiglu"),
+    (2745, 1088, 2368, "geglu")]] + [
     ("f32", 993, 64, 6208, "none"), ("f32", 2562, 2944, 256, "silu"),
     ("f32", 1336, 2112, 64, "swiglu")] + [("f32", *c) for c in [
         (1818, 128, 4160, "none"), (1601, 64, 4032, "gelu"),
@@ -189,7 +199,8 @@ DENSE = [
 ]
 # (every product on its large tiles, the gradient of h among them)
 DENSE_LARGE = [(2048, 1024, 4096, "silu"), (1500, 832, 7040, "swiglu"),
-               (4100, 704, 2112, "geglu")]
+               (4100, 704, 2112, "geglu"), (2875, 384, 7296, "silu"),
+               (6583, 448, 3136, "gelu")]
 OF_BLOCK = ("x", "w1", "w2", "w3", "b1", "b2", "b3")
 
 
