@@ -219,7 +219,9 @@ def guarded(rows, cols, dtype, fill=7.0):
 @pytest.mark.parametrize("M,N,K,act", [
     (1, 64, 64, "none"), (37, 192, 128, "swiglu"), (50, 64, 320, "gelu"),
     (70, 320, 64, "geglu"), (300, 192, 512, "silu"),
-    (2049, 2112, 128, "none"), (1100, 4160, 192, "swiglu")])
+    (2049, 2112, 128, "none"), (1100, 4160, 192, "swiglu"),
+    (2680, 7744, 448, "none"), (1177, 8832, 384, "swiglu"),
+    (2437, 1408, 768, "silu"), (73, 2880, 4224, "geglu")])
 def test_neighbouring_memory_stays(dtype, M, N, K, act):
     """Results lie between bands of other data, which stay as they were; the
     same call gives the same bits again."""
@@ -256,7 +258,8 @@ def test_neighbouring_memory_stays(dtype, M, N, K, act):
 
 @pytest.mark.parametrize("M,N,K", [(1, 128, 64), (33, 192, 128),
                                    (70, 192, 256), (300, 4096, 512),
-                                   (1300, 4160, 192)])
+                                   (1300, 4160, 192), (2680, 7744, 448),
+                                   (69, 6848, 3200)])
 def test_values_that_are_not_finite_stay_in_their_row(M, N, K):
     """A NaN or infinity of one row of x or of the residual reaches that row,
     of one row of the weights that column; in memory after the tensors it
@@ -298,15 +301,17 @@ def test_values_that_are_not_finite_stay_in_their_row(M, N, K):
         assert torch.equal(y, clean)
 
 
-@pytest.mark.parametrize("T", [1, 33, 70, 321])
-def test_gradients_with_nan_after_the_tensors(T):
+@pytest.mark.parametrize("T,d,F", [(1, 128, 320), (33, 128, 320),
+                                   (70, 128, 320), (321, 128, 320),
+                                   (1287, 1088, 3520), (2437, 768, 1408)])
+def test_gradients_with_nan_after_the_tensors(T, d, F):
     """Sums over rows end with the last row, whatever lies after it."""
     for name, dtype in (("bf16", BF), ("f32", F32)):
-        t, layer = dense_case(name, T, 128, 320, "swiglu", True)
+        t, layer = dense_case(name, T, d, F, "swiglu", True)
         want = {n: g.clone() for n, g in layer.backward(
             t["x"], t["dy"]).as_dict().items()}
-        x = torch.cat([t["x"], nan_like((300, 128), dtype)])[:T]
-        dy = torch.cat([t["dy"], nan_like((300, 128), dtype)])[:T]
+        x = torch.cat([t["x"], nan_like((300, d), dtype)])[:T]
+        dy = torch.cat([t["dy"], nan_like((300, d), dtype)])[:T]
         layer._ws.fill_(0xFF)
         got = layer.backward(x, dy).as_dict()
         for n in want:
@@ -398,3 +403,29 @@ def test_offsets_over_31_bits():
         off = float((getattr(gr, n).double() - total[n]).norm() /
                     total[n].norm())
         assert off < 2 * half, n
+
+
+@pytest.mark.parametrize("name", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,F,act", [
+    (1, 64, 64, "gelu"), (33, 320, 192, "swiglu"), (200, 320, 256, "silu"),
+    (1030, 1024, 704, "geglu"), (2875, 384, 7296, "silu")])
+def test_first_calls_inside_a_capture(name, T, d, F, act):
+    """A layer whose first calls are captured, replayed with new inputs: the
+    bits of an eager layer, with eager work in between."""
+    t, layer = dense_case(name, T, d, F, act, True)
+    other = dense_case(name, T, d, F, act, True)[1]
+    x, dy = t["x"].clone(), t["dy"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer.forward(x, residual=x)
+        g = layer.backward(x, dy, residual=True)
+    for _ in range(3):
+        x.normal_()
+        dy.normal_()
+        graph.replay()
+        want = other.forward(x, residual=x)
+        grads = other.backward(x, dy, residual=True).as_dict()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        for n in grads:
+            assert torch.equal(getattr(g, n), grads[n]), n
