@@ -87,7 +87,7 @@ struct DenseWeights {
 };
 // Fills in small, splits, per and offset; returns the planes' elements.
 size_t dense_weights_plan(DenseWeights &p, int dtype);
-hipError_t launch_dense_weights_mfma(const DenseWeights &p, hipStream_t s);
+hipError_t launch_dense_weights_mfma(const DenseWeights &p, hipStream_t s);   // large tiles
 
 // Rows copied and rows zeroed, up to five items: dst[0, copied) = src, then
 // zeros up to rows.
@@ -129,6 +129,10 @@ struct DenseBack {
     DenseTails t;
 };
 hipError_t launch_dense_back(const DenseBack &p, int dtype, hipStream_t s);
+// The weights' gradients in small tiles, and what a launch before left to join
+// (blocks of the rows' gradient, and of the column sums), bf16.
+hipError_t launch_dense_weights_joins(const DenseWeights &p, const DenseRows &dx,
+                                      const DenseSums &b, int rows, int sums, hipStream_t s);
 // Products and sums of ranges, not yet joined (fp32).
 hipError_t launch_dense_back_f32(const DenseBack &p, hipStream_t s);
 // The rows' gradient (small tiles; a split one's sums are left in its plane)

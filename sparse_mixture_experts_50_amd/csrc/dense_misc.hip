@@ -13,56 +13,11 @@ __global__ __launch_bounds__(256) void dense_sums(DenseSums p, DenseTails tails)
     sums_and_tails<uint16_t>(p, tails, blockIdx.x, lds);
 }
 
-// What products and sums of ranges left behind, added up: the rows' gradient
-// (blocks up to `rows`), the weights' (up to `weights`, as many for each
-// matrix), the column sums (64 columns by four ranges at a time).
 template <typename T>
 __global__ __launch_bounds__(256) void dense_joins(DenseRows p, DenseWeights w, DenseSums b,
                                                    int rows, int weights) {
-    constexpr int N = Vec<T>::N;
-    int block = blockIdx.x;
-    if (block < rows) {
-        const size_t plane = (size_t)p.M * p.N, at = ((size_t)block * 256 + threadIdx.x) * N;
-        if (at >= plane) return;
-        Vec<T> s, a;
-        s.clear();
-#pragma unroll 4
-        for (int i = 0; i < p.plan.splits; ++i) s.add(p.plane + i * plane + at);
-        if (p.res) {
-            a.load((const T *)p.res + at);
-#pragma unroll
-            for (int i = 0; i < N; ++i) s.v[i] += a.v[i];
-        }
-        s.store((T *)p.y + at);
-        return;
-    }
-    block -= rows;
-    if (block < weights) {
-        const int each = weights / w.count, k = block / each;
-        const DenseMat &m = w.m[k];
-        const size_t size = (size_t)m.R * m.C;
-        const size_t at = ((size_t)(block - k * each) * 256 + threadIdx.x) * N;
-        if (at >= size) return;
-        Vec<T> s;
-        s.clear();
-#pragma unroll 4
-        for (int i = 0; i < w.splits; ++i) s.add(w.plane + w.offset[k] + i * size + at);
-        s.store((T *)m.out + at);
-        return;
-    }
-    block -= weights;
-    __shared__ float red[4][64];
-    int k = 0;
-    while (block >= b.t[k].C / 64) block -= b.t[k++].C / 64;
-    const DenseSums::Item &t = b.t[k];
-    const int c = block * 64 + (threadIdx.x & 63), lane = threadIdx.x >> 6;
-    float s = 0.0f;
-    for (int r = lane; r < dense_sum_ranges(b.M); r += 4) s += t.part[(size_t)r * t.C + c];
-    red[lane][threadIdx.x & 63] = s;
-    __syncthreads();
-    if (lane) return;
-    s = (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
-    put((T *)t.out + c, s);
+    __shared__ float lds[256];
+    join<T>(p, w, b, blockIdx.x, rows, weights, lds);
 }
 
 // y = res + act(sums + bias), or h, dz, du: one vector of a row a thread.
@@ -182,24 +137,12 @@ hipError_t launch_dense_rows(const DenseRows &p, int dtype, hipStream_t s) {
 }
 
 // A launch that waits for another costs 4 to 6 us, so small parts that do not
-// depend on each other share one: the sums and the last rows with a product,
-// what is joined with each other, in fp32 both products (fp32, 256 tokens, 64 x
-// 256, all gradients 36 us apart, 26 so; bf16, 33 rows, 1024 to 2816: 27 and
-// 24; 1030 tokens, 1024 x 704: 54 and 49).
+// depend on each other share one: the sums and the last rows with the rows'
+// gradient, what that leaves to join with the weights', in fp32 both products
+// (fp32, 256 tokens, 64 x 256, all gradients 36 us apart, 26 so; bf16, 33 rows,
+// 1024 to 2816: 27 and 20; 1030 tokens, 1024 x 704: 54 and 46).
 hipError_t launch_dense_back(const DenseBack &p, int dtype, hipStream_t s) {
-    hipError_t e;
-    if (dtype != 1) {
-        e = launch_dense_back_f32(p, s);
-    } else {
-        if (p.rows && p.dx.plan.small) {
-            e = launch_dense_dx_sums(p.dx, p.b, p.t, s);
-        } else {
-            e = launch_dense_sums(p.b, p.t, s);
-            if (e == hipSuccess && p.rows) e = launch_dense_product(p.dx, dtype, s);
-        }
-        if (e == hipSuccess && p.w.count) e = launch_dense_weights_mfma(p.w, s);
-    }
-    if (e != hipSuccess) return e;
+    // what is left to join
     const int per = 256 * (dtype == 1 ? 8 : 4);
     int rows = 0, weights = 0, sums = 0;
     if (p.rows && p.dx.plan.splits > 1)
@@ -214,7 +157,24 @@ hipError_t launch_dense_back(const DenseBack &p, int dtype, hipStream_t s) {
     }
     if (dense_sum_ranges(p.b.M) > 1)
         for (int k = 0; k < p.b.count; ++k) sums += p.b.t[k].C / 64;
-    if (rows + weights + sums == 0) return hipSuccess;
+    hipError_t e;
+    if (dtype != 1) {
+        e = launch_dense_back_f32(p, s);
+    } else {
+        if (p.rows && p.dx.plan.small) {
+            e = launch_dense_dx_sums(p.dx, p.b, p.t, s);
+        } else {
+            e = launch_dense_sums(p.b, p.t, s);
+            if (e == hipSuccess && p.rows) e = launch_dense_product(p.dx, dtype, s);
+        }
+        if (e == hipSuccess && p.w.count && p.w.small) {
+            e = launch_dense_weights_joins(p.w, p.dx, p.b, rows, sums, s);
+            rows = sums = 0;
+        } else if (e == hipSuccess && p.w.count) {
+            e = launch_dense_weights_mfma(p.w, s);
+        }
+    }
+    if (e != hipSuccess || rows + weights + sums == 0) return e;
     const dim3 grid(rows + weights + sums);
     if (dtype == 1)
         hipLaunchKernelGGL((dense_joins<uint16_t>), grid, dim3(256), 0, s, p.dx, p.w, p.b, rows,

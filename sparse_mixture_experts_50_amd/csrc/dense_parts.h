@@ -84,6 +84,57 @@ __device__ __forceinline__ void sum_columns(const DenseSums::Item &t, int M, int
     }
 }
 
+// What products and sums of ranges left behind, added up: the rows' gradient
+// (blocks up to `rows`), the weights' (up to `weights` more, as many for each
+// matrix), the column sums (64 columns by four ranges at a time; 256 floats of
+// LDS).
+template <typename T>
+__device__ __forceinline__ void join(const DenseRows &p, const DenseWeights &w,
+                                     const DenseSums &b, int block, int rows, int weights,
+                                     float *lds) {
+    constexpr int N = Vec<T>::N;
+    if (block < rows) {
+        const size_t plane = (size_t)p.M * p.N, at = ((size_t)block * 256 + threadIdx.x) * N;
+        if (at >= plane) return;
+        Vec<T> s, a;
+        s.clear();
+#pragma unroll 4
+        for (int i = 0; i < p.plan.splits; ++i) s.add(p.plane + i * plane + at);
+        if (p.res) {
+            a.load((const T *)p.res + at);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s.v[i] += a.v[i];
+        }
+        s.store((T *)p.y + at);
+        return;
+    }
+    block -= rows;
+    if (block < weights) {
+        const int each = weights / w.count, k = block / each;
+        const DenseMat &m = w.m[k];
+        const size_t size = (size_t)m.R * m.C;
+        const size_t at = ((size_t)(block - k * each) * 256 + threadIdx.x) * N;
+        if (at >= size) return;
+        Vec<T> s;
+        s.clear();
+#pragma unroll 4
+        for (int i = 0; i < w.splits; ++i) s.add(w.plane + w.offset[k] + i * size + at);
+        s.store((T *)m.out + at);
+        return;
+    }
+    block -= weights;
+    int k = 0;
+    for (; k + 1 < b.count && block >= b.t[k].C / 64; ++k) block -= b.t[k].C / 64;
+    const DenseSums::Item &t = b.t[k];
+    const int in = threadIdx.x & 63, c = block * 64 + in, lane = threadIdx.x >> 6;
+    float s = 0.0f;
+    for (int r = lane; r < dense_sum_ranges(b.M); r += 4) s += t.part[(size_t)r * t.C + c];
+    lds[threadIdx.x] = s;
+    __syncthreads();
+    if (lane) return;
+    put((T *)t.out + c, (lds[in] + lds[64 + in]) + (lds[128 + in] + lds[192 + in]));
+}
+
 // Rows copied, and rows zeroed after them, by block `block` of TAIL_BLOCKS.
 constexpr int TAIL_BLOCKS = 8;
 __device__ __forceinline__ void copy_tail(const DenseTails::Item &t, int block) {

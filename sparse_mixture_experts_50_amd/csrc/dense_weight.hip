@@ -9,6 +9,7 @@
 // of 4096 x 14336 in one launch 1049 us, also 1.37 (busy 67 % at 1.88 GHz).
 // Tails of zeros instead of masks: with a mask on the rows the loads could not
 // go straight to LDS.
+#include "dense_parts.h"
 #include "dense_tile.h"
 
 namespace {
@@ -19,13 +20,17 @@ struct WeightTile {
     int k, mi, ni, split;
 };
 
+template <bool SMALL>
+using WeightTiles = mt::Tiles<SMALL ? 128 : 256, SMALL ? 128 : 256, 2, 2, 1, true, true, true>;
+
+// The tiles of one block.  scr: 128 TN vectors, large tiles that leave no
+// plane.
 template <bool SMALL, bool PLANE>
-__global__ __launch_bounds__(256, SMALL ? 2 : 1) void dense_weight(DenseWeights p) {
+__device__ __forceinline__ void weight_work(const DenseWeights &p, int block, int blocks,
+                                            u32x4 *slot0, u32x4 *slot1, u32x4 *scr) {
     constexpr int B = SMALL ? 128 : 256;
-    typedef mt::Tiles<B, B, 2, 2, 1, true, true, true> P;
+    typedef WeightTiles<SMALL> P;
     constexpr int TN = P::TN, RB = B / 32;
-    constexpr bool TURN = !SMALL && !PLANE;
-    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], scr[TURN ? 4 * 32 * TN : 1];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / 2, wn = wave % 2;
     const int stages = (p.M + mt::SK - 1) / mt::SK;
@@ -63,7 +68,7 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void dense_weight(DenseWeights 
         ln.split = p.M / mt::SK;
         return ln;
     };
-    int L = mt::tile_of(0);
+    int L = dn::first_tile(block, blocks);
     if (L >= total) return;
     WeightTile t = tile_at(L);
     typename P::Source src = source(t);
@@ -71,9 +76,9 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void dense_weight(DenseWeights 
     P::load_stage(src, ln, 0, slot0, wave);
     P::load_stage(src, ln, 1, slot1, wave);
     mt::wait_loads<0>();
-    for (int r = 1;; ++r) {
+    for (;;) {
         const int lane = mt::tile_lane();
-        L = mt::tile_of(r);
+        L += blocks;
         const bool more = L < total;
         const WeightTile tn = more ? tile_at(L) : t;
         const typename P::Source next = source(tn);
@@ -129,24 +134,49 @@ __global__ __launch_bounds__(256, SMALL ? 2 : 1) void dense_weight(DenseWeights 
     __builtin_amdgcn_s_waitcnt(0);
 }
 
-template <bool SMALL, bool PLANE> void launch(const DenseWeights &p, hipStream_t s) {
-    constexpr int B = SMALL ? 128 : 256;
+template <bool PLANE>
+__global__ __launch_bounds__(256, 1) void dense_weight(DenseWeights p) {
+    typedef WeightTiles<false> P;
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE], scr[PLANE ? 1 : 128 * P::TN];
+    weight_work<false, PLANE>(p, blockIdx.x, gridDim.x, slot0, slot1, scr);
+}
+
+// The first `tiles` blocks; the others join.
+template <bool PLANE>
+__global__ __launch_bounds__(256, 2) void dense_weight_joins(DenseWeights p, DenseRows dx,
+                                                             DenseSums b, int tiles, int rows) {
+    typedef WeightTiles<true> P;
+    __shared__ u32x4 slot0[P::STAGE], slot1[P::STAGE];
+    const int block = blockIdx.x;
+    if (block < tiles)
+        weight_work<true, PLANE>(p, block, tiles, slot0, slot1, nullptr);
+    else
+        dense_parts::join<bf16>(dx, p, b, block - tiles, rows, 0, (float *)slot0);
+}
+
+int blocks_of(const DenseWeights &p, int B, int per_cu) {
     long long tiles = 0;
     for (int k = 0; k < p.count; ++k)
         tiles += (long long)((p.m[k].R + B - 1) / B) * ((p.m[k].C + B - 1) / B) * p.splits;
-    hipLaunchKernelGGL((dense_weight<SMALL, PLANE>), dim3(mt::grid_for(tiles, SMALL ? 2 : 1)),
-                       dim3(256), 0, s, p);
+    return mt::grid_for(tiles, per_cu);
 }
 
 }  // namespace
 
 hipError_t launch_dense_weights_mfma(const DenseWeights &p, hipStream_t s) {
-    if (p.small) {
-        if (p.splits > 1) launch<true, true>(p, s);
-        else launch<true, false>(p, s);
-    } else {
-        if (p.splits > 1) launch<false, true>(p, s);
-        else launch<false, false>(p, s);
-    }
+    const dim3 grid(blocks_of(p, 256, 1));
+    if (p.splits > 1) hipLaunchKernelGGL(dense_weight<true>, grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL(dense_weight<false>, grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_dense_weights_joins(const DenseWeights &p, const DenseRows &dx,
+                                      const DenseSums &b, int rows, int sums, hipStream_t s) {
+    const int tiles = blocks_of(p, 128, 2);
+    const dim3 grid(tiles + rows + sums);
+    if (p.splits > 1)
+        hipLaunchKernelGGL(dense_weight_joins<true>, grid, dim3(256), 0, s, p, dx, b, tiles, rows);
+    else
+        hipLaunchKernelGGL(dense_weight_joins<false>, grid, dim3(256), 0, s, p, dx, b, tiles, rows);
     return hipGetLastError();
 }
