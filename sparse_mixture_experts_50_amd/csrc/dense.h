@@ -17,7 +17,8 @@ enum DenseEpilogue {
 };
 
 // How a product is cut: tiles of 32 * rb rows (small: 64) by 256 (small: 128)
-// columns, K in `splits` ranges of `per` stages.  stream: the kernel for few
+// columns (fp32: 128 by 128, small: 64 by 64), which two panels share, and K in
+// `splits` ranges of `per` stages.  stream: the kernel for few
 // rows, which cuts by itself.  The last nt2 columns of tiles may be lower ones
 // (rb2, mt2 of them a column), which come after the others.
 struct DensePlan {

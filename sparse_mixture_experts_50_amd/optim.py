@@ -142,6 +142,7 @@ class AdamW:
         if norm is not None:
             _need(norm, "norm", (1,), torch.float32, self.device)
         device, words, k = self.device, self._words, 0
+        index = device.index
         for g, (p, shape, at, n, types) in zip(grads, self._of):
             if g is None:
                 words[k + 7] = 0
@@ -151,7 +152,7 @@ class AdamW:
             if word is None:
                 raise ValueError(f"gradient {k // 10}: unsupported dtype "
                                  f"{g.dtype}")
-            if g.shape != shape or g.device != device or \
+            if g.get_device() != index or g.shape != shape or \
                     not g.is_contiguous():
                 _need(g, f"gradient {k // 10}", shape, g.dtype, device)
             if p.data_ptr() != at:
