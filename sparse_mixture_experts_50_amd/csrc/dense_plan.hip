@@ -68,16 +68,11 @@ int split_blocks(int M) {
     return rb <= 4 ? 4 : rb <= 6 ? 6 : rb;
 }
 
-}  // namespace
-
-DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, bool two) {
+// The best tiles, and their time.
+DensePlan tiles_plan(int dtype, int M, int N, int K, int panels, bool two, double &us) {
     DensePlan p = {};
     p.rb = 2;
     p.splits = 1;
-    if (M <= 64 && !bk) {
-        p.stream = true;
-        return p;
-    }
     const int stages = K / 64;
     const double elements = (double)M * N * panels;
     if (dtype != 1) {
@@ -89,7 +84,7 @@ DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, b
         // ranges 25)
         const int n = two ? 2 : 1;
         const Cost c = {4, {1.5 * n, 2.05 * n, 3.2 * n, 3.85 * n}, 2.0};
-        double us = 0, big = 0;
+        double big = 0;
         p.splits = best_splits(stages, 16, false, us, p.per, [&](int s, int len) {
             return product_us(c, (long long)p.mt * p.nt * s, len) + plane_us(elements, s);
         });
@@ -104,7 +99,10 @@ DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, b
             return product_us(l, (long long)b.mt * b.nt * s, len) + plane_us(elements, s);
         });
         // (as good: the small ones share launches)
-        if (big < 0.98 * us) return b;
+        if (big < 0.98 * us) {
+            us = big;
+            return b;
+        }
         return p;
     }
     const int all = two ? 2 * stages : stages;
@@ -113,7 +111,6 @@ DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, b
     a.small = true;
     a.mt = ceil_div(M, 64);
     a.nt = ceil_div(N, 128 / panels);
-    double us = 0;
     {
         // (512 x 4096 x 4096: 256 tiles 25 us; 1024 x 4096 x 4096: 512 41;
         // 2048 x 8192 x 1024: 2048 45)
@@ -160,7 +157,38 @@ DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, b
             }
         }
     }
+    us = big;
     return b;
+}
+
+// The kernel for few rows: a block's runs of 16 columns, its rows of x and of
+// the weights at 90 GB/s and its MFMAs, or all weights at the memory's rate.
+double stream_us(int dtype, int M, int N, int K, int panels) {
+    const int units = N / 16, per = ceil_div(units, 512), rows = ceil_div(M, 16);
+    const double es = dtype == 1 ? 2 : 4, products = (double)rows * panels * K;
+    const double block = per * ((rows + panels) * 16 * K * es / 90e3 +
+                                products * (dtype == 1 ? 1 / 128.0 * 16 : 1 / 16.0 * 32) / 2400);
+    const double all = N * es * panels * K / 5.2e6;
+    return 3.0 + (block > all ? block : all);
+}
+
+}  // namespace
+
+DensePlan dense_rows_plan(int dtype, int M, int N, int K, int panels, bool bk, bool two) {
+    double us = 0;
+    const DensePlan p = tiles_plan(dtype, M, N, K, panels, two, us);
+    if (bk || M > 64) return p;
+    // few columns leave most CUs without a block, where tiles have ranges of K
+    // (45 x 128 x 8000, bf16: 17 us, in ranges 10; 64 x 4096 x 14336 37 and 31;
+    // 64 x 1024 x 8192, fp32: 60 and 20)
+    const double stream = stream_us(dtype, M, N, K, panels);
+    const double all = 3.0 + (double)N * panels * K * (dtype == 1 ? 2 : 4) / 4.5e6;
+    if ((us > all ? us : all) < stream) return p;
+    DensePlan s = {};
+    s.stream = true;
+    s.rb = 2;
+    s.splits = 1;
+    return s;
 }
 
 size_t dense_weights_plan(DenseWeights &p, int dtype) {

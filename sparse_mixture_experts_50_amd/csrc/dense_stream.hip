@@ -1,5 +1,5 @@
-// Linear layers of few rows (M <= 64), both types: the weights are streamed
-// once from memory.
+// Linear layers of few rows (M <= 64) and enough columns to give most CUs a
+// block, both types: the weights are streamed once from memory.
 //
 // A block takes 16 columns (of each panel) at a time and all rows; its four
 // waves split K.  Both operands pass through LDS: a stage is 16 rows by 1 KB

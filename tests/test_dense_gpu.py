@@ -96,9 +96,16 @@ LARGE = [("bf16", *c) for c in [
         (65, 4224, 2560, "swiglu"), (67, 6400, 2240, "geglu")]]
 
 
+# few rows of few columns, in ranges of K
+FEW = [(t, *c) for t in ("bf16", "f32") for c in [
+    (6, 64, 6976, "geglu"), (48, 64, 6976, "swiglu"), (1, 64, 19968, "gelu"),
+    (45, 128, 8000, "silu"), (64, 64, 16384, "none"),
+    (64, 1024, 8192, "none"), (45, 2048, 4096, "swiglu")]]
+
+
 @pytest.mark.parametrize("dtype,M,N,K,act",
                          [(t, *c) for c in LINEAR for t in ("bf16", "f32")] +
-                         LARGE)
+                         LARGE + FEW)
 def test_linear(dtype, M, N, K, act):
     half = ref.HALF[DT[dtype]]
     for bias, res in ((False, False), (True, True)):
@@ -152,7 +159,7 @@ LARGE_GRAD = [("bf16", *c) for c in [
 
 @pytest.mark.parametrize("dtype,M,N,K,act",
                          [(t, *c) for c in LINEAR_GRAD
-                          for t in ("bf16", "f32")] + LARGE_GRAD)
+                          for t in ("bf16", "f32")] + LARGE_GRAD + FEW)
 def test_linear_grad(dtype, M, N, K, act):
     half = ref.HALF[DT[dtype]]
     rounds = 1 if act == "none" else 2
