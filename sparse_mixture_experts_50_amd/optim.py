@@ -34,7 +34,7 @@ class AdamW:
     which are the same for the same seed and step.
     ``device_steps``: count steps on the GPU, as a step that is captured into
     a graph needs.  ``lr_scale``: float32 [1] on the GPU that multiplies
-    ``lr`` (a schedule that a graph's replays see).
+    ``lr`` (a schedule that a graph's replays see), or None.
 
     The states are the lists ``m`` and ``v`` (float32, or float8_e4m3fn with
     ``m_scale`` and ``v_scale``: uint8 exponents + 127, one per block) and
@@ -210,6 +210,8 @@ class AdamW:
             self._captured = True
         if norm is not None:
             _need(norm, "norm", (1,), torch.float32, self.device)
+        if self.lr_scale is not None:
+            _need(self.lr_scale, "lr_scale", (1,), torch.float32, self.device)
         self._check_places()
         device = self.device
         try:                         # (20 tensors: 1 us less than the loop)

@@ -130,6 +130,22 @@ def test_states_of_a_captured_step_stay(calls, monkeypatch):
     assert len(calls) == 2
 
 
+def test_a_replaced_schedule_is_checked(calls):
+    """As the one that is given at first is: its address goes to the GPU."""
+    opt = moe.AdamW([torch.zeros(40)], lr=1.0, lr_scale=torch.ones(1))
+    for bad in (torch.ones(1, dtype=torch.float64), torch.ones(2), 0.5,
+                torch.ones(1, device="meta"), torch.ones(())):
+        opt.lr_scale = bad
+        with pytest.raises((ValueError, AttributeError)):
+            opt.step([torch.zeros(40)])
+    assert not calls and opt.steps == 0
+    opt.lr_scale = torch.ones(1)
+    opt.step([torch.zeros(40)])
+    opt.lr_scale = None
+    opt.step([torch.zeros(40)])
+    assert len(calls) == 2
+
+
 def test_changing_types_and_missing_gradients(calls):
     opt, grads = optimizer(32)
     opt.step(grads)
