@@ -607,7 +607,10 @@ typedef struct moe_adamw {
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   x = x - (lr weight_decay x
  *            + lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps))
- * in fp32, from m and v before they are rounded to 8 bits.  A block of 8-bit
+ * in fp32, from m and v before they are rounded to 8 bits.  That rounding is
+ * right in the mean for m and sqrt(v), so v gains its variance: 2 to 5 % in a
+ * long run with normal gradients, 2/7 at most (but for values under 2^-28 of
+ * their block's largest).  A block of 8-bit
  * states with a value that is not finite becomes not-a-number throughout.
  * Needs 0 <= beta1, beta2 < 1, eps >= 2^-126, lr and weight_decay >= 0, all
  * below 1e30.

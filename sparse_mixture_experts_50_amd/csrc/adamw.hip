@@ -10,10 +10,17 @@
 // under which the block's largest magnitude is at most 448, and hold e4m3
 // codes: a power of two costs no rounding of its own.  v is held as its root,
 // which has m's range: v itself would need twice the exponents.  Codes are
-// rounded at random, with probabilities that make the mean right: a step of
-// e4m3 is 2^-3 of the value, and rounding to nearest would throw away every
-// change of less than half of it, as (1 - b2) g^2 nearly always is.  A root
-// that is not 0 never becomes 0 (m / eps would be what follows).  The update
+// rounded at random, with probabilities that make the mean of m and of the
+// root right in each step: a step of e4m3 is 2^-3 of the value, and rounding
+// to nearest would throw away every change of less than half of it, as (1 - b2)
+// g^2 nearly always is.  A root that is not 0 never becomes 0 (m / eps would be
+// what follows).  v, the root's square, gains the rounding's variance: of a
+// root u that comes from a code c, with steps of s <= u / 8, at most |u - c| s
+// <= (1 - b2) |g^2 - c^2| / 8, and half of that where u is near c.  So a long
+// run ends with E c^2 - E g^2 <= (E g^2 + E c^2) / 8, or 2/7 over the 32-bit v
+// at most; with normal gradients it is 2 % (b2 = 0.95) to 5 % (0.999), and
+// updates are 1 to 2.5 % smaller.  (Codes under 2^-6, of roots under 2^-14 of
+// their block's largest, have longer steps.)  The update
 // itself uses m and v before they are rounded.  The random bits are a hash of
 // seed, step, tensor and element, so the same call gives the same bits.
 // bf16 parameters without a master copy can be rounded in the same way: lr

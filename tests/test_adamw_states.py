@@ -159,6 +159,37 @@ def test_changing_types_and_missing_gradients(calls):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("b2,steps", [(0.999, 4000), (0.95, 400)])
+def test_second_moments_of_a_long_run(b2, steps):
+    """8-bit second moments beside 32-bit ones of the same gradients.  The
+    root's rounding is right in the mean, so v gains its variance.  With a = 1
+    - b2, a code c and the root u^2 = b2 c^2 + a g^2 the variance is at most
+    |u - c| s, s <= u / 8 the step, and |u - c| = a |g^2 - c^2| / (u + c):
+    E c^2 <= E g^2 (1 + f / 8) / (1 - f / 8) with f = u / (u + c), and never
+    less than E g^2.  f: |g| <= 6 c of 65536 values, u <= c sqrt(b2 + 36 a).
+    The mean over the values is off by its sampling: a code is off by half a
+    step or so, v by 2 / 16 of itself; six standard deviations."""
+    n, g = 1 << 16, torch.Generator(device="cuda").manual_seed(9)
+    # every place between two powers of two
+    std = torch.exp2(torch.arange(n, device="cuda") // 32 / (n / 32))
+    grad = torch.zeros(n, device="cuda")
+    opts = [moe.AdamW([torch.zeros(n, device="cuda")], lr=0.0, betas=(0.9, b2),
+                      state_bits=bits, seed=2) for bits in (32, 8)]
+    for _ in range(steps):
+        grad.normal_(generator=g).mul_(std)
+        for opt in opts:
+            opt.step([grad])
+    full, codes = opts
+    unit = torch.exp2(codes.v_scale[0].double() - 127).repeat_interleave(32)
+    v = (codes.v[0].double() * unit) ** 2
+    ratio = float((v / std ** 2).sum() / (full.v[0].double() / std ** 2).sum())
+    far = (b2 + 36 * (1 - b2)) ** 0.5
+    f = far / (1 + far)
+    noise = 6 * 0.125 / n ** 0.5
+    assert 1 - noise <= ratio <= (1 + f / 8) / (1 - f / 8) + noise, ratio
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("bits", [32, 8])
 def test_a_loaded_checkpoint(bits):
     """States put in others' place, and states copied into them: the same
