@@ -8,7 +8,10 @@
 // first in each range of K and stay in registers while the weights' follow.
 // The waves' sums are added in order before the epilogue.  (fp32: the four k
 // of a lane go to four MFMAs; which k an MFMA adds up does not matter as long
-// as both operands agree.)  Rows past M re-read the last.
+// as both operands agree.)  Rows past M re-read the last.  A wave's quarter of
+// K is one chain of fp32 sums: f32, 4096 deep, off by 5.7e-7 of the norm, 16384
+// deep by 1.1e-6, where tiles that join a total every 64 terms are off by 1.7e-7
+// and 1.8e-7.
 //
 // Bound by HBM, from 32 rows on by what x adds to the loads (MB stages for
 // every P of weights, from L2).  Fragments straight from memory, 16 rows by 64
