@@ -22,7 +22,10 @@
 // updates are 1 to 2.5 % smaller.  (Codes under 2^-6, of roots under 2^-14 of
 // their block's largest, have longer steps.)  The update
 // itself uses m and v before they are rounded.  The random bits are a hash of
-// seed, step, tensor and element, so the same call gives the same bits.
+// seed, step, tensor and element, so the same call gives the same bits: its
+// mixing steps are published ones of low bias (C. Wellons, "Prospecting for
+// Hash Functions", 2018), the multipliers that make its key are primes of Y.
+// Collet's published xxHash specification.
 // bf16 parameters without a master copy can be rounded in the same way: lr
 // is far below 2^-9 of a parameter, and nearest rounding keeps small updates
 // out.
