@@ -331,8 +331,9 @@ template <int EPI> hipError_t by_act(const DenseRows &p, hipStream_t s) {
     case ACT_SILU: return launch<1, false, EPI, ACT_SILU>(p, s);
     case ACT_SWIGLU: return launch<2, false, EPI, ACT_SWIGLU>(p, s);
     case ACT_GEGLU: return launch<2, false, EPI, ACT_GEGLU>(p, s);
-    default: return launch<1, false, EPI, ACT_NONE>(p, s);
     }
+    // (a layer without an activation has no pre-activation's gradient)
+    return launch<1, false, DENSE_FORWARD, ACT_NONE>(p, s);
 }
 
 }  // namespace

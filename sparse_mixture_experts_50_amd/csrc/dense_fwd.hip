@@ -6,8 +6,8 @@ hipError_t launch_dense_forward_mfma(const DenseRows &p, hipStream_t s) {
     if (p.bk) return launch_dense_dx_mfma(p, s);
     if (p.panels() == 2) return launch_dense_gated_mfma(p, s);
     switch (p.act) {
-    case ACT_GELU: return launch_forward<1, false, false, ACT_GELU>(p, s);
-    case ACT_SILU: return launch_forward<1, false, false, ACT_SILU>(p, s);
-    default: return launch_forward<1, false, false, ACT_NONE>(p, s);
+    case ACT_GELU: return launch_forward<1, ACT_GELU>(p, s);
+    case ACT_SILU: return launch_forward<1, ACT_SILU>(p, s);
+    default: return launch_forward<1, ACT_NONE>(p, s);
     }
 }

@@ -4,6 +4,6 @@
 
 hipError_t launch_dense_gated_mfma(const DenseRows &p, hipStream_t s) {
     using namespace dn;
-    return p.act == ACT_SWIGLU ? launch_forward<2, false, false, ACT_SWIGLU>(p, s)
-                               : launch_forward<2, false, false, ACT_GEGLU>(p, s);
+    return p.act == ACT_SWIGLU ? launch_forward<2, ACT_SWIGLU>(p, s)
+                               : launch_forward<2, ACT_GEGLU>(p, s);
 }

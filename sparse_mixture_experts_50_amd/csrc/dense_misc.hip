@@ -94,7 +94,10 @@ template <typename T, int EPI> void finish_as(const DenseRows &p, hipStream_t s)
     case ACT_GEGLU:
         hipLaunchKernelGGL((dense_finish<T, EPI, ACT_GEGLU>), grid, block, 0, s, p);
         break;
-    default: hipLaunchKernelGGL((dense_finish<T, EPI, ACT_NONE>), grid, block, 0, s, p);
+    default:
+        // (a layer without an activation has no pre-activation's gradient)
+        if constexpr (EPI == DENSE_FORWARD)
+            hipLaunchKernelGGL((dense_finish<T, EPI, ACT_NONE>), grid, block, 0, s, p);
     }
 }
 

@@ -239,8 +239,9 @@ __global__ __launch_bounds__(256, 2) void dense_stream(DenseRows p) {
                 else finish<T, EPI, ACT_GEGLU>(p, z, v, at);
             } else {
                 if (p.act == ACT_GELU) finish<T, EPI, ACT_GELU>(p, z, v, at);
-                else if (p.act == ACT_SILU) finish<T, EPI, ACT_SILU>(p, z, v, at);
-                else finish<T, EPI, ACT_NONE>(p, z, v, at);
+                else if (EPI == DENSE_GRAD || p.act == ACT_SILU)
+                    finish<T, EPI, ACT_SILU>(p, z, v, at);
+                else finish<T, DENSE_FORWARD, ACT_NONE>(p, z, v, at);
             }
         }
     }

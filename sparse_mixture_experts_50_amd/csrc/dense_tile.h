@@ -371,6 +371,10 @@ hipError_t launch_as(const DenseRows &p, hipStream_t s) {
 // By the parity of a tile's stages, and the tiles' size.
 template <int PANELS, bool BK, bool TWO, int EPI, int ACT, bool RES>
 hipError_t launch_large(const DenseRows &p, hipStream_t s) {
+    // planes of ranges of K, which are even and of one height (all of K in one
+    // plane: the gradient of h alone)
+    if constexpr (EPI == DENSE_PLANE && (TWO || !BK))
+        return launch_as<PANELS, BK, TWO, EPI, ACT, RES, mt::EVEN, false>(p, s);
     auto launch = [&](auto kind) {
         constexpr mt::Stages KIND = decltype(kind)::value;
         return p.plan.nt2 ? launch_as<PANELS, BK, TWO, EPI, ACT, RES, KIND, false, true>(p, s)
@@ -387,10 +391,9 @@ hipError_t launch_by_plan(const DenseRows &p, hipStream_t s) {
 }
 
 // The forward's epilogue, with or without a residual.
-template <int PANELS, bool BK, bool TWO, int ACT>
-hipError_t launch_forward(const DenseRows &p, hipStream_t s) {
-    return p.res ? launch_by_plan<PANELS, BK, TWO, DENSE_FORWARD, ACT, true>(p, s)
-                 : launch_by_plan<PANELS, BK, TWO, DENSE_FORWARD, ACT, false>(p, s);
+template <int PANELS, int ACT> hipError_t launch_forward(const DenseRows &p, hipStream_t s) {
+    return p.res ? launch_by_plan<PANELS, false, false, DENSE_FORWARD, ACT, true>(p, s)
+                 : launch_by_plan<PANELS, false, false, DENSE_FORWARD, ACT, false>(p, s);
 }
 
 }  // namespace dn
