@@ -38,7 +38,7 @@
 // enough for a cache (non-temporal), and eight waves a SIMD hide what stands
 // between a load and its store.  0.18 G bf16 elements with master copies (28
 // bytes each) 0.99 ms, 5.1 TB/s; 0.58 G with 8-bit states (10.1 bytes) 1.25 ms,
-// 4.7 TB/s, with four waves 1.47, by way of the caches 1.32, with the codes'
+// 4.7 TB/s (by the card 1.24 to 1.30), with four waves 1.47, by way of the caches 1.32, with the codes'
 // rounding by integer steps instead of the conversion's 0.04 more.  Chunks of
 // 16384 elements of all tensors (fewer where that leaves blocks without work)
 // are dealt round-robin to the blocks, as the clipping's are.

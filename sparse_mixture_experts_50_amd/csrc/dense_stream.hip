@@ -17,10 +17,10 @@
 // every P of weights, from L2).  Fragments straight from memory, 16 rows by 64
 // bytes an instruction, end at 12 bytes a clock and CU, however many are in
 // flight: 32 rows, 4096 to 14336 features, gated (235 MB of weights) 78 us,
-// through the ring 43 (5.5 TB/s); 14336 to 4096 (117 MB) 46 and 32; one row,
-// 41 and 25.  Two or four groups of 16 columns a unit: 46 and 42 us of the
-// first, 39 and 52 of the second; six to nine slots, one block a CU: 46 to 48,
-// and 32 to 34.
+// through the ring 43 (5.5 TB/s; the median of 40 calls 45); 14336 to 4096
+// (117 MB) 46 and 32; one row, 41 and 25.  Two or four groups of 16 columns a
+// unit: 46 and 42 us of the first, 39 and 52 of the second; six to nine slots,
+// one block a CU: 46 to 48, and 32 to 34.
 #include <type_traits>
 #include <utility>
 

@@ -10,11 +10,13 @@
 // tiles, no store is a branch.
 //
 // Bound by the matrix cores, and in long products by the power that they draw:
-// 4096 x 4096 to 14336 gated 653 us, 1.47 PFLOP/s, cores busy 75 % at 1.71 GHz;
-// the same with the gradient's epilogue 721.  Short K: 8192 x 2048 to 7168 with
-// a residual 213 to 218, 1.1 PFLOP/s: while a tile's epilogue reads and writes 128 KB
-// its matrix cores wait.  Tiles of one height, 896 of them or 3.5 rounds of the
-// CUs: 227.  The first of the residual fetched ahead of the product: 1 % more.
+// 4096 x 4096 to 14336 gated 700 to 720 us (best of 40 calls 653 to 689, by the
+// card), 1.34 to 1.37 PFLOP/s, cores busy 75 % at 1.71 GHz; the same with the
+// gradient's epilogue 750 to 770.  Short K: 8192 x 2048 to 7168 with a residual
+// 213 to 223, 1.1 PFLOP/s: while a tile's epilogue reads and writes 128 KB its
+// matrix cores wait.  Tiles of one height, 896 of them or 3.5 rounds of the CUs:
+// 227 where two took 218.  The first of the residual fetched ahead of the
+// product: 1 % more.
 #pragma once
 
 #include "act.h"

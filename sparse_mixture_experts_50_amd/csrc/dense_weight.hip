@@ -5,8 +5,9 @@
 // buffer of 64 rows that is zero from M on, as a second product.
 // Few tiles: the rows go in ranges, each to an fp32 plane of its own.
 //
-// Bound by the matrix cores: 4096 rows, 4096 x 4096 100 us, 1.37 PFLOP/s; three
-// of 4096 x 14336 in one launch 1049 us, also 1.37 (busy 67 % at 1.88 GHz).
+// Bound by the matrix cores: 4096 rows, 4096 x 4096 106 us in long runs, 1.30
+// PFLOP/s (best call 100, in runs of 40 calls 120); three of 4096 x 14336 in one
+// launch 1095 to 1120 us, 1.3 (busy 67 % at 1.86 GHz).
 // Tails of zeros instead of masks: with a mask on the rows the loads could not
 // go straight to LDS.
 #include "dense_parts.h"
