@@ -109,6 +109,7 @@ class AdamW:
         self._grad_words, self._type_words = words[1::10], words[9::10]
         self._types = None           # of the gradients in the list
         self._captured = False       # whether a graph holds the addresses
+        self._memory = []
         self._shapes = [p.shape for p in self.params]
         for e, p, decay in zip(self._list, self.params, self.weight_decay):
             e.param, e.weight_decay = p.data_ptr(), decay
@@ -132,7 +133,8 @@ class AdamW:
 
     def _hold(self):
         """Takes over the states' addresses.  They are held under other names
-        too: while these live, no other memory gets one of the addresses."""
+        too: while these live, no other memory gets one of the addresses.
+        What was replaced is given back once the steps behind are done."""
         for name, want in self._states.items():
             own = getattr(self, name)
             if len(own) != len(want):
@@ -148,6 +150,9 @@ class AdamW:
         for name in self._states:
             for e, t in zip(self._list, getattr(self, name)):
                 setattr(e, name, None if t is None else t.data_ptr())
+        for t in self._memory:
+            if t.is_cuda:
+                t.record_stream(torch.cuda.current_stream(t.device))
         self._places, self._memory = places, [t.detach() for t in self._all()]
 
     def _check_places(self):

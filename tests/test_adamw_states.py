@@ -190,6 +190,30 @@ def test_second_moments_of_a_long_run(b2, steps):
 
 
 @pytest.mark.gpu
+def test_a_replaced_state_outlives_the_steps_that_use_it():
+    """Steps on a stream of their own: the memory of a state that was replaced
+    is not another tensor's on the stream that it came from while they run."""
+    n, side = 1 << 26, torch.cuda.Stream()
+    p, grad = (torch.zeros(n, device="cuda") for _ in range(2))
+    opt = moe.AdamW([p], lr=0.0)
+    torch.cuda.synchronize()
+    at = opt.m[0].data_ptr()
+    done = torch.cuda.Event()
+    with torch.cuda.stream(side):
+        for _ in range(300):                 # (of 0.35 ms each)
+            opt.step([grad])
+        done.record()
+        opt.m[0] = torch.zeros(n, device="cuda")
+        opt.step([grad])
+    # (not touched)
+    other = [torch.empty(n, device="cuda") for _ in range(2)]
+    places = {t.data_ptr() for t in other}
+    running = not done.query()               # still, after the allocations
+    assert at not in places or not running
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("bits", [32, 8])
 def test_a_loaded_checkpoint(bits):
     """States put in others' place, and states copied into them: the same
