@@ -210,15 +210,15 @@ class AdamW:
         1e-6)) on the way."""
         if len(grads) != len(self.params):
             raise ValueError("as many gradients as there are parameters")
-        if _capturing(self.device):
-            if self._dev_steps is None:
-                raise ValueError("a captured step needs device_steps=True")
-            self._captured = True
+        capturing = _capturing(self.device)
+        if capturing and self._dev_steps is None:
+            raise ValueError("a captured step needs device_steps=True")
         if norm is not None:
             _need(norm, "norm", (1,), torch.float32, self.device)
         if self.lr_scale is not None:
             _need(self.lr_scale, "lr_scale", (1,), torch.float32, self.device)
         self._check_places()
+        self._captured = self._captured or capturing
         device = self.device
         try:                         # (20 tensors: 1 us less than the loop)
             right = (list(map(_shape, grads)) == self._shapes and

@@ -119,7 +119,10 @@ def test_states_of_a_captured_step_stay(calls, monkeypatch):
     and their memory is not given back."""
     opt = moe.AdamW([torch.zeros(40)], lr=1.0, device_steps=True)
     monkeypatch.setattr(optim_module, "_capturing", lambda device: True)
+    # (replaced before the capture: what is captured)
+    opt.v[0] = torch.zeros(40)
     opt.step([torch.zeros(40)])
+    assert calls[0][0]["v"] == opt.v[0].data_ptr()
     monkeypatch.setattr(optim_module, "_capturing", lambda device: False)
     opt.step([torch.zeros(40)])
     at = opt.m[0].data_ptr()
